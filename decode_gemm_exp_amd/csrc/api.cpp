@@ -21,6 +21,12 @@
 
 using namespace uw;
 
+namespace {
+void pal_words(const Tables& t, PalView* out);
+}
+
+void uw::palette_view(const uw_matrix* m, PalView* out) { pal_words(m->t, out); }
+
 int uw::device_cus() {
   static int cached[64] = {0};
   int dev = 0;

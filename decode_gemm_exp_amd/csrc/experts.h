@@ -1,0 +1,212 @@
+// experts.h -- shared declarations of the mixture-of-experts and MXFP4
+// operators: the experts' weights as the kernels see them, the search of a
+// block's share of ragged rows, MXFP4 unpacking, and the launchers.
+#pragma once
+
+#include "rebuild.h"
+
+namespace uw {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopk = 16;
+
+// Weight forms of the expert products, a template argument of the kernels.
+// kFormPal serves UWF1 matrices whose palettes differ in kind (one of them
+// not a run of consecutive exponents), kFormPalRun those that all are runs.
+enum ExpertForm { kFormBf16 = 0, kFormPal = 2, kFormPalRun = 3, kFormMx4 = 4 };
+constexpr bool form_is_pal(int f) { return f == kFormPal || f == kFormPalRun; }
+
+// One UWF1 expert (device table).
+struct ExpertEntry {
+  const uint8_t* sm;
+  const uint8_t* pidx;
+  const uint32_t* vflags;
+  const uint32_t* vrank;
+  const uint8_t* vexp;
+  uint64_t vexp_bytes;
+  PalView pal;
+};
+
+// All experts of one projection: expert e's W_e[N][K].
+struct ExpertsView {
+  int form;
+  int count;
+  int64_t n, k;
+  const uint8_t* w;        // BF16 rows or packed MXFP4 elements of expert 0
+  const uint8_t* scale;    // MXFP4: scales of expert 0, mx4_scale_stride(k) bytes a row
+  int64_t w_stride;        // bytes from one expert's weights to the next
+  int64_t scale_stride;
+  const ExpertEntry* table;   // UWF1
+};
+
+__host__ __device__ constexpr int64_t mx4_scale_stride(int64_t k) { return (k + 127) / 128 * 4; }
+
+// Ragged rows: expert e's are slots [offsets[e], offsets[e + 1]); slot s
+// multiplies row rows[s] of x, or row s when rows is NULL.  offsets NULL: one
+// expert with all `slots` rows.
+struct RaggedRows {
+  const int32_t* offsets;
+  const int32_t* rows;
+  int64_t slots;      // capacity: offsets are clamped to it
+  int64_t x_rows;     // rows of x; a row index outside selects a row of zeros
+};
+
+// A block's share: `count` slots from `first`, all of expert `expert`;
+// count 0: nothing to do.
+struct Share {
+  int expert;
+  int64_t first;
+  int count;
+};
+
+// Chunk `j` of the experts' slots cut into chunks of at most `chunk`: expert
+// e has ceil(rows_e / chunk).  Every wave searches by itself, without a
+// barrier: a lane holds four consecutive experts, one wave-wide prefix sum
+// per 256 experts.  Offsets are clamped to [0, slots] and to their
+// predecessor, so no content of the array leads outside the slots.
+__device__ __forceinline__ Share find_share(const RaggedRows& r, int experts, int64_t j, int chunk) {
+  Share out{0, 0, 0};
+  if (!r.offsets) {
+    const int64_t first = j * chunk;
+    if (first < r.slots) {
+      out.first = first;
+      out.count = (int)(r.slots - first < chunk ? r.slots - first : chunk);
+    }
+    return out;
+  }
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;   // chunks of the experts before this round's
+  for (int e0 = 0; e0 < experts; e0 += 256) {
+    int32_t o[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int e = e0 + 4 * lane + i;
+      const int32_t v = r.offsets[e < experts ? e : experts];
+      o[i] = v < 0 ? 0 : (int64_t)v < r.slots ? v : (int32_t)r.slots;
+    }
+    int c[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = o[i + 1] > o[i] ? (int)(((int64_t)o[i + 1] - o[i] + chunk - 1) / chunk) : 0;
+      mine += c[i];
+    }
+    int sum = mine;   // inclusive prefix over lanes
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d);
+      sum += lane >= d ? up : 0;
+    }
+    const int64_t lo = before + sum - mine;
+    const uint64_t hit = __ballot(j >= lo && j < lo + mine);
+    if (hit) {
+      int at = (int)(j - lo), e = 0;
+      int32_t b = o[0], n = o[1];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const bool go = e == i && at >= c[i];
+        at -= go ? c[i] : 0;
+        e = go ? i + 1 : e;
+        b = go ? o[i + 1] : b;
+        n = go ? o[i + 2] : n;
+      }
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      out.expert = __builtin_amdgcn_readlane(e0 + 4 * lane + e, src);
+      const int32_t begin = __builtin_amdgcn_readlane(b, src), end = __builtin_amdgcn_readlane(n, src);
+      out.first = (int64_t)begin + (int64_t)__builtin_amdgcn_readlane(at, src) * chunk;
+      out.count = (int)(end - out.first < chunk ? end - out.first : chunk);
+      return out;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return out;
+}
+
+// Chunks that slots rows over `experts` experts can make at most: every
+// expert with rows adds less than one chunk beyond its share.
+inline int64_t max_chunks(int64_t slots, int experts, int chunk, bool ragged) {
+  if (!ragged) return (slots + chunk - 1) / chunk;
+  const int64_t with_rows = slots < experts ? slots : experts;
+  const int64_t c = slots / chunk + with_rows;
+  return c < slots ? c : slots;
+}
+
+// ---- MXFP4 --------------------------------------------------------------------
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
+typedef __attribute__((ext_vector_type(4))) float f32x4_t;
+
+// an E8M0 scale as the float whose exponent field it is (byte 0: the field of
+// 2^-127, which the scaled conversions read as such)
+__device__ __forceinline__ float e8m0_float(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
+
+// 8 elements (one dword) times their block's scale -> 8 BF16, exact unless
+// the product overflows BF16 (scale bytes 253 and up)
+__device__ __forceinline__ uint4 mx4_unpack8(uint32_t q, float scale) {
+  uint4 o;
+  o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0));
+  o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1));
+  o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2));
+  o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3));
+  return o;
+}
+
+// float -> BF16, to nearest even (NaN stays NaN)
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  typedef __attribute__((ext_vector_type(2))) float f2;
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf16x2_t));
+}
+
+// g / (1 + exp(-g)): exp(-g) overflows to infinity for g below -88.7, where
+// the quotient is -0, as it should round
+__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+
+// ---- launchers ----------------------------------------------------------------
+// y (fp32, mode 0) or h = silu(W x) * (U x) (BF16, mode 1; u the second
+// projection) over ragged rows
+struct ExpertsCall {
+  ExpertsView w, u;
+  bool gated;
+  RaggedRows r;
+  const uint16_t* x;
+  void* y;
+};
+hipError_t launch_experts(const ExpertsCall& c, hipStream_t s);
+hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s);
+
+hipError_t launch_quantize_mx4(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* elem,
+                               uint8_t* scale, hipStream_t s);
+hipError_t launch_dequantize_mx4(const uint8_t* elem, const uint8_t* scale, int64_t rows, int64_t cols, uint16_t* out,
+                                 int64_t ld, hipStream_t s);
+// x -> the BF16 values its MXFP4 form stands for
+hipError_t launch_round_mx4(const uint16_t* x, int64_t rows, int64_t cols, uint16_t* out, hipStream_t s);
+
+struct RouteCall {
+  const void* logits;   // NULL: ids are given
+  bool bf16;
+  int64_t tokens, ld;
+  int experts, topk, scoring;
+  const float* bias;
+  int32_t* ids;
+  const int32_t* ids_in;
+  float* weights;
+  int32_t *offsets, *rows, *slots;
+  int32_t* hist;        // [blocks][experts], unless one block does it all
+};
+int route_blocks(int64_t tokens, int topk);   // 1: no workspace
+hipError_t launch_route(const RouteCall& c, hipStream_t s);
+
+// out[t] = sum over j of weights[t][j] d[slots[t][j]], in the order of j
+hipError_t launch_combine(const float* d, const int32_t* slots, const float* weights, int64_t tokens, int topk,
+                          int64_t n, int64_t d_rows, uint16_t* out, hipStream_t s);
+
+}  // namespace uw
+
+// A set of experts (host object; the weights stay the caller's).
+struct uw_experts {
+  uw::ExpertsView v{};
+  int device = 0;
+  const uw_matrix** ms = nullptr;       // UWF1: the matrices, and their indices when the table was made
+  const uint8_t** pidx = nullptr;
+  uw::ExpertEntry* table = nullptr;     // device
+  uw_allocator alloc{};
+};

@@ -143,6 +143,23 @@ _SIGS = {
                                         ctypes.POINTER(uw_tune_entry)]),
     "uw_lookup_tuning_grouped": (ctypes.c_int, [ctypes.c_uint64, ctypes.c_uint64, ctypes.c_int32, ctypes.c_int32,
                                                 ctypes.c_int32, _i64, ctypes.POINTER(uw_tune_entry)]),
+    "uw_quantize_mx4": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "uw_dequantize_mx4": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp]),
+    "uw_workspace_size_mx4": (ctypes.c_int, [_i64, _i64, _i64, ctypes.c_int, ctypes.POINTER(_sz)]),
+    "uw_matmul_mx4": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, ctypes.c_int, _vp, _sz, _vp]),
+    "uw_workspace_size_route": (ctypes.c_int, [_i64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_sz)]),
+    "uw_route_experts": (ctypes.c_int, [_vp, ctypes.c_int, _i64, ctypes.c_int32, _i64, _vp, ctypes.c_int32,
+                                        ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "uw_plan_experts": (ctypes.c_int, [_vp, _i64, ctypes.c_int32, ctypes.c_int32, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "uw_experts_bf16": (ctypes.c_int, [_vp, ctypes.c_int32, _i64, _i64, _i64, ctypes.POINTER(_vp)]),
+    "uw_experts_mx4": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, _i64, _i64, _i64, _i64, ctypes.POINTER(_vp)]),
+    "uw_experts_uwf1": (ctypes.c_int, [ctypes.POINTER(_vp), ctypes.c_int32, _vp, ctypes.POINTER(_vp)]),
+    "uw_free_experts": (None, [_vp]),
+    "uw_matmul_experts": (ctypes.c_int, [_vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "uw_matmul_experts_gated": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp]),
+    "uw_workspace_size_expert_mlp": (ctypes.c_int, [_vp, _vp, _i64, ctypes.c_int32, ctypes.POINTER(_sz)]),
+    "uw_expert_mlp": (ctypes.c_int, [_vp, _vp, _vp, _i64, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                     _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -523,3 +540,264 @@ class TorchAllocator:
     def free(self, p: int) -> None:
         self.live.pop(p, None)
         self.frees += 1
+
+
+# ---- MXFP4 -----------------------------------------------------------------
+# The calls below check what a pointer cannot carry -- element type, shape,
+# contiguity, device -- and raise ValueError before the library sees them.
+
+ACT_BF16, ACT_MX4 = 0, 1
+SCORE = {"softmax": 0, "softmax_topk": 1, "sigmoid": 2}
+_TYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _want(t: torch.Tensor, what: str, dtype, shape=None) -> int:
+    """Pointer of a contiguous tensor of this type (and shape) on the current device."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: must be contiguous")
+    _on_device(t, what)
+    return t.data_ptr()
+
+
+def _on_device(t: torch.Tensor, what: str) -> None:
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{what}: must be on the current device, is on {t.device}")
+
+
+def _rows2d(t: torch.Tensor, what: str) -> int:
+    """Row stride in elements of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: two dimensions with contiguous rows expected")
+    _on_device(t, what)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
+    if ws is None:
+        return None, 0
+    if not ws.is_contiguous():
+        raise ValueError("ws: must be contiguous")
+    _on_device(ws, "ws")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def mx4_scale_stride(cols: int) -> int:
+    """Bytes of scales per row (UW_MX4_SCALE_STRIDE)."""
+    return (cols + 127) // 128 * 4
+
+
+def uw_quantize_mx4(src: torch.Tensor, elem: torch.Tensor, scale: torch.Tensor, stream=None) -> None:
+    """src [rows][cols] BF16 or FP32 (rows may be strided) -> elem [rows][cols/2], scale [rows][mx4_scale_stride]."""
+    if src.dtype not in _TYPES:
+        raise ValueError(f"src: float32 or bfloat16 expected, got {src.dtype}")
+    ld = _rows2d(src, "src")
+    rows, cols = src.shape
+    pe = _want(elem, "elem", torch.uint8, (rows, cols // 2))
+    ps = _want(scale, "scale", torch.uint8, (rows, mx4_scale_stride(cols)))
+    _check(_lib.uw_quantize_mx4(src.data_ptr(), _TYPES[src.dtype], rows, cols, ld, pe, ps, _stream(stream)),
+           "uw_quantize_mx4")
+
+
+def uw_dequantize_mx4(elem: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, stream=None) -> None:
+    """The values of uw_quantize_mx4's arrays into out [rows][cols] BF16 (rows may be strided)."""
+    if out.dtype is not torch.bfloat16:
+        raise ValueError(f"out: bfloat16 expected, got {out.dtype}")
+    ld = _rows2d(out, "out")
+    rows, cols = out.shape
+    pe = _want(elem, "elem", torch.uint8, (rows, cols // 2))
+    ps = _want(scale, "scale", torch.uint8, (rows, mx4_scale_stride(cols)))
+    _check(_lib.uw_dequantize_mx4(pe, ps, rows, cols, out.data_ptr(), ld, _stream(stream)), "uw_dequantize_mx4")
+
+
+def uw_workspace_size_mx4(n: int, k: int, batch: int, act: int = ACT_BF16) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.uw_workspace_size_mx4(n, k, batch, act, ctypes.byref(b)), "uw_workspace_size_mx4")
+    return b.value
+
+
+def uw_matmul_mx4(elem: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                  ws: torch.Tensor | None = None, act: int = ACT_BF16, stream=None) -> None:
+    """y [batch][n] FP32 = x [batch][k] BF16 times the MXFP4 matrix (elem [n][k/2], scale [n][stride])."""
+    if x.dim() != 2 or elem.dim() != 2:
+        raise ValueError("x and elem: two dimensions expected")
+    (batch, k), n = x.shape, elem.shape[0]
+    pe = _want(elem, "elem", torch.uint8, (n, k // 2))
+    ps = _want(scale, "scale", torch.uint8, (n, mx4_scale_stride(k)))
+    px = _want(x, "x", torch.bfloat16)
+    py = _want(y, "y", torch.float32, (batch, n))
+    pw, nb = _ws(ws)
+    _check(_lib.uw_matmul_mx4(pe, ps, n, k, px, batch, py, act, pw, nb, _stream(stream)), "uw_matmul_mx4")
+
+
+# ---- mixture of experts ------------------------------------------------------
+
+class Routing:
+    """The buffers of a router's choice and of the plan that sorts its pairs by expert (see unweight.h)."""
+
+    def __init__(self, tokens: int, experts: int, topk: int, device="cuda"):
+        self.tokens, self.experts, self.topk = tokens, experts, topk
+        n = ctypes.c_size_t()
+        _check(_lib.uw_workspace_size_route(tokens, experts, topk, ctypes.byref(n)), "uw_workspace_size_route")
+        pairs = tokens * topk
+        self.ids = torch.empty(tokens, topk, dtype=torch.int32, device=device)
+        self.weights = torch.empty(tokens, topk, dtype=torch.float32, device=device)
+        self.offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
+        self.rows = torch.zeros(pairs, dtype=torch.int32, device=device)
+        self.slots = torch.empty(tokens, topk, dtype=torch.int32, device=device)
+        self.ws = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+
+
+def uw_route_experts(logits: torch.Tensor, routing: Routing, scoring: str = "softmax_topk",
+                     bias: torch.Tensor | None = None, stream=None) -> None:
+    """logits [tokens][experts] FP32 or BF16 (rows may be strided) -> routing's ids, weights and plan."""
+    r = routing
+    if logits.dtype not in _TYPES:
+        raise ValueError(f"logits: float32 or bfloat16 expected, got {logits.dtype}")
+    if scoring not in SCORE:
+        raise ValueError(f"scoring: one of {sorted(SCORE)} expected, got {scoring!r}")
+    ld = _rows2d(logits, "logits")
+    if logits.shape != (r.tokens, r.experts):
+        raise ValueError(f"logits: shape {(r.tokens, r.experts)} expected, got {tuple(logits.shape)}")
+    pb = _want(bias, "bias", torch.float32, (r.experts,)) if bias is not None else None
+    _on_device(r.ids, "routing")
+    pw, nb = _ws(r.ws)
+    _check(_lib.uw_route_experts(logits.data_ptr(), _TYPES[logits.dtype], r.tokens, r.experts, ld, pb, r.topk,
+                                 SCORE[scoring], r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
+                                 r.rows.data_ptr(), r.slots.data_ptr(), pw, nb, _stream(stream)),
+           "uw_route_experts")
+
+
+def uw_plan_experts(ids: torch.Tensor, routing: Routing, stream=None) -> None:
+    """The plan for choices made elsewhere: ids [tokens][topk] int32, outside 0..experts-1 = none."""
+    r = routing
+    pi = _want(ids, "ids", torch.int32, (r.tokens, r.topk))
+    _on_device(r.ids, "routing")
+    pw, nb = _ws(r.ws)
+    _check(_lib.uw_plan_experts(pi, r.tokens, r.experts, r.topk, r.offsets.data_ptr(), r.rows.data_ptr(),
+                                r.slots.data_ptr(), pw, nb, _stream(stream)), "uw_plan_experts")
+
+
+class Experts:
+    """Owns one uw_experts handle and keeps the weights it names alive."""
+
+    def __init__(self, handle: int, count: int, n: int, k: int, keep):
+        self.handle = ctypes.c_void_p(handle)
+        self.count, self.n, self.k, self.keep = count, n, k, keep
+
+    def free(self) -> None:
+        if self.handle and self.handle.value:
+            _lib.uw_free_experts(self.handle)
+            self.handle = ctypes.c_void_p(None)
+        self.keep = None
+
+    def __del__(self):
+        try:
+            self.free()
+        except Exception:
+            pass
+
+
+def uw_experts_bf16(w: torch.Tensor, count: int, n: int, k: int, stride: int = 0) -> Experts:
+    """w: BF16, expert e's [n][k] at element e * stride (0: n * k); w may be a view into a larger array."""
+    if w.dtype is not torch.bfloat16:
+        raise ValueError(f"w: bfloat16 expected, got {w.dtype}")
+    _on_device(w, "w")
+    h = ctypes.c_void_p()
+    _check(_lib.uw_experts_bf16(w.data_ptr(), count, n, k, stride, ctypes.byref(h)), "uw_experts_bf16")
+    try:
+        _holds(w, 2 * (((stride or n * k) * (count - 1)) + n * k), "w")
+    except ValueError:
+        _lib.uw_free_experts(h)
+        raise
+    return Experts(h.value, count, n, k, w)
+
+
+def _holds(t: torch.Tensor, nbytes: int, what: str) -> None:
+    """t's storage holds nbytes from t's first element on."""
+    have = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+    if have < nbytes:
+        raise ValueError(f"{what}: {nbytes} bytes expected, {have} there")
+
+
+def uw_experts_mx4(elem: torch.Tensor, scale: torch.Tensor, count: int, n: int, k: int, elem_stride: int = 0,
+                   scale_stride: int = 0) -> Experts:
+    """elem, scale: uint8, expert e's [n][k/2] and [n][mx4_scale_stride(k)] at byte e * their stride (0: contiguous)."""
+    for t, what in ((elem, "elem"), (scale, "scale")):
+        if t.dtype is not torch.uint8:
+            raise ValueError(f"{what}: uint8 expected, got {t.dtype}")
+        _on_device(t, what)
+    h = ctypes.c_void_p()
+    _check(_lib.uw_experts_mx4(elem.data_ptr(), scale.data_ptr(), count, n, k, elem_stride, scale_stride,
+                               ctypes.byref(h)), "uw_experts_mx4")
+    eb, sb = n * (k // 2), n * mx4_scale_stride(k)
+    try:
+        _holds(elem, (elem_stride or eb) * (count - 1) + eb, "elem")
+        _holds(scale, (scale_stride or sb) * (count - 1) + sb, "scale")
+    except ValueError:
+        _lib.uw_free_experts(h)
+        raise
+    return Experts(h.value, count, n, k, (elem, scale))
+
+
+def uw_experts_uwf1(ms, stream=None) -> Experts:
+    """ms: compressed matrices of one shape with resident palette indices, one per expert."""
+    arr = (ctypes.c_void_p * len(ms))(*[m.handle.value for m in ms])
+    h = ctypes.c_void_p()
+    _check(_lib.uw_experts_uwf1(arr, len(ms), _stream(stream), ctypes.byref(h)), "uw_experts_uwf1")
+    i = ms[0].info()
+    return Experts(h.value, len(ms), i.n, i.k, list(ms))
+
+
+def uw_free_experts(w: Experts) -> None:
+    w.free()
+
+
+def _ragged(w: Experts, offsets: torch.Tensor, rows, x: torch.Tensor, y: torch.Tensor, dtype):
+    if x.dim() != 2 or x.shape[1] != w.k:
+        raise ValueError(f"x: shape [rows, {w.k}] expected, got {tuple(x.shape)}")
+    if y.dim() != 2 or y.shape[1] != w.n:
+        raise ValueError(f"output: shape [slots, {w.n}] expected, got {tuple(y.shape)}")
+    slots = y.shape[0]
+    po = _want(offsets, "offsets", torch.int32, (w.count + 1,))
+    pr = _want(rows, "rows", torch.int32, (slots,)) if rows is not None else None
+    return po, pr, slots, _want(x, "x", torch.bfloat16), x.shape[0], _want(y, "output", dtype)
+
+
+def uw_matmul_experts(w: Experts, offsets: torch.Tensor, rows: torch.Tensor | None, x: torch.Tensor,
+                      y: torch.Tensor, stream=None) -> None:
+    """y [slots][n] FP32, x [x_rows][k] BF16; rows [slots] int32 or None (slot s multiplies row s)."""
+    _check(_lib.uw_matmul_experts(w.handle, *_ragged(w, offsets, rows, x, y, torch.float32), _stream(stream)),
+           "uw_matmul_experts")
+
+
+def uw_matmul_experts_gated(gate: Experts, up: Experts, offsets: torch.Tensor, rows: torch.Tensor | None,
+                            x: torch.Tensor, h: torch.Tensor, stream=None) -> None:
+    """h [slots][n] BF16 = silu(x . gate^T) * (x . up^T)."""
+    _check(_lib.uw_matmul_experts_gated(gate.handle, up.handle, *_ragged(gate, offsets, rows, x, h, torch.bfloat16),
+                                        _stream(stream)), "uw_matmul_experts_gated")
+
+
+def uw_workspace_size_expert_mlp(gate: Experts, down: Experts, tokens: int, topk: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.uw_workspace_size_expert_mlp(gate.handle, down.handle, tokens, topk, ctypes.byref(b)),
+           "uw_workspace_size_expert_mlp")
+    return b.value
+
+
+def uw_expert_mlp(gate: Experts, up: Experts, down: Experts, routing: Routing, x: torch.Tensor, out: torch.Tensor,
+                  ws: torch.Tensor, stream=None) -> None:
+    """out [tokens][k] BF16: the layer's MLP on a routing made by uw_route_experts (or a plan and weights)."""
+    r = routing
+    if r.experts != gate.count:
+        raise ValueError(f"routing: {gate.count} experts expected, got {r.experts}")
+    px = _want(x, "x", torch.bfloat16, (r.tokens, gate.k))
+    po = _want(out, "out", torch.bfloat16, (r.tokens, gate.k))
+    _on_device(r.ids, "routing")
+    pw, nb = _ws(ws)
+    _check(_lib.uw_expert_mlp(gate.handle, up.handle, down.handle, r.tokens, r.topk, r.offsets.data_ptr(),
+                              r.rows.data_ptr(), r.slots.data_ptr(), r.weights.data_ptr(), px, po, pw, nb,
+                              _stream(stream)), "uw_expert_mlp")

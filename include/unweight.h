@@ -489,6 +489,147 @@ uw_status uw_yardstick(int kind, const void* src_dev, void* dst_dev, size_t byte
  * (UW_ERR_CORRUPT); clears the flag. */
 uw_status uw_sync_status(const uw_matrix* m, void* stream);
 
+/* ---- MXFP4 weights and activations -------------------------------------------
+ * OCP Microscaling MXFP4: E2M1 elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ * negatives), one E8M0 scale (2^(byte - 127), 255 = NaN) per 32 consecutive
+ * elements of a row.  Elements are [rows][cols / 2] bytes, element 2i in the
+ * low nibble of byte i.  Scales are [rows][UW_MX4_SCALE_STRIDE(cols)] bytes:
+ * cols / 32 of them, then padding up to a multiple of four (written as 0,
+ * never used), so that a row's scales start on a 4-byte boundary; without
+ * padding whenever cols is a multiple of 128.  cols must be a multiple of 32
+ * (UW_ERR_UNSUPPORTED).  (saidapartage.blog, section "Un complément, pas un
+ * remplaçant": quantised weights are the other half of what is served.) */
+#define UW_MX4_SCALE_STRIDE(cols) (((cols) + 127) / 128 * 4)
+
+typedef enum { UW_TYPE_F32 = 0, UW_TYPE_BF16 = 1 } uw_type;
+
+/* Quantise a [rows][cols] array whose rows start `ld` elements apart (ld >=
+ * cols, a multiple of 8).  A block's scale is 2^(floor(log2 max|v|) - 2), at
+ * least 2^-127; elements are v / scale rounded to nearest, ties to the even
+ * code, at most 6 in magnitude (what lies between 6 and 8 scales saturates).  A
+ * block with an infinity or a NaN gets scale byte 255 and zero elements.
+ * src_dev, elem_dev 16-byte, scale_dev 4-byte aligned.  Here and below, a call
+ * on no rows, slots or tokens does nothing (the routing calls still write
+ * offsets) and needs none of its arrays. */
+uw_status uw_quantize_mx4(const void* src_dev, uw_type src_type, int64_t rows, int64_t cols, int64_t ld,
+                          uint8_t* elem_dev, uint8_t* scale_dev, void* stream);
+
+/* The BF16 values the elements stand for, rows `ld` apart (>= cols, a multiple
+ * of 8); what lies between rows is left as it was.  Exact, except that scale
+ * bytes of 253 and 254, which uw_quantize_mx4 never writes, can overflow to
+ * infinity; byte 255 gives NaN. */
+uw_status uw_dequantize_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64_t rows, int64_t cols,
+                            uint16_t* out_dev, int64_t ld, void* stream);
+
+/* y[b][n] = sum_k x[b][k] W[n][k] for b < batch with W in MXFP4 ([n][k]), fp32
+ * sums and output.  act: UW_ACT_BF16 takes x as it is, UW_ACT_MX4 its MXFP4
+ * quantisation (uw_quantize_mx4's, made inside the call), so that both
+ * operands have 4 bits.  Elements times scale are what is multiplied; a
+ * weight whose value overflows BF16 (scale bytes 253 and 254) counts as
+ * infinite.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
+ * 16-byte aligned.  The workspace (uw_workspace_size_mx4 bytes, 16-byte
+ * aligned) serves one call at a time. */
+typedef enum { UW_ACT_BF16 = 0, UW_ACT_MX4 = 1 } uw_activation;
+uw_status uw_workspace_size_mx4(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes);
+uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64_t n, int64_t k,
+                        const uint16_t* x_dev, int64_t batch, float* y_dev, uw_activation act, void* ws_dev,
+                        size_t ws_bytes, void* stream);
+
+/* ---- mixture of experts --------------------------------------------------------
+ * The MLP of a mixture-of-experts layer: a router picks topk of the experts for
+ * each token, the (token, choice) pairs are sorted by expert, and each expert
+ * multiplies its own rows.
+ *
+ * A pair is token * topk + choice; a slot is a pair's place in the sorted
+ * order.  The plan is three device arrays:
+ *   offsets [experts + 1]     expert e has slots offsets[e] .. offsets[e + 1) - 1
+ *   rows    [tokens * topk]   slot -> token; entries from offsets[experts] on
+ *                             are left as they were
+ *   slots   [tokens * topk]   pair -> slot, -1 for a pair without an expert
+ * Within an expert, slots keep the order of their pairs.
+ *
+ * Router.  logits_dev is [tokens][experts], rows `ld` elements apart, FP32 or
+ * BF16.  A choice is by key = logit + bias (bias_dev [experts] FP32, may be
+ * NULL), larger first, equal keys by the lower index; experts whose key is
+ * NaN or -inf are never chosen.  A token with fewer selectable experts than
+ * topk (a padded token's row of -inf has none) gets id -1 and weight 0 for
+ * the rest.  Weights use the logits without the bias:
+ *   UW_SCORE_SOFTMAX        softmax over the selectable experts
+ *   UW_SCORE_SOFTMAX_TOPK   softmax over the chosen ones
+ *   UW_SCORE_SIGMOID        sigmoids divided by their sum over the chosen ones
+ * ids_dev and weights_dev are [tokens][topk].  experts <= 1024 and topk <= 16
+ * (UW_ERR_UNSUPPORTED), topk <= experts.  Results repeat bit for bit.  The
+ * workspace (uw_workspace_size_route bytes, may be 0) serves one call at a
+ * time. */
+typedef enum { UW_SCORE_SOFTMAX = 0, UW_SCORE_SOFTMAX_TOPK = 1, UW_SCORE_SIGMOID = 2 } uw_scoring;
+uw_status uw_workspace_size_route(int64_t tokens, int32_t experts, int32_t topk, size_t* bytes);
+uw_status uw_route_experts(const void* logits_dev, uw_type type, int64_t tokens, int32_t experts, int64_t ld,
+                           const float* bias_dev, int32_t topk, uw_scoring scoring, int32_t* ids_dev,
+                           float* weights_dev, int32_t* offsets_dev, int32_t* rows_dev, int32_t* slots_dev,
+                           void* ws_dev, size_t ws_bytes, void* stream);
+
+/* The plan alone, for choices made elsewhere: ids_dev [tokens][topk]; ids
+ * outside 0 .. experts - 1 count as no expert.  An expert may appear twice in a
+ * token. */
+uw_status uw_plan_experts(const int32_t* ids_dev, int64_t tokens, int32_t experts, int32_t topk,
+                          int32_t* offsets_dev, int32_t* rows_dev, int32_t* slots_dev, void* ws_dev, size_t ws_bytes,
+                          void* stream);
+
+/* The experts' weights of one projection, W_e[n][k] for e < count, in one of
+ * three forms.  The set keeps the pointers; the weights stay the caller's and
+ * must outlive it.  k must be a multiple of 32, count <= 1024
+ * (UW_ERR_UNSUPPORTED).
+ *   uw_experts_bf16   BF16, expert e at w_dev + e * stride elements (0: n * k;
+ *                     a multiple of 8), rows contiguous
+ *   uw_experts_mx4    MXFP4, expert e's elements and scales e * their stride
+ *                     in bytes on (0: contiguous; multiples of 16 and 4)
+ *   uw_experts_uwf1   `count` compressed matrices of one shape, stored [N][K]
+ *                     (UW_ERR_UNSUPPORTED otherwise), with resident palette
+ *                     indices (uw_transcode_palette(m, NULL);
+ *                     UW_ERR_STATE without), the direct-palette form: the
+ *                     Huffman stream is not needed.  Copies a small table to
+ *                     the device and synchronises `stream`.  The matrices
+ *                     must not be freed before the set; a call after an index
+ *                     array was dropped or replaced returns UW_ERR_STATE. */
+typedef struct uw_experts uw_experts;
+uw_status uw_experts_bf16(const uint16_t* w_dev, int32_t count, int64_t n, int64_t k, int64_t stride,
+                          uw_experts** out);
+uw_status uw_experts_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int32_t count, int64_t n, int64_t k,
+                         int64_t elem_stride, int64_t scale_stride, uw_experts** out);
+uw_status uw_experts_uwf1(const uw_matrix* const* ms, int32_t count, void* stream, uw_experts** out);
+void uw_free_experts(uw_experts* w);
+
+/* Products grouped by expert over ragged rows: for every slot s of expert e
+ *   y[s][n] = sum_k x[rows[s]][k] W_e[n][k]                       (fp32)
+ *   h[s][n] = silu(g) * u, g and u the products with gate and up   (BF16)
+ * with fp32 sums; silu(g) = g / (1 + exp(-g)), and h is rounded once.
+ * offsets_dev as above (values outside 0 .. slots and descending ones are
+ * clamped); slots is the capacity of rows_dev, y_dev and h_dev: rows from
+ * offsets[experts] on are left as they were.  rows_dev NULL: slot s
+ * multiplies row s of x.  x_dev is [x_rows][k]; a row index outside it selects
+ * a row of zeros.  gate and up have the same form, count and shape.  x_dev,
+ * y_dev, h_dev 16-byte aligned.  Needs no workspace; results repeat bit for
+ * bit. */
+uw_status uw_matmul_experts(const uw_experts* w, const int32_t* offsets_dev, const int32_t* rows_dev, int64_t slots,
+                            const uint16_t* x_dev, int64_t x_rows, float* y_dev, void* stream);
+uw_status uw_matmul_experts_gated(const uw_experts* gate, const uw_experts* up, const int32_t* offsets_dev,
+                                  const int32_t* rows_dev, int64_t slots, const uint16_t* x_dev, int64_t x_rows,
+                                  uint16_t* h_dev, void* stream);
+
+/* The layer on a plan: out[t] = sum_j weights[t][j] * (h[s] . D_e^T), s the slot
+ * of choice j, h as above (rounded to BF16, the down product's input), the
+ * sum in fp32 in the order of j and rounded to BF16 once.  A token without
+ * experts gets zeros.  gate, up [n][k] and down [k][n] of the same count; the
+ * sets may differ in form between (gate, up) and down.  out_dev is
+ * [tokens][k].  The workspace (uw_workspace_size_expert_mlp bytes) serves one
+ * call at a time. */
+uw_status uw_workspace_size_expert_mlp(const uw_experts* gate, const uw_experts* down, int64_t tokens, int32_t topk,
+                                       size_t* bytes);
+uw_status uw_expert_mlp(const uw_experts* gate, const uw_experts* up, const uw_experts* down, int64_t tokens,
+                        int32_t topk, const int32_t* offsets_dev, const int32_t* rows_dev, const int32_t* slots_dev,
+                        const float* weights_dev, const uint16_t* x_dev, uint16_t* out_dev, void* ws_dev,
+                        size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
