@@ -121,6 +121,91 @@ __device__ __forceinline__ Share find_share(const RaggedRows& r, int experts, in
   return out;
 }
 
+// The same for tiles of ntiles columns, dealt so that each XCD works on one
+// contiguous run of the list: blocks go to the 8 XCDs round robin, so block b
+// takes entry b / 8 of XCD b % 8's eighth of the list that really exists (its
+// length follows from the offsets).  The list runs over experts, then column
+// tiles, then an expert's row chunks, so neighbours share weights and x in
+// one L2.  Returns the column tile, or -1: nothing to do.
+__device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, unsigned block, int ntiles, int chunk,
+                                         Share& out) {
+  out = Share{0, 0, 0};
+  const int lane = threadIdx.x & 63;
+  int64_t total = 0;
+  auto round = [&](int e0, int32_t (&o)[5], int (&c)[4]) __attribute__((always_inline)) {
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int e = e0 + 4 * lane + i;
+      const int32_t v = r.offsets[e < experts ? e : experts];
+      o[i] = v < 0 ? 0 : (int64_t)v < r.slots ? v : (int32_t)r.slots;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = o[i + 1] > o[i] ? (int)(((int64_t)o[i + 1] - o[i] + chunk - 1) / chunk) : 0;
+      mine += c[i];
+    }
+    int sum = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(sum, d);
+      sum += lane >= d ? up : 0;
+    }
+    return sum;   // inclusive over lanes
+  };
+  if (!r.offsets) {
+    total = (r.slots + chunk - 1) / chunk;
+  } else {
+    for (int e0 = 0; e0 < experts; e0 += 256) {
+      int32_t o[5];
+      int c[4];
+      total += __builtin_amdgcn_readlane(round(e0, o, c), 63);
+    }
+  }
+  const int64_t tiles = total * ntiles, share = (tiles + 7) / 8;
+  const int64_t at = (block & 7) * share + (block >> 3);
+  if ((int64_t)(block >> 3) >= share || at >= tiles) return -1;
+  if (!r.offsets) {
+    const int64_t m = at % total;
+    out.first = m * chunk;
+    out.count = (int)(r.slots - out.first < chunk ? r.slots - out.first : chunk);
+    return (int)(at / total);
+  }
+  int64_t before = 0;   // chunks of the experts before this round's
+  for (int e0 = 0; e0 < experts; e0 += 256) {
+    int32_t o[5];
+    int c[4];
+    const int sum = round(e0, o, c);
+    const int mine = c[0] + c[1] + c[2] + c[3];
+    const int64_t lo = (before + sum - mine) * ntiles, hi = (before + sum) * ntiles;
+    const uint64_t hit = __ballot(at >= lo && at < hi);
+    if (hit) {
+      int64_t left = at - lo;   // in tiles of this lane's four experts
+      int e = 0, n = c[0];
+      int32_t b = o[0], end = o[1];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const bool go = e == i && left >= (int64_t)c[i] * ntiles;
+        left -= go ? (int64_t)c[i] * ntiles : 0;
+        e = go ? i + 1 : e;
+        n = go ? c[i + 1] : n;
+        b = go ? o[i + 1] : b;
+        end = go ? o[i + 2] : end;
+      }
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      out.expert = __builtin_amdgcn_readlane(e0 + 4 * lane + e, src);
+      const int chunks = __builtin_amdgcn_readlane(n, src);
+      const int l = __builtin_amdgcn_readlane((int)left, src);
+      const int32_t begin = __builtin_amdgcn_readlane(b, src), stop = __builtin_amdgcn_readlane(end, src);
+      out.first = (int64_t)begin + (int64_t)(l % chunks) * chunk;
+      out.count = (int)(stop - out.first < chunk ? stop - out.first : chunk);
+      return l / chunks;
+    }
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  return -1;
+}
+
 // Chunks that slots rows over `experts` experts can make at most: every
 // expert with rows adds less than one chunk beyond its share.
 inline int64_t max_chunks(int64_t slots, int experts, int chunk, bool ragged) {
@@ -172,6 +257,7 @@ struct ExpertsCall {
 };
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s);
 hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s);
+hipError_t launch_experts_tile(const ExpertsCall& c, int rows, hipStream_t s);   // rows of a tile: 64, 128 or 256
 
 hipError_t launch_quantize_mx4(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* elem,
                                uint8_t* scale, hipStream_t s);

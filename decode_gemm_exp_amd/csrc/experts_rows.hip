@@ -322,6 +322,19 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
   }
 }
 
-hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) { return launch_experts_rows(c, s); }
+// Which kernel: by the rows an expert has on average if every slot is used
+// (the counts themselves are on the device).  The register-fed kernel streams
+// weights for few rows; the LDS tiles rebuild and read each weight once per
+// tile of 64, 128 or 256 rows.  Measured (us, register-fed / 64 / 128 / 256):
+//   BF16, 16 experts 2048x2048: 16 rows 39 / 30 / 34 / 45, 64 rows 70 / 35 / 43 / 61
+//   BF16 gated, 64 experts 1408x2048, 512 rows: 1988 / 563 / 499 / 454
+//   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1445 / 625 / 522 / 427
+//   UWF1, 32 experts 2048x4096, 3 rows: 83 / 114 / 120 / 175
+hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
+  const int64_t e = c.r.offsets ? c.w.count : 1;
+  const int64_t avg = (c.r.slots + e - 1) / e;
+  if (avg <= 8) return launch_experts_rows(c, s);
+  return launch_experts_tile(c, avg <= 96 ? 64 : avg <= 320 ? 128 : 256, s);
+}
 
 }  // namespace uw

@@ -182,8 +182,15 @@ def _ptr(t) -> int | None:
     return int(t)
 
 
+# torch's current stream as a raw handle: a tenth of the time of building a
+# Stream object, which small calls notice
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
