@@ -39,6 +39,24 @@ struct ExpertsView {
   const ExpertEntry* table;   // UWF1
 };
 
+// A load the compiler knows to be from global memory.  Pointers read from the
+// device table have no address space of their own, and flat loads would
+// count with the LDS reads: every wait for one would wait for all.
+template <typename T>
+__device__ __forceinline__ T gload(const void* p) {
+  return *reinterpret_cast<const __attribute__((address_space(1))) T*>(reinterpret_cast<uintptr_t>(p));
+}
+typedef __attribute__((ext_vector_type(4))) unsigned int u32x4_t;
+typedef __attribute__((ext_vector_type(2))) unsigned int u32x2_t;
+__device__ __forceinline__ uint4 gload16(const void* p) {
+  const u32x4_t v = gload<u32x4_t>(p);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+__device__ __forceinline__ uint2 gload8(const void* p) {
+  const u32x2_t v = gload<u32x2_t>(p);
+  return make_uint2(v.x, v.y);
+}
+
 __host__ __device__ constexpr int64_t mx4_scale_stride(int64_t k) { return (k + 127) / 128 * 4; }
 
 // Ragged rows: expert e's are slots [offsets[e], offsets[e + 1]); slot s
@@ -121,10 +139,25 @@ __device__ __forceinline__ Share find_share(const RaggedRows& r, int experts, in
   return out;
 }
 
+// Tile `l` of a grid of `chunks` row chunks times `ntiles` column tiles: bands
+// of eight column tiles, within a band the row chunks in turn, each over the
+// band's columns.  The 32 blocks an XCD runs at once then cover about 4 x 8
+// tiles, 12 panels of x and weights to keep in its L2 instead of 33.
+__device__ __forceinline__ void tile_of(uint32_t l, uint32_t chunks, uint32_t ntiles, int& chunk, int& nt) {
+  constexpr uint32_t kBand = 8;
+  const uint32_t band = l / (kBand * chunks), in = l - band * kBand * chunks;
+  const uint32_t width = ntiles - band * kBand < kBand ? ntiles - band * kBand : kBand;
+  const uint32_t m = in / width;
+  chunk = __builtin_amdgcn_readfirstlane((int)m);
+  nt = __builtin_amdgcn_readfirstlane((int)(band * kBand + in - m * width));
+}
+
 // The same for tiles of ntiles columns, dealt so that each XCD works on one
 // contiguous run of the list: blocks go to the 8 XCDs round robin, so block b
 // takes entry b / 8 of XCD b % 8's eighth of the list that really exists (its
-// length follows from the offsets).  The list runs over experts, then column
+// length follows from the offsets).  What it returns is in scalar registers:
+// buffer resources built from it then need no loop over a wave's lanes (a
+// division done in vector registers would leave it there).  The list runs over experts, then column
 // tiles, then an expert's row chunks, so neighbours share weights and x in
 // one L2.  Returns the column tile, or -1: nothing to do.
 __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, unsigned block, int ntiles, int chunk,
@@ -166,10 +199,11 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, unsig
   const int64_t at = (block & 7) * share + (block >> 3);
   if ((int64_t)(block >> 3) >= share || at >= tiles) return -1;
   if (!r.offsets) {
-    const int64_t m = at % total;
-    out.first = m * chunk;
+    int m, nt;
+    tile_of((uint32_t)at, (uint32_t)total, (uint32_t)ntiles, m, nt);   // (at < 2^31: the grid is)
+    out.first = m * (int64_t)chunk;
     out.count = (int)(r.slots - out.first < chunk ? r.slots - out.first : chunk);
-    return (int)(at / total);
+    return nt;
   }
   int64_t before = 0;   // chunks of the experts before this round's
   for (int e0 = 0; e0 < experts; e0 += 256) {
@@ -197,9 +231,11 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, unsig
       const int chunks = __builtin_amdgcn_readlane(n, src);
       const int l = __builtin_amdgcn_readlane((int)left, src);
       const int32_t begin = __builtin_amdgcn_readlane(b, src), stop = __builtin_amdgcn_readlane(end, src);
-      out.first = (int64_t)begin + (int64_t)(l % chunks) * chunk;
+      int m, nt;
+      tile_of((uint32_t)l, (uint32_t)chunks, (uint32_t)ntiles, m, nt);
+      out.first = (int64_t)begin + (int64_t)m * chunk;
       out.count = (int)(stop - out.first < chunk ? stop - out.first : chunk);
-      return l / chunks;
+      return nt;
     }
     before += __builtin_amdgcn_readlane(sum, 63);
   }
@@ -263,6 +299,9 @@ hipError_t launch_quantize_mx4(const void* src, bool f32, int64_t rows, int64_t 
                                uint8_t* scale, hipStream_t s);
 hipError_t launch_dequantize_mx4(const uint8_t* elem, const uint8_t* scale, int64_t rows, int64_t cols, uint16_t* out,
                                  int64_t ld, hipStream_t s);
+// both operands in MXFP4 (rows contiguous, scales mx4_scale_stride(k) a row)
+hipError_t launch_mx4_tile(const uint8_t* we, const uint8_t* ws, int64_t n, int64_t k, const uint8_t* xe,
+                           const uint8_t* xs, int64_t batch, float* y, hipStream_t s);
 // x -> the BF16 values its MXFP4 form stands for
 hipError_t launch_round_mx4(const uint16_t* x, int64_t rows, int64_t cols, uint16_t* out, hipStream_t s);
 

@@ -97,6 +97,10 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
   return status_of(launch_experts(c, s));
 }
 
+// Up to this many rows x's 4-bit values go through the register-fed kernel as
+// BF16; beyond, both operands stay in 4 bits.
+constexpr int64_t kMx4RowsMax = 8;
+
 uw_status check_route(int64_t tokens, int32_t experts, int32_t topk) {
   if (tokens < 0 || experts <= 0 || topk <= 0 || topk > experts) return UW_ERR_INVALID;
   if (experts > kMaxExperts || topk > kMaxTopk || tokens > INT32_MAX / topk) return UW_ERR_UNSUPPORTED;
@@ -151,7 +155,10 @@ uw_status uw_workspace_size_mx4(int64_t n, int64_t k, int64_t batch, uw_activati
   const uw_status st = check_shape(n, k);
   if (st != UW_OK) return st;
   if (batch > INT32_MAX) return UW_ERR_UNSUPPORTED;
-  *bytes = act == UW_ACT_MX4 ? pad256(2 * (uint64_t)batch * (uint64_t)k) : 0;
+  const uint64_t b = (uint64_t)batch;
+  *bytes = act != UW_ACT_MX4     ? 0
+           : batch <= kMx4RowsMax ? pad256(2 * b * (uint64_t)k)
+                                  : pad256(b * (uint64_t)(k / 2)) + pad256(b * (uint64_t)mx4_scale_stride(k));
   return UW_OK;
 }
 
@@ -168,6 +175,12 @@ uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64
     return UW_ERR_INVALID;
   if (need && (!ws_dev || ws_bytes < need)) return UW_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
+  if (act == UW_ACT_MX4 && batch > kMx4RowsMax) {
+    uint8_t* xe = static_cast<uint8_t*>(ws_dev);
+    uint8_t* xs = xe + pad256((uint64_t)batch * (uint64_t)(k / 2));
+    st = status_of(launch_quantize_mx4(x_dev, false, batch, k, k, xe, xs, s));
+    return st != UW_OK ? st : status_of(launch_mx4_tile(elem_dev, scale_dev, n, k, xe, xs, batch, y_dev, s));
+  }
   if (act == UW_ACT_MX4) {
     st = status_of(launch_round_mx4(x_dev, batch, k, static_cast<uint16_t*>(ws_dev), s));
     if (st != UW_OK) return st;

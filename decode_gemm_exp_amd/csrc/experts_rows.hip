@@ -70,8 +70,8 @@ template <int FORM>
 __device__ __forceinline__ void load_flags(const Mat& m, int64_t row, int64_t K, int64_t k, bool ok, Flags& f) {
   if constexpr (form_is_pal(FORM)) {
     const uint64_t w = ok ? (uint64_t)(row * K + k) >> 11 : 0;
-    f.fw = m.t.vflags[w];
-    f.rw = m.t.vrank[w];
+    f.fw = gload<uint32_t>(m.t.vflags + w);
+    f.rw = gload<uint32_t>(m.t.vrank + w);
   }
 }
 
@@ -98,13 +98,13 @@ __device__ __forceinline__ void load_raw(const Mat& m, int64_t row, int64_t K, i
   } else {
     const int64_t k = k0 + k_off<FORM>(0, 0, g);
     const uint64_t el = (uint64_t)(row * K + (k < K ? k : 0));
-    r.d[0] = *reinterpret_cast<const uint4*>(m.t.sm + el);
-    r.d[1] = *reinterpret_cast<const uint4*>(m.t.sm + el + 16);
+    r.d[0] = gload16(m.t.sm + el);
+    r.d[1] = gload16(m.t.sm + el + 16);
     const uint64_t grp = el >> 6;
     const bool v = k < K && group_verbatim(fl.fw, grp);
     const uint8_t* p = v ? m.t.vexp + (uint64_t)group_rank(fl.fw, fl.rw, grp) * 64 + (el & 63) : m.t.pidx + el / 2;
-    r.d[2] = *reinterpret_cast<const uint4*>(p);
-    if (v) r.d[3] = *reinterpret_cast<const uint4*>(p + 16);
+    r.d[2] = gload16(p);
+    if (v) r.d[3] = gload16(p + 16);
     r.f = v ? 1u : 0u;
   }
 }
@@ -326,15 +326,16 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
 // (the counts themselves are on the device).  The register-fed kernel streams
 // weights for few rows; the LDS tiles rebuild and read each weight once per
 // tile of 64, 128 or 256 rows.  Measured (us, register-fed / 64 / 128 / 256):
-//   BF16, 16 experts 2048x2048: 16 rows 39 / 30 / 34 / 45, 64 rows 70 / 35 / 43 / 61
-//   BF16 gated, 64 experts 1408x2048, 512 rows: 1988 / 563 / 499 / 454
-//   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1445 / 625 / 522 / 427
-//   UWF1, 32 experts 2048x4096, 3 rows: 83 / 114 / 120 / 175
+//   BF16, 16 experts 2048x2048, 64 rows: 69 / 42 / 44 / 53
+//   BF16 gated, 64 experts 1408x2048, 512 rows: 1985 / 581 / 529 / 450
+//   BF16 layer, 64 experts 1408x2048, 281 rows: 1902 / 601 / 593 / 539
+//   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1438 / 772 / 495 / 409
+//   UWF1, 32 experts 2048x4096, 3 rows: 78 / 106 / 110 / 135
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
   const int64_t e = c.r.offsets ? c.w.count : 1;
   const int64_t avg = (c.r.slots + e - 1) / e;
   if (avg <= 8) return launch_experts_rows(c, s);
-  return launch_experts_tile(c, avg <= 96 ? 64 : avg <= 320 ? 128 : 256, s);
+  return launch_experts_tile(c, avg <= 96 ? 64 : avg <= 160 ? 128 : 256, s);
 }
 
 }  // namespace uw

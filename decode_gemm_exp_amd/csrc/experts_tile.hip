@@ -8,24 +8,32 @@
 // four along the columns, each BM/2 x 64.  K advances 64 at a time through two
 // LDS buffers:
 //   * step s runs its MFMAs from one buffer, fragments one 16-wide slice ahead
-//     of use, while every thread moves step s+1 from registers into the other
-//     buffer (weights rebuilt to BF16 on the way, once per block) and asks for
-//     the data of step s+2;
+//     of use.  x and BF16 weights go straight from memory to LDS (16 bytes a
+//     lane, no registers); UWF1 and MXFP4 weights through registers, rebuilt
+//     to BF16 once per block, loaded two steps ahead and stored one ahead;
 //   * the one barrier of a step stands before its last slice's MFMAs, so the
-//     next step's first fragments travel while those run;
+//     next step's first fragments travel while those run, and the buffer the
+//     step leaves is refilled for the step after the next right behind it;
 //   * LDS rows are 128 bytes without padding; 16-byte piece c of row r sits at
-//     c ^ (r & 7), so eight rows of one fragment column meet eight different
-//     piece columns and neither reads nor writes collide.
-// Gathered rows of x cost nothing extra: a thread keeps the pointers of its
-// rows.  Waves whose slots all lie behind the expert's last row skip their
+//     c ^ (r / 2 % 8).  LDS has 64 banks, two rows' worth, and serves 16 lanes of
+//     a 16-byte read at a time: 16 rows of one fragment column then meet all
+//     of them once.  (With c ^ r % 8 rows eight apart shared banks: four lost
+//     cycles for each of the reads, a quarter of the kernel's cycles.)
+// Gathered rows of x cost nothing extra: a thread keeps the offsets of its rows
+// in a buffer resource over x, and what must read as zero (a K tail, a row
+// index outside x) lies past the resource's end.  Beyond 2 GiB of x the rows go
+// by 64-bit pointers instead (BIG, 256-row tiles only): those loads are of the
+// flat kind, whose counters the compiler must drain before any LDS read, about
+// 10 % of the time.  Waves whose slots all lie behind the expert's last row skip their
 // MFMAs.
+#include <type_traits>
+
 #include "experts.h"
 
 namespace uw {
 namespace {
 
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
-typedef __attribute__((ext_vector_type(4))) unsigned int u32x4_t;
 
 constexpr int kBK = 64, kBN = 256, kNT = 512;
 constexpr uint32_t kOutside = 0x7FFF0000u;   // past the end of every buffer resource here
@@ -38,7 +46,7 @@ __device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t byte
   return make_uint4(v.x, v.y, v.z, v.w);
 }
 
-__device__ __forceinline__ uint32_t piece_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ (row & 7)) << 4)); }
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ ((row >> 1) & 7)) << 4)); }
 
 // A thread's share of the weight tile: what it loads for a step and how it
 // becomes BF16 in LDS.  Rows: LDS row c of the tile is weight row row_of(c).
@@ -46,38 +54,36 @@ __device__ __forceinline__ uint32_t piece_at(int row, int piece) { return (uint3
 template <int FORM>
 struct Weights;
 
-// BF16: four pieces of eight weights, LDS rows tid / 8 + 64 i
+// what a K tail or a row index outside x reads where x goes by pointers
+__device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+// the piece of its LDS row that lands at this thread's place (see piece_at)
+__device__ __forceinline__ int own_piece() { return (threadIdx.x ^ (threadIdx.x >> 4)) & 7; }
+
+// BF16: four pieces of eight weights, LDS rows tid / 8 + 64 i, straight to LDS
 template <>
 struct Weights<kFormBf16> {
+  static constexpr bool kDirect = true;
   __amdgpu_buffer_rsrc_t r;
   uint32_t off[4], col;
-  uint4 d[4];
   template <typename RowOf>
   __device__ __forceinline__ void init(const ExpertsView& w, const ExpertsView& u, int e, int64_t n0, RowOf&& row_of) {
     const int tid = threadIdx.x;
-    col = 8u * (tid & 7);
-    int first_up = 0;
+    col = 8u * own_piece();
+    bool up = false;   // the same for a wave's rows and for each i
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      bool up;
-      const int n = row_of(tid / 8 + 64 * i, up);
-      off[i] = (uint32_t)n * (uint32_t)(2 * w.k) + 2u * col;
-      first_up = up;   // the same for a wave's rows and for each i
-    }
-    const ExpertsView& m = __builtin_amdgcn_readfirstlane(first_up) ? u : w;
+    for (int i = 0; i < 4; ++i) off[i] = (uint32_t)row_of(tid / 8 + 64 * i, up) * (uint32_t)(2 * w.k) + 2u * col;
+    const ExpertsView& m = __builtin_amdgcn_readfirstlane((int)up) ? u : w;
     const int64_t rows = m.n - n0 < kBN ? m.n - n0 : kBN;
     r = rsrc_of(m.w + (int64_t)e * m.w_stride + n0 * 2 * m.k, (uint64_t)rows * 2 * m.k);
   }
-  __device__ __forceinline__ void load(int64_t k0, int64_t K) {
+  __device__ __forceinline__ void direct(int64_t k0, int64_t K, lds_char* to) const {
     const uint32_t ko = k0 + col < K ? (uint32_t)(2 * k0) : kOutside;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = bload16(r, off[i] + ko);
-  }
-  __device__ __forceinline__ void store(char* lds, int part) const {
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int i = 2 * part; i < 2 * part + 2; ++i)
-      *reinterpret_cast<uint4*>(lds + piece_at(tid / 8 + 64 * i, tid & 7)) = d[i];
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + 8192 * i, 16, (int)(off[i] + ko), 0, 0, 0);
   }
 };
 
@@ -85,9 +91,10 @@ struct Weights<kFormBf16> {
 template <>
 struct Weights<kFormMx4> {
   __amdgpu_buffer_rsrc_t r, rs;
+  static constexpr bool kDirect = false;
   uint32_t off, soff, col;
-  uint4 d;
-  uint32_t sc;
+  uint4 d[2];
+  uint32_t sc[2];
   template <typename RowOf>
   __device__ __forceinline__ void init(const ExpertsView& w, const ExpertsView& u, int e, int64_t n0, RowOf&& row_of) {
     const int tid = threadIdx.x;
@@ -101,16 +108,17 @@ struct Weights<kFormMx4> {
     r = rsrc_of(m.w + (int64_t)e * m.w_stride + n0 * (m.k / 2), (uint64_t)rows * (m.k / 2));
     rs = rsrc_of(m.scale + (int64_t)e * m.scale_stride + n0 * mx4_scale_stride(m.k), (uint64_t)rows * mx4_scale_stride(m.k));
   }
-  __device__ __forceinline__ void load(int64_t k0, int64_t K) {
+  __device__ __forceinline__ void load(int64_t k0, int64_t K, int set) {
     const bool in = k0 + col < K;
-    d = bload16(r, off + (in ? (uint32_t)(k0 / 2) : kOutside));
-    sc = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(soff + (in ? (uint32_t)(k0 / 32) : kOutside)), 0, 0);
+    d[set] = bload16(r, off + (in ? (uint32_t)(k0 / 2) : kOutside));
+    sc[set] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(soff + (in ? (uint32_t)(k0 / 32) : kOutside)), 0, 0);
   }
-  __device__ __forceinline__ void store(char* lds, int part) const {
+  __device__ __forceinline__ void store(char* lds, int part, int set) const {
     const int tid = threadIdx.x;
-    const float s = e8m0_float(sc & 255u);
-    const bool nan = (sc & 255u) == 255u;
-    const uint32_t q[4] = {d.x, d.y, d.z, d.w};
+    const uint32_t byte = sc[set] & 255u;
+    const float s = e8m0_float(byte);
+    const bool nan = byte == 255u;
+    const uint32_t q[4] = {d[set].x, d[set].y, d[set].z, d[set].w};
 #pragma unroll
     for (int i = 2 * part; i < 2 * part + 2; ++i) {
       uint4 v = mx4_unpack8(q[i], s);
@@ -125,56 +133,54 @@ struct Weights<kFormMx4> {
 // its data
 template <bool RUN>
 struct WeightsPal {
-  const ExpertEntry* t;
-  int64_t el[2];     // element of the piece at k = 0
-  uint4 s[2];
-  uint2 a[2], b[2];
-  uint32_t fw[2], rw[2], verb;
+  static constexpr bool kDirect = false;
+  ExpertEntry t;
+  uint32_t el[2];    // element of the piece at k = 0 (a matrix has fewer than 2^32)
+  uint4 s[2][2];
+  uint2 a[2][2], b[2][2];
+  uint32_t fw[2], rw[2], verb[2];
   template <typename RowOf>
   __device__ __forceinline__ void init(const ExpertsView& w, const ExpertsView& u, int e, int64_t n0, RowOf&& row_of) {
     const int tid = threadIdx.x;
-    int first_up = 0;
+    bool up = false;                 // 16 rows a wave, 128 apart: all gate or all up
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      bool up;
       int64_t n = n0 + row_of(tid / 4 + 128 * i, up);
-      n = n < w.n ? n : w.n - 1;   // rows past N are not stored
-      el[i] = n * w.k + 16 * (tid & 3);
-      first_up = up;               // 16 rows a wave, 128 apart: all gate or all up
+      n = n < w.n ? n : w.n - 1;     // rows past N are not stored
+      el[i] = (uint32_t)(n * w.k) + 16u * (tid & 3);
     }
-    t = (__builtin_amdgcn_readfirstlane(first_up) ? u : w).table + e;
-    verb = 0;
+    t = (__builtin_amdgcn_readfirstlane((int)up) ? u : w).table[e];
     flags(0, w.k);
   }
   __device__ __forceinline__ void flags(int64_t k0, int64_t K) {
-    const int64_t k = k0 < K ? k0 : 0;
+    const uint32_t k = k0 < K ? (uint32_t)k0 : 0u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      fw[i] = t->vflags[(uint64_t)(el[i] + k) >> 11];
-      rw[i] = t->vrank[(uint64_t)(el[i] + k) >> 11];
+      fw[i] = gload<uint32_t>(t.vflags + ((el[i] + k) >> 11));
+      rw[i] = gload<uint32_t>(t.vrank + ((el[i] + k) >> 11));
     }
   }
-  __device__ __forceinline__ void load(int64_t k0, int64_t K) {   // K % 64 == 0: a step is whole or absent
-    const int64_t k = k0 < K ? k0 : 0;
-    verb = 0;
+  __device__ __forceinline__ void load(int64_t k0, int64_t K, int set) {   // K % 64 == 0: a step is whole or absent
+    const uint32_t k = k0 < K ? (uint32_t)k0 : 0u;
+    verb[set] = 0;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint64_t x = (uint64_t)(el[i] + k), g = x >> 6;
-      s[i] = *reinterpret_cast<const uint4*>(t->sm + x);
+      const uint32_t x = el[i] + k, g = x >> 6;
+      s[set][i] = gload16(t.sm + x);
       const bool v = group_verbatim(fw[i], g);
-      const uint8_t* p = v ? t->vexp + (uint64_t)group_rank(fw[i], rw[i], g) * 64 + (x & 63) : t->pidx + x / 2;
-      a[i] = *reinterpret_cast<const uint2*>(p);
-      b[i] = *reinterpret_cast<const uint2*>(p + (v ? 8 : 0));
-      verb |= (v ? 1u : 0u) << i;
+      const uint8_t* p = v ? t.vexp + (uint64_t)group_rank(fw[i], rw[i], g) * 64 + (x & 63) : t.pidx + x / 2;
+      a[set][i] = gload8(p);
+      b[set][i] = gload8(p + (v ? 8 : 0));
+      verb[set] |= (v ? 1u : 0u) << i;
     }
     flags(k0 + kBK, K);
   }
-  __device__ __forceinline__ void store(char* lds, int part) const {
+  __device__ __forceinline__ void store(char* lds, int part, int set) const {
     const int tid = threadIdx.x, i = part;
-    uint4 e = pal16<RUN>(a[i].x, a[i].y, t->pal);
-    if ((verb >> i) & 1u) e = make_uint4(a[i].x, a[i].y, b[i].x, b[i].y);
+    uint4 e = pal16<RUN>(a[set][i].x, a[set][i].y, t.pal);
+    if ((verb[set] >> i) & 1u) e = make_uint4(a[set][i].x, a[set][i].y, b[set][i].x, b[set][i].y);
     uint32_t o[8];
-    rebuild16(s[i], e, o);
+    rebuild16(s[set][i], e, o);
     const int row = tid / 4 + 128 * i, c = 2 * (tid & 3);
     *reinterpret_cast<uint4*>(lds + piece_at(row, c)) = make_uint4(o[0], o[1], o[2], o[3]);
     *reinterpret_cast<uint4*>(lds + piece_at(row, c + 1)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -183,15 +189,19 @@ struct WeightsPal {
 template <> struct Weights<kFormPal> : WeightsPal<false> {};
 template <> struct Weights<kFormPalRun> : WeightsPal<true> {};
 
-template <int FORM, int BM, bool GATED>
+template <int FORM, int BM, bool GATED, bool BIG>
 __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsView vu, RaggedRows rr,
                                                       const uint16_t* __restrict__ x, void* __restrict__ y,
                                                       int ntiles) {
   constexpr int TM = BM / 64;                 // 32-row tiles of a wave; two column tiles
   constexpr int XP = BM / 64;                 // pieces of x a thread moves per step
+  using W = Weights<FORM>;
   constexpr int OUT = GATED ? 128 : 256;      // output columns of a block
-  constexpr int kStage = (BM + kBN) * 128;
-  extern __shared__ __attribute__((aligned(128))) char lds[];
+  // objects of their own rather than parts of one, so that the compiler sees that
+  // what is read from or stored to one does not wait for what travels into
+  // another
+  __shared__ __attribute__((aligned(128))) char xa[BM * 128], xb[BM * 128];
+  __shared__ __attribute__((aligned(128))) char wa[kBN * 128], wb[kBN * 128];
 
   Share sh;
   const int nt = find_tile(rr, vw.count, blockIdx.x, ntiles, BM, sh);
@@ -201,40 +211,40 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   const int64_t N = vw.n, K = vw.k;
   const int64_t n0 = (int64_t)nt * OUT;
 
-  // x: LDS rows tid / 8 + 64 i, piece tid % 8
-  const uint16_t* xp[XP];
-  uint32_t xok = 0;
+  // x: LDS rows tid / 8 + 64 i
+  const int xcol = 8 * own_piece();
+  uint32_t xo[XP];          // byte offset of the row
+  const uint16_t* xp[XP];   // BIG: its address, NULL for a row of zeros
 #pragma unroll
   for (int i = 0; i < XP; ++i) {
     const int b = tid / 8 + 64 * i;
     int64_t row = sh.first + (b < sh.count ? b : 0);
     if (rr.rows) row = rr.rows[row];
-    const bool ok = row >= 0 && row < rr.x_rows;   // outside: a row of zeros
-    xok |= (ok ? 1u : 0u) << i;
-    xp[i] = x + (ok ? row : 0) * K;
+    const bool in = row >= 0 && row < rr.x_rows;
+    xo[i] = in ? (uint32_t)(2 * (row * K + xcol)) : kOutside;
+    xp[i] = in ? x + row * K + xcol : nullptr;
   }
-  const int xcol = 8 * (tid & 7);
-  uint4 xd[XP];
-  bool xin = false;
-  auto load_x = [&](int64_t k0) __attribute__((always_inline)) {
-    xin = k0 + xcol < K;
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, BIG ? 0 : (uint64_t)rr.x_rows * 2 * K);
+  auto direct_x = [&](int64_t k0, lds_char* to) __attribute__((always_inline)) {
+    if constexpr (BIG) {
 #pragma unroll
-    for (int i = 0; i < XP; ++i) xd[i] = *reinterpret_cast<const uint4*>(xp[i] + (xin ? k0 + xcol : 0));
-  };
-  auto store_x = [&](char* buf) __attribute__((always_inline)) {
+      for (int i = 0; i < XP; ++i) {
+        const void* p = xp[i] && k0 + xcol < K ? (const void*)(xp[i] + k0) : (const void*)g_zero16;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, to + 8192 * i, 16, 0, 0);
+      }
+    } else {
+      const uint32_t ko = k0 + xcol < K ? (uint32_t)(2 * k0) : kOutside;
 #pragma unroll
-    for (int i = 0; i < XP; ++i) {
-      const bool ok = xin && ((xok >> i) & 1u);
-      uint4 v = xd[i];
-      v.x = ok ? v.x : 0u;
-      v.y = ok ? v.y : 0u;
-      v.z = ok ? v.z : 0u;
-      v.w = ok ? v.w : 0u;
-      *reinterpret_cast<uint4*>(buf + piece_at(tid / 8 + 64 * i, tid & 7)) = v;
+      for (int i = 0; i < XP; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to + 8192 * i, 16, (int)(xo[i] + ko), 0, 0, 0);
     }
   };
-
-  Weights<FORM> w;
+  // the step from k0, as far as it goes straight to LDS
+  W w;
+  auto direct = [&](int64_t k0, char* xbuf, char* wbuf) __attribute__((always_inline)) {
+    direct_x(k0, (lds_char*)(xbuf + wave * 1024));
+    if constexpr (W::kDirect) w.direct(k0, K, (lds_char*)(wbuf + wave * 1024));
+  };
   w.init(vw, vu, sh.expert, n0, [](int c, bool& up) __attribute__((always_inline)) {
     up = GATED && (c & 32);
     return GATED ? (c >> 6) * 32 + (c & 31) : c;
@@ -247,13 +257,21 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
   bf16x8_t fa[2][TM], fb[2][2];
   const int frow = lane & 31, fpiece = lane >> 5;
-  auto read = [&](const char* buf, int slice, int p) __attribute__((always_inline)) {
+  // Piece 2 slice + lane / 32 of row r lies at r * 128 + 16 ((lane / 32 ^ r / 2 % 8)
+  // ^ 2 slice): one base for x and one for the weights, the slice flipping
+  // two of its bits, a row tile 4096 bytes further.  (The empty asm makes a base
+  // opaque, or the compiler keeps all sixteen addresses of two buffers in
+  // registers, and spills.)
+  const uint32_t base_a = piece_at(wm * (BM / 2) + frow, fpiece), base_b = piece_at(wn * 64 + frow, fpiece);
+  auto read = [&](const char* xbuf, const char* wbuf, int slice, int p) __attribute__((always_inline)) {
+    uint32_t a = base_a, b = base_b;
+    asm volatile("" : "+v"(a), "+v"(b));
+    a ^= 32u * slice;
+    b ^= 32u * slice;
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-      fa[p][i] = *reinterpret_cast<const bf16x8_t*>(buf + piece_at(wm * (BM / 2) + 32 * i + frow, 2 * slice + fpiece));
+    for (int i = 0; i < TM; ++i) fa[p][i] = *reinterpret_cast<const bf16x8_t*>(xbuf + a + 4096 * i);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      fb[p][j] = *reinterpret_cast<const bf16x8_t*>(buf + BM * 128 + piece_at(wn * 64 + 32 * j + frow, 2 * slice + fpiece));
+    for (int j = 0; j < 2; ++j) fb[p][j] = *reinterpret_cast<const bf16x8_t*>(wbuf + b + 4096 * j);
   };
   auto mma = [&](int p) __attribute__((always_inline)) {
 #pragma unroll
@@ -264,46 +282,78 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   };
 
   const int steps = (int)((K + kBK - 1) / kBK);
-  load_x(0);
-  w.load(0, K);
-  store_x(lds);
-  w.store(lds + BM * 128, 0);
-  w.store(lds + BM * 128, 1);
-  load_x(kBK);
-  w.load(kBK, K);
+  auto store = [&](char* wbuf, int part, int set) __attribute__((always_inline)) {
+    if constexpr (!W::kDirect) w.store(wbuf, part, set);
+  };
+  auto load = [&](int64_t k0, int set) __attribute__((always_inline)) {
+    if constexpr (!W::kDirect) w.load(k0, K, set);
+  };
+  direct(0, xa, wa);
+  load(0, 0);
+  load(kBK, 1);
+  store(wa, 0, 0);
+  store(wa, 1, 0);
+  direct(kBK, xb, wb);
+  load(2 * kBK, 0);
+  asm volatile("" : : "s"(y));   // its scalar load ends here: pending, it would make the loop's first LDS wait a full one
+  __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
-  if (wm * (BM / 2) < sh.count) {
-    read(lds, 0, 0);
-    for (int s = 0; s < steps; ++s) {
-      char* cur = lds + (s & 1) * kStage;
-      char* nxt = lds + ((s + 1) & 1) * kStage;
-      read(cur, 1, 1);
-      store_x(nxt);
+  const bool active = wm * (BM / 2) < sh.count;
+  if (active) read(xa, wa, 0, 0);
+  // two steps an iteration, so that buffers and register sets are constants;
+  // step s of parity q finds its data in xcur and wcur, that of s + 1 in set
+  // 1 - q and on its way to xnxt and wnxt
+  auto step = [&](int s, char* xcur, char* wcur, char* xnxt, char* wnxt, auto Q, auto Active) __attribute__((always_inline)) {
+    constexpr int q = decltype(Q)::value;
+    constexpr bool kActive = decltype(Active)::value;
+    if constexpr (kActive) {
+      // (the scheduling barriers keep each slice's reads ahead of the MFMAs of
+      // the slice before, which cover their latency)
+      read(xcur, wcur, 1, 1);
+      __builtin_amdgcn_sched_barrier(0);
+      store(wnxt, 0, 1 - q);
       mma(0);
-      read(cur, 2, 0);
-      w.store(nxt + BM * 128, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      read(xcur, wcur, 2, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      store(wnxt, 1, 1 - q);
       mma(1);
-      read(cur, 3, 1);
-      w.store(nxt + BM * 128, 1);
-      load_x((int64_t)kBK * (s + 2));
-      w.load((int64_t)kBK * (s + 2), K);
+      __builtin_amdgcn_sched_barrier(0);
+      read(xcur, wcur, 3, 1);
+      __builtin_amdgcn_sched_barrier(0);
       mma(0);
-      __syncthreads();
-      read(nxt, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    } else {   // moves data for the other waves
+      store(wnxt, 0, 1 - q);
+      store(wnxt, 1, 1 - q);
+    }
+    // this thread's part of step s + 1 has landed, and this wave has read all
+    // of step s: after the barrier both hold for the block
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    direct((int64_t)kBK * (s + 2), xcur, wcur);
+    load((int64_t)kBK * (s + 3), 1 - q);
+    if constexpr (kActive) {
+      read(xnxt, wnxt, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
       mma(1);
+      __builtin_amdgcn_sched_barrier(0);
     }
-  } else {
-    for (int s = 0; s < steps; ++s) {   // moves data for the other waves
-      char* nxt = lds + ((s + 1) & 1) * kStage;
-      store_x(nxt);
-      w.store(nxt + BM * 128, 0);
-      w.store(nxt + BM * 128, 1);
-      load_x((int64_t)kBK * (s + 2));
-      w.load((int64_t)kBK * (s + 2), K);
-      __syncthreads();
+  };
+  auto run = [&](auto Active) __attribute__((always_inline)) {
+    int s = 0;
+    for (; s + 1 < steps; s += 2) {
+      step(s, xa, wa, xb, wb, std::integral_constant<int, 0>{}, Active);
+      step(s + 1, xb, wb, xa, wa, std::integral_constant<int, 1>{}, Active);
     }
+    if (s < steps) step(s, xa, wa, xb, wb, std::integral_constant<int, 0>{}, Active);
+  };
+  // (a wave takes one of the two loops as a whole; both pass the same barriers)
+  if (!active) {
+    run(std::false_type{});
     return;
   }
+  run(std::true_type{});
 
   // D of the MFMA: lane l, register r: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
 #pragma unroll
@@ -326,23 +376,24 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
     }
 }
 
-template <int FORM, int BM, bool GATED>
+// x up to here goes through a buffer resource (an offset past it plus a K tail's
+// kOutside stays below 2^32)
+constexpr int64_t kBigBytes = kOutside;
+
+template <int FORM, int BM, bool GATED, bool BIG = false>
 hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
-  constexpr int bytes = 2 * (BM + kBN) * 128;
-  const auto k = k_experts_tile<FORM, BM, GATED>;
-  const hipError_t e = allow_dynamic_lds(reinterpret_cast<const void*>(k), bytes);
-  if (e != hipSuccess) return e;
   const int64_t out = GATED ? 128 : 256, ntiles = (c.w.n + out - 1) / out;
   // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
   const int64_t tiles = max_chunks(c.r.slots, c.w.count, BM, c.r.offsets != nullptr) * ntiles;
   const int64_t grid = (tiles + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorNotSupported;
-  hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(kNT), bytes, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles);
+  hipLaunchKernelGGL((k_experts_tile<FORM, BM, GATED, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles);
   return hipGetLastError();
 }
 
 template <int FORM, bool GATED>
 hipError_t launch_rows(const ExpertsCall& c, int rows, hipStream_t s) {
+  if (c.r.x_rows * 2 * c.w.k > kBigBytes) return launch_one<FORM, 256, GATED, true>(c, s);
   if (rows <= 64) return launch_one<FORM, 64, GATED>(c, s);
   if (rows <= 128) return launch_one<FORM, 128, GATED>(c, s);
   return launch_one<FORM, 256, GATED>(c, s);
