@@ -23,6 +23,23 @@ namespace {
 
 __device__ __forceinline__ uint32_t word4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 
+// Every load goes through a buffer resource (or, for a UWF1 expert's
+// exponents, a selected pointer): what must count as nothing -- weights and
+// x beyond K, rows beyond N, slots beyond the share, row indices outside x --
+// has an offset past the resource's end and reads zero, so the loop holds no
+// selects.
+constexpr uint32_t kOutside = 0x7FFF0000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t byte) {
+  const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)byte, 0, 0);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+__device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
+
 // units of 32 weights a lane takes of a window, and the window's width
 template <int FORM> constexpr int units() { return FORM == kFormMx4 ? 2 : 1; }
 template <int FORM> constexpr int window() { return 128 * units<FORM>(); }
@@ -33,21 +50,30 @@ __device__ __forceinline__ int k_off(int u, int m, int g) {
   return FORM == kFormBf16 ? 32 * m + 8 * g : 32 * units<FORM>() * g + 32 * u + 8 * m;
 }
 
-// one expert's matrix
+// A block's rows [n0, n0 + rows) of one expert's matrix.
+template <int FORM>
 struct Mat {
-  const uint8_t* w;
-  const uint8_t* scale;
-  ExpertEntry t;
+  __amdgpu_buffer_rsrc_t w, scale;   // BF16, MXFP4: from row n0
+  ExpertEntry t;                     // UWF1
+  uint32_t el0, el_end;              // ... its elements [n0 K, (n0 + rows) K)
 };
 
 template <int FORM>
-__device__ __forceinline__ Mat matrix_of(const ExpertsView& v, int e) {
-  Mat m{};
+__device__ __forceinline__ Mat<FORM> matrix_of(const ExpertsView& v, int e, int64_t n0, int span) {
+  Mat<FORM> m{};
+  const int64_t rows = v.n - n0 < span ? v.n - n0 : span;
   if constexpr (form_is_pal(FORM)) {
     m.t = v.table[e];
+    m.el0 = (uint32_t)(n0 * v.k);
+    m.el_end = (uint32_t)((n0 + rows) * v.k);
+    m.w = rsrc_of(m.t.sm + n0 * v.k, (uint64_t)(rows * v.k));
   } else {
-    m.w = v.w + (int64_t)e * v.w_stride;
-    if constexpr (FORM == kFormMx4) m.scale = v.scale + (int64_t)e * v.scale_stride;
+    const int64_t bytes = FORM == kFormBf16 ? 2 * v.k : v.k / 2;
+    m.w = rsrc_of(v.w + (int64_t)e * v.w_stride + n0 * bytes, (uint64_t)(rows * bytes));
+    if constexpr (FORM == kFormMx4) {
+      const int64_t st = mx4_scale_stride(v.k);
+      m.scale = rsrc_of(v.scale + (int64_t)e * v.scale_stride + n0 * st, (uint64_t)(rows * st));
+    }
   }
   return m;
 }
@@ -66,59 +92,61 @@ struct Flags {
   uint32_t fw, rw;
 };
 
+// row: from n0
 template <int FORM>
-__device__ __forceinline__ void load_flags(const Mat& m, int64_t row, int64_t K, int64_t k, bool ok, Flags& f) {
+__device__ __forceinline__ void load_flags(const Mat<FORM>& m, int row, int K, int k, Flags& f) {
   if constexpr (form_is_pal(FORM)) {
-    const uint64_t w = ok ? (uint64_t)(row * K + k) >> 11 : 0;
+    const uint32_t el = m.el0 + (uint32_t)row * (uint32_t)K + (uint32_t)k;
+    const uint32_t w = (k < K && el < m.el_end ? el : m.el0) >> 11;
     f.fw = gload<uint32_t>(m.t.vflags + w);
     f.rw = gload<uint32_t>(m.t.vrank + w);
   }
 }
 
-// row: inside the matrix; k0: the window's start; weights at k >= K are not
-// loaded (the row's first are, and are zeroed when unpacked)
+// k0: the window's start (K or more: nothing)
 template <int FORM>
-__device__ __forceinline__ void load_raw(const Mat& m, int64_t row, int64_t K, int64_t k0, int g, const Flags& fl, Raw& r) {
+__device__ __forceinline__ void load_raw(const Mat<FORM>& m, int row, int K, int k0, int g, const Flags& fl, Raw& r) {
   if constexpr (FORM == kFormBf16) {
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(m.w) + row * K;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int64_t k = k0 + k_off<FORM>(0, i, g);
-      r.d[i] = *reinterpret_cast<const uint4*>(p + (k < K ? k : 0));
+      const int k = k0 + k_off<FORM>(0, i, g);
+      r.d[i] = bload16(m.w, k < K ? (uint32_t)(row * K + k) * 2u : kOutside);
     }
   } else if constexpr (FORM == kFormMx4) {
-    const uint8_t* p = m.w + row * (K / 2);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int64_t k = k0 + k_off<FORM>(u, 0, g);
-      r.d[u] = *reinterpret_cast<const uint4*>(p + (k < K ? k : 0) / 2);
+      const int k = k0 + k_off<FORM>(u, 0, g);
+      r.d[u] = bload16(m.w, k < K ? (uint32_t)(row * (K / 2) + k / 2) : kOutside);
     }
-    const int64_t k = k0 + k_off<FORM>(0, 0, g);   // a multiple of 64: the pair of scales is aligned
-    r.f = *reinterpret_cast<const uint16_t*>(m.scale + row * mx4_scale_stride(K) + (k < K ? k : 0) / 32);
+    const int k = k0 + k_off<FORM>(0, 0, g);   // a multiple of 64: the pair of scales is aligned
+    r.f = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
+        m.scale, (int)(k < K ? (uint32_t)(row * (int)mx4_scale_stride(K) + k / 32) : kOutside), 0, 0);
   } else {
-    const int64_t k = k0 + k_off<FORM>(0, 0, g);
-    const uint64_t el = (uint64_t)(row * K + (k < K ? k : 0));
-    r.d[0] = gload16(m.t.sm + el);
-    r.d[1] = gload16(m.t.sm + el + 16);
-    const uint64_t grp = el >> 6;
-    const bool v = k < K && group_verbatim(fl.fw, grp);
-    const uint8_t* p = v ? m.t.vexp + (uint64_t)group_rank(fl.fw, fl.rw, grp) * 64 + (el & 63) : m.t.pidx + el / 2;
+    const int k = k0 + k_off<FORM>(0, 0, g);
+    const uint32_t at = (uint32_t)row * (uint32_t)K + (uint32_t)k, el = m.el0 + at;
+    const bool in = k < K && el < m.el_end;
+    r.d[0] = bload16(m.w, in ? at : kOutside);
+    r.d[1] = bload16(m.w, in ? at + 16u : kOutside);
+    const uint32_t grp = el >> 6;
+    const bool v = in && group_verbatim(fl.fw, grp);
+    const uint32_t vo = group_rank(fl.fw, fl.rw, grp) * 64u + (el & 63u);
+    // outside the matrix the exponents are zeros, as of a verbatim group
+    const uint8_t* p = v ? m.t.vexp + vo : in ? m.t.pidx + el / 2 : reinterpret_cast<const uint8_t*>(g_zero16);
     r.d[2] = gload16(p);
-    if (v) r.d[3] = gload16(p + 16);
-    r.f = v ? 1u : 0u;
+    r.d[3] = make_uint4(0u, 0u, 0u, 0u);
+    if (v) r.d[3] = gload16(p + 16);   // (rarely any lane: a fourth load for all would cost 10 %)
+    r.f = v || !in ? 1u : 0u;
   }
 }
 
-// A operand of MFMA (u, m)
+// A operand of MFMA (u, m); scale: of unit u (MXFP4)
 template <int FORM>
-__device__ __forceinline__ bf16x8_t a_frag(const Mat& mt, const Raw& r, int u, int m, bool ok) {
+__device__ __forceinline__ bf16x8_t a_frag(const Mat<FORM>& mt, const Raw& r, float scale, int u, int m) {
   uint4 o;
   if constexpr (FORM == kFormBf16) {
     o = r.d[m];
   } else if constexpr (FORM == kFormMx4) {
-    o = mx4_unpack8(word4(r.d[u], m), e8m0_float((r.f >> (8 * u)) & 255u));
-    // (scale 255 is NaN, whatever the element)
-    if (((r.f >> (8 * u)) & 255u) == 255u) o = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+    o = mx4_unpack8(word4(r.d[u], m), scale);
   } else {
     const int wi = 2 * (m & 1);
     uint32_t e0, e1;
@@ -128,10 +156,6 @@ __device__ __forceinline__ bf16x8_t a_frag(const Mat& mt, const Raw& r, int u, i
     rebuild4(word4(r.d[m >> 1], wi), e0, o.x, o.y);
     rebuild4(word4(r.d[m >> 1], wi + 1), e1, o.z, o.w);
   }
-  o.x = ok ? o.x : 0u;
-  o.y = ok ? o.y : 0u;
-  o.z = ok ? o.z : 0u;
-  o.w = ok ? o.w : 0u;
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
@@ -148,84 +172,78 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   if (sh.count == 0) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i16 = lane & 15, g = lane >> 4;
-  const int64_t N = vw.n, K = vw.k;
+  const int64_t N = vw.n;
+  const int K = (int)vw.k;
   const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)ntiles) * (16 * RT);
-  const Mat mw = matrix_of<FORM>(vw, sh.expert);
-  Mat mu = mw;
-  if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert);
-  auto mat = [&](int t) __attribute__((always_inline)) -> const Mat& { return GATED && t >= RT ? mu : mw; };
+  const Mat<FORM> mw = matrix_of<FORM>(vw, sh.expert, n0, 16 * RT);
+  Mat<FORM> mu = mw;
+  if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert, n0, 16 * RT);
+  auto mat = [&](int t) __attribute__((always_inline)) -> const Mat<FORM>& { return GATED && t >= RT ? mu : mw; };
+  auto row_of = [&](int t) __attribute__((always_inline)) { return 16 * (t % RT) + i16; };
 
-  // x rows of this lane's slots; slots past the share and rows outside x read
-  // row 0 and are zeroed
-  const uint16_t* xrow[Q];
-  bool xok[Q];
+  // x rows of this lane's slots
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
+  uint32_t xrow[Q];
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const int b = 16 * q + i16;
     int64_t row = sh.first + (b < sh.count ? b : 0);
     if (rr.rows) row = rr.rows[row];
-    xok[q] = b < sh.count && row >= 0 && row < rr.x_rows;
-    xrow[q] = x + (xok[q] ? row : 0) * K;
-  }
-  // weight rows of this lane, clamped into the matrix (those past it are not stored)
-  int64_t wrow[R];
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const int64_t n = n0 + 16 * (t % RT) + i16;
-    wrow[t] = n < N ? n : N - 1;
+    xrow[q] = b < sh.count && row >= 0 && row < rr.x_rows ? (uint32_t)(row * K) * 2u : kOutside;
   }
 
-  const int nwin = (int)((K + W - 1) / W);
+  const int nwin = (K + W - 1) / W;
   f32x4_t acc[R][Q];
 #pragma unroll
   for (int t = 0; t < R; ++t)
 #pragma unroll
     for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint32_t top[R] = {};   // MXFP4: the largest scale byte of the lane's rows
 
   struct Win {
     Raw r[R];
     uint4 xv[Q][4 * U];
   };
   auto flags = [&](int j, Flags (&f)[R]) __attribute__((always_inline)) {
-    const int64_t k = (int64_t)W * j + k_off<FORM>(0, 0, g);
 #pragma unroll
-    for (int t = 0; t < R; ++t) load_flags<FORM>(mat(t), wrow[t], K, k, j < nwin && k < K, f[t]);
+    for (int t = 0; t < R; ++t) load_flags<FORM>(mat(t), row_of(t), K, W * j + k_off<FORM>(0, 0, g), f[t]);
   };
+  // windows past the last (whole rounds of four) lie past K and load zeros
   auto load = [&](int j, const Flags (&f)[R], Win& w) __attribute__((always_inline)) {
-    const int64_t k0 = j < nwin ? (int64_t)W * j : 0;
+    const int k0 = W * j;
 #pragma unroll
-    for (int t = 0; t < R; ++t) load_raw<FORM>(mat(t), wrow[t], K, k0, g, f[t], w.r[t]);
+    for (int t = 0; t < R; ++t) load_raw<FORM>(mat(t), row_of(t), K, k0, g, f[t], w.r[t]);
 #pragma unroll
     for (int q = 0; q < Q; ++q)
 #pragma unroll
       for (int i = 0; i < 4 * U; ++i) {
-        const int64_t k = k0 + k_off<FORM>(i / 4, i % 4, g);
-        w.xv[q][i] = *reinterpret_cast<const uint4*>(xrow[q] + (k < K ? k : 0));
+        const int k = k0 + k_off<FORM>(i / 4, i % 4, g);
+        w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
       }
   };
   auto compute = [&](int j, const Win& w) __attribute__((always_inline)) {
-    const int64_t k0 = (int64_t)W * j;
-#pragma unroll
-    for (int i = 0; i < 4 * U; ++i) {
-      const bool ok = j < nwin && k0 + k_off<FORM>(i / 4, i % 4, g) < K;
-      bf16x8_t b[Q];
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        uint4 v = w.xv[q][i];
-        const bool in = ok && xok[q];
-        v.x = in ? v.x : 0u;
-        v.y = in ? v.y : 0u;
-        v.z = in ? v.z : 0u;
-        v.w = in ? v.w : 0u;
-        b[q] = __builtin_bit_cast(bf16x8_t, v);
-      }
+    float scale[R][U] = {};
+    if constexpr (FORM == kFormMx4) {
+      // (the second of a lane's two blocks may lie past K: its scale is padding)
+      const bool second = W * j + k_off<FORM>(1, 0, g) < K;
 #pragma unroll
       for (int t = 0; t < R; ++t) {
-        const bf16x8_t a = a_frag<FORM>(mat(t), w.r[t], i / 4, i % 4, ok);
-#pragma unroll
-        for (int q = 0; q < Q; ++q) acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b[q], acc[t][q], 0, 0, 0);
+        const uint32_t lo = w.r[t].f & 255u, hi = second ? w.r[t].f >> 8 : 0u;
+        scale[t][0] = e8m0_float(lo);
+        scale[t][1] = e8m0_float(hi);
+        top[t] = max(top[t], max(lo, hi));
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4 * U; ++i)
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const bf16x8_t a = a_frag<FORM>(mat(t), w.r[t], scale[t][i / 4], i / 4, i % 4);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, w.xv[q][i]), acc[t][q],
+                                                              0, 0, 0);
+      }
   };
 
   Win wa, wb;
@@ -241,6 +259,18 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
     load(j + 8, fa, wa);
     flags(j + 16, fa);
     compute(j + 4, wb);
+  }
+  if constexpr (FORM == kFormMx4) {
+    // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      const uint32_t n = top[t] == 255u ? 0x7FC07FC0u : 0u;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(n, n, n, n)),
+                                                            __builtin_bit_cast(bf16x8_t, zero), acc[t][q], 0, 0, 0);
+    }
   }
 
   // the waves' sums, added in wave order.  D of the MFMA: lane l holds output
@@ -289,53 +319,77 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   }
 }
 
-template <int FORM, int Q>
-hipError_t launch_q(const ExpertsCall& c, hipStream_t s) {
-  const int64_t chunks = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr);
-  const int64_t ntiles = (c.w.n + (c.gated ? 15 : 31)) / (c.gated ? 16 : 32);
-  if (chunks * ntiles > INT32_MAX) return hipErrorNotSupported;
-  const dim3 grid((unsigned)(chunks * ntiles));
-  if (c.gated)
-    hipLaunchKernelGGL((k_experts_rows<FORM, 2, Q, true>), grid, dim3(256), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles);
-  else
-    hipLaunchKernelGGL((k_experts_rows<FORM, 2, Q, false>), grid, dim3(256), 0, s, c.w, c.w, c.r, c.x, c.y, (int)ntiles);
+template <int FORM, int R, int Q, bool GATED>
+hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
+  const int64_t rows = 16 * (GATED ? R / 2 : R), ntiles = (c.w.n + rows - 1) / rows;
+  const int64_t grid = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr) * ntiles;
+  if (grid > INT32_MAX) return hipErrorNotSupported;
+  hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,
+                     c.y, (int)ntiles);
   return hipGetLastError();
 }
 
+// MXFP4 weights are few bytes a tile beside x's: four tiles a wave share each x
+// fragment.  The other forms do better with two and more waves (one token,
+// two of eight experts, us with 2 / 4: BF16 84 / 115, UWF1 70 / 75, MXFP4 37 / 36; MXFP4
+// layer of 37 tokens over 32 experts 158 / 128).
+template <int FORM, int Q, bool GATED>
+hipError_t launch_r(const ExpertsCall& c, hipStream_t s) {
+  return launch_one<FORM, FORM == kFormMx4 ? 4 : 2, Q, GATED>(c, s);
+}
+
+// Two groups of 16 slots where experts have more than 16 rows as a rule and the
+// blocks still fill the chip (MXFP4 14336x4096, 32 rows: 22.4 / 18.8 us; 5001x8224, 45 rows,
+// half the blocks: 23 / 34 us).
+template <int FORM, bool GATED>
+hipError_t launch_form(const ExpertsCall& c, int64_t avg, hipStream_t s) {
+  const int64_t rows = 16 * (FORM == kFormMx4 ? 4 : 2) / (GATED ? 2 : 1);
+  const int64_t blocks =
+      (c.w.n + rows - 1) / rows * max_chunks(c.r.slots, c.w.count, 32, c.r.offsets != nullptr);
+  if (avg <= (c.r.offsets ? 12 : 16) || blocks < device_cus()) return launch_r<FORM, 1, GATED>(c, s);
+  return launch_r<FORM, 2, GATED>(c, s);
+}
+
 template <int FORM>
-hipError_t launch_form(const ExpertsCall& c, hipStream_t s) {
-  const int64_t e = c.r.offsets ? c.w.count : 1;
-  const int64_t avg = (c.r.slots + e - 1) / e;
-  if (avg <= 16) return launch_q<FORM, 1>(c, s);
-  if (avg <= 32) return launch_q<FORM, 2>(c, s);
-  return launch_q<FORM, 4>(c, s);
+hipError_t launch_gated(const ExpertsCall& c, int64_t avg, hipStream_t s) {
+  return c.gated ? launch_form<FORM, true>(c, avg, s) : launch_form<FORM, false>(c, avg, s);
 }
 
 }  // namespace
 
 hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
+  const int64_t e = c.r.offsets ? c.w.count : 1, avg = (c.r.slots + e - 1) / e;
   switch (c.w.form) {
-    case kFormBf16: return launch_form<kFormBf16>(c, s);
-    case kFormPal: return launch_form<kFormPal>(c, s);
-    case kFormPalRun: return launch_form<kFormPalRun>(c, s);
-    default: return launch_form<kFormMx4>(c, s);
+    case kFormBf16: return launch_gated<kFormBf16>(c, avg, s);
+    case kFormPal: return launch_gated<kFormPal>(c, avg, s);
+    case kFormPalRun: return launch_gated<kFormPalRun>(c, avg, s);
+    default: return launch_gated<kFormMx4>(c, avg, s);
   }
 }
 
 // Which kernel: by the rows an expert has on average if every slot is used
-// (the counts themselves are on the device).  The register-fed kernel streams
-// weights for few rows; the LDS tiles rebuild and read each weight once per
-// tile of 64, 128 or 256 rows.  Measured (us, register-fed / 64 / 128 / 256):
-//   BF16, 16 experts 2048x2048, 64 rows: 69 / 42 / 44 / 53
+// (the counts themselves are on the device) and the blocks that makes.  The
+// register-fed kernel streams weights for few rows; the LDS tiles rebuild and
+// read each weight once per tile of 64, 128 or 256 rows, but need a block on
+// every CU: with fewer, smaller tiles, and below three quarters of the CUs the
+// register-fed kernel again, up to the rows where its reloading of weights
+// costs more.  Measured (us, register-fed / 64 / 128 / 256):
+//   BF16, 32 experts 2048x2048, 16 rows: 73 / 70 / 72 / 74
 //   BF16 gated, 64 experts 1408x2048, 512 rows: 1985 / 581 / 529 / 450
-//   BF16 layer, 64 experts 1408x2048, 281 rows: 1902 / 601 / 593 / 539
 //   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1438 / 772 / 495 / 409
-//   UWF1, 32 experts 2048x4096, 3 rows: 78 / 106 / 110 / 135
+//   UWF1, 32 experts 2048x4096, 3 rows: 75 / 106 / 110 / 135
+//   MXFP4 14336x4096: 64 rows 35 / 52 / 59 / 69, 128 rows 66 / 53 / 63 / 73
+//   MXFP4, few tiles: 5001x8224, 200 rows 84 / 109 / 125 / 179; 4096x4096, 256 rows 34 / 52 / 63 / 95
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
   const int64_t e = c.r.offsets ? c.w.count : 1;
   const int64_t avg = (c.r.slots + e - 1) / e;
-  if (avg <= 8) return launch_experts_rows(c, s);
-  return launch_experts_tile(c, avg <= 96 ? 64 : avg <= 160 ? 128 : 256, s);
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_experts_tile(c, 256, s);   // x past 2 GiB: by pointers
+  const int64_t cus = device_cus(), ntiles = (c.w.n + (c.gated ? 127 : 255)) / (c.gated ? 128 : 256);
+  auto blocks = [&](int rows) { return ntiles * max_chunks(c.r.slots, c.w.count, rows, c.r.offsets != nullptr); };
+  int rows = avg <= 96 ? 64 : avg <= 160 ? 128 : 256;
+  while (rows > 64 && blocks(rows) < cus) rows /= 2;
+  if (avg <= 12 || (avg <= 256 && blocks(rows) < cus * 3 / 4)) return launch_experts_rows(c, s);
+  return launch_experts_tile(c, rows, s);
 }
 
 }  // namespace uw

@@ -231,9 +231,11 @@ hipError_t launch_bm(const uint8_t* we, const uint8_t* ws, int64_t n, int64_t k,
 
 hipError_t launch_mx4_tile(const uint8_t* we, const uint8_t* ws, int64_t n, int64_t k, const uint8_t* xe,
                            const uint8_t* xs, int64_t batch, float* y, hipStream_t s) {
-  if (batch <= 64) return launch_bm<64>(we, ws, n, k, xe, xs, batch, y, s);
-  if (batch <= 128) return launch_bm<128>(we, ws, n, k, xe, xs, batch, y, s);
-  return launch_bm<256>(we, ws, n, k, xe, xs, batch, y, s);
+  // the tallest tile that still gives every CU a block
+  const int64_t cus = device_cus(), ntiles = (n + kBN - 1) / kBN;
+  if (batch > 128 && (batch + 255) / 256 * ntiles >= cus) return launch_bm<256>(we, ws, n, k, xe, xs, batch, y, s);
+  if (batch > 64 && (batch + 127) / 128 * ntiles >= cus) return launch_bm<128>(we, ws, n, k, xe, xs, batch, y, s);
+  return launch_bm<64>(we, ws, n, k, xe, xs, batch, y, s);
 }
 
 }  // namespace uw

@@ -12,18 +12,19 @@
 // topk rounds is a lane-local search and a butterfly of lane permutes over
 // (key, index), so nothing leaves registers.
 //
-// Plan.  A stable counting sort of the (token, choice) pairs by expert.  Up to
-// 1024 pairs one block does everything; beyond, each block counts its tokens'
-// experts, and a second launch places its pairs behind the counts of all
-// blocks before it.  No atomics decide an order: the rank of a pair among its
-// wave's equals comes from ballots, the waves' counts are added in wave order.
+// Plan.  A stable counting sort of the (token, choice) pairs by expert.  Up to 64
+// pairs one wave does everything, without a barrier, up to 1024 one block;
+// beyond, each block counts its tokens' experts, and a second launch places
+// its pairs behind the counts of all blocks before it.  No atomics decide an
+// order: the rank of a pair among its wave's equals comes from ballots, the
+// waves' counts are added in wave order.
 #include "experts.h"
 
 namespace uw {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kOneBlockPairs = 1024;
+constexpr int kOneBlockPairs = 1024, kOneWavePairs = 64;
 
 // larger floats have larger keys; 0 = not selectable
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -140,10 +141,10 @@ __device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live,
 
 // The block's tokens [t0, t1): ids and weights to memory, and expert(pair)
 // for each of their pairs through `each` (pair counted from t0's first).
-template <int L, int NV, typename F>
+template <int L, int NV, int NT = kThreads, typename F>
 __device__ __forceinline__ void choose_range(const RouteCall& c, int64_t t0, int64_t t1, F&& each) {
   const int l = threadIdx.x % L, group = threadIdx.x / L;
-  for (int64_t t = t0; t < t1; t += kThreads / L) {
+  for (int64_t t = t0; t < t1; t += NT / L) {
     const int64_t mine = t + group;
     const bool live = mine < t1;
     int id;
@@ -226,6 +227,51 @@ __device__ __forceinline__ int place_chunk(PlanLds& s, int experts, int e) {
   return slot;
 }
 
+// Everything in one wave (tokens * topk <= 64): the wave's LDS operations are
+// in order, so a fence for the compiler is all that stands between them.
+template <int L, int NV>
+__global__ __launch_bounds__(64) void k_route_wave(RouteCall c) {
+  __shared__ int32_t ids[64], first[kMaxExperts];
+  const int pairs = (int)(c.tokens * c.topk), lane = threadIdx.x;
+  const int per = (c.experts + 63) / 64;   // experts of a lane, consecutive
+  for (int i = lane; i < c.experts; i += 64) first[i] = 0;
+  if (c.logits) {
+    choose_range<L, NV, 64>(c, 0, c.tokens, [&](int64_t p, int id) { ids[p] = id; });
+  } else if (lane < pairs) {
+    ids[lane] = valid_id(c.ids_in[lane], c.experts);
+  }
+  __builtin_amdgcn_wave_barrier();
+  const int e = lane < pairs ? ids[lane] : -1;
+  int rank, same;
+  wave_rank(e, rank, same);
+  if (e >= 0 && rank == 0) first[e] = same;
+  __builtin_amdgcn_wave_barrier();
+  int mine = 0;
+  for (int i = 0; i < per; ++i) mine += lane * per + i < c.experts ? first[lane * per + i] : 0;
+  int sum = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(sum, d);
+    sum += lane >= d ? up : 0;
+  }
+  int at = sum - mine;
+  for (int i = 0; i < per; ++i) {
+    const int x = lane * per + i;
+    if (x >= c.experts) break;
+    const int n = first[x];
+    first[x] = at;
+    c.offsets[x] = at;
+    at += n;
+  }
+  if (lane == 63) c.offsets[c.experts] = sum;
+  __builtin_amdgcn_wave_barrier();
+  if (lane < pairs) {
+    const int slot = e >= 0 ? first[e] + rank : -1;
+    c.slots[lane] = slot;
+    if (slot >= 0) c.rows[slot] = lane / c.topk;
+  }
+}
+
 // Everything in one block (tokens * topk <= 1024).
 template <int L, int NV>
 __global__ __launch_bounds__(kThreads) void k_route_one(RouteCall c) {
@@ -283,13 +329,34 @@ __global__ __launch_bounds__(kThreads) void k_route_count(RouteCall c, int64_t p
 __global__ __launch_bounds__(kThreads) void k_route_place(RouteCall c, int64_t per) {
   __shared__ PlanLds s;
   const int tid = threadIdx.x;
-  // thread e: its expert's pairs in the blocks before this one, and in all
+  // its expert's pairs in the blocks before this one, and in all: the threads
+  // form rows of `experts`, each row adding every rows-th block's counts, eight
+  // loads in flight (one row and one load at a time this took 30 us)
+  __shared__ int32_t part[2][kThreads];
+  const int rows = kThreads / c.experts, row = tid / c.experts, col = tid - row * c.experts;
+  const int nb = (int)gridDim.x, me = (int)blockIdx.x;
   int before = 0, all = 0;
+  if (row < rows) {
+    const int32_t* h = c.hist + col;
+    for (int b0 = row; b0 < nb; b0 += 8 * rows) {
+      int v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = b0 + i * rows < nb ? h[(int64_t)(b0 + i * rows) * c.experts] : 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        before += b0 + i * rows < me ? v[i] : 0;
+        all += v[i];
+      }
+    }
+  }
+  part[0][tid] = before;
+  part[1][tid] = all;
+  __syncthreads();
+  before = all = 0;
   if (tid < c.experts)
-    for (int b = 0; b < (int)gridDim.x; ++b) {
-      const int h = c.hist[(int64_t)b * c.experts + tid];
-      before += b < (int)blockIdx.x ? h : 0;
-      all += h;
+    for (int r = 0; r < rows; ++r) {
+      before += part[0][r * c.experts + tid];
+      all += part[1][r * c.experts + tid];
     }
   int total;
   const int first = block_prefix(all, s.wsum, total);
@@ -312,15 +379,19 @@ __global__ __launch_bounds__(kThreads) void k_route_place(RouteCall c, int64_t p
   }
 }
 
-// no more than 128 blocks: each reads every block's counts
+// no more than 256 blocks: each reads every block's counts
 int64_t tokens_per_block(int64_t tokens) {
-  const int64_t per = (tokens + 127) / 128;
+  const int64_t per = (tokens + 255) / 256;
   return per < 64 ? 64 : per;
 }
 
 template <int L, int NV>
 hipError_t launch_nv(const RouteCall& c, hipStream_t s) {
   const int blocks = route_blocks(c.tokens, c.topk);
+  if (c.tokens * c.topk <= kOneWavePairs) {
+    hipLaunchKernelGGL((k_route_wave<L, NV>), dim3(1), dim3(64), 0, s, c);
+    return hipGetLastError();
+  }
   if (blocks == 1) {
     hipLaunchKernelGGL((k_route_one<L, NV>), dim3(1), dim3(kThreads), 0, s, c);
     return hipGetLastError();
@@ -367,6 +438,7 @@ hipError_t launch_route(const RouteCall& c, hipStream_t s) {
   // lanes a token times keys a lane cover the experts
   if (c.experts <= 64) return launch_nv<16, 4>(c, s);
   if (c.experts <= 128) return launch_nv<16, 8>(c, s);
+  if (c.experts <= 192) return launch_nv<16, 12>(c, s);
   if (c.experts <= 256) return launch_nv<16, 16>(c, s);
   return launch_nv<64, 16>(c, s);
 }

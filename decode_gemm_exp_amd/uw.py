@@ -558,37 +558,43 @@ SCORE = {"softmax": 0, "softmax_topk": 1, "sigmoid": 2}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _want(t: torch.Tensor, what: str, dtype, shape=None) -> int:
-    """Pointer of a contiguous tensor of this type (and shape) on the current device."""
+def _want(t: torch.Tensor, what: str, dtype, shape, dev: int) -> int:
+    """Pointer of a contiguous tensor of this type (and shape, unless None) on the current device `dev`."""
     if t.dtype is not dtype:
         raise ValueError(f"{what}: {dtype} expected, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{what}: must be contiguous")
-    _on_device(t, what)
+    if t.get_device() != dev:
+        _on_device(t, what, dev)
     return t.data_ptr()
 
 
-def _on_device(t: torch.Tensor, what: str) -> None:
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+def _current() -> int:
+    """The current device; without one every tensor is refused as being elsewhere."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+
+
+def _on_device(t: torch.Tensor, what: str, dev: int) -> None:
+    if t.get_device() != dev:
         raise ValueError(f"{what}: must be on the current device, is on {t.device}")
 
 
-def _rows2d(t: torch.Tensor, what: str) -> int:
+def _rows2d(t: torch.Tensor, what: str, dev: int) -> int:
     """Row stride in elements of a 2-D tensor whose rows are contiguous."""
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{what}: two dimensions with contiguous rows expected")
-    _on_device(t, what)
+    _on_device(t, what, dev)
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _ws(ws: torch.Tensor | None) -> tuple[int | None, int]:
+def _ws(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
     if ws is None:
         return None, 0
     if not ws.is_contiguous():
         raise ValueError("ws: must be contiguous")
-    _on_device(ws, "ws")
+    _on_device(ws, "ws", dev)
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
@@ -601,10 +607,11 @@ def uw_quantize_mx4(src: torch.Tensor, elem: torch.Tensor, scale: torch.Tensor, 
     """src [rows][cols] BF16 or FP32 (rows may be strided) -> elem [rows][cols/2], scale [rows][mx4_scale_stride]."""
     if src.dtype not in _TYPES:
         raise ValueError(f"src: float32 or bfloat16 expected, got {src.dtype}")
-    ld = _rows2d(src, "src")
+    dev = _current()
+    ld = _rows2d(src, "src", dev)
     rows, cols = src.shape
-    pe = _want(elem, "elem", torch.uint8, (rows, cols // 2))
-    ps = _want(scale, "scale", torch.uint8, (rows, mx4_scale_stride(cols)))
+    pe = _want(elem, "elem", torch.uint8, (rows, cols // 2), dev)
+    ps = _want(scale, "scale", torch.uint8, (rows, mx4_scale_stride(cols)), dev)
     _check(_lib.uw_quantize_mx4(src.data_ptr(), _TYPES[src.dtype], rows, cols, ld, pe, ps, _stream(stream)),
            "uw_quantize_mx4")
 
@@ -613,10 +620,11 @@ def uw_dequantize_mx4(elem: torch.Tensor, scale: torch.Tensor, out: torch.Tensor
     """The values of uw_quantize_mx4's arrays into out [rows][cols] BF16 (rows may be strided)."""
     if out.dtype is not torch.bfloat16:
         raise ValueError(f"out: bfloat16 expected, got {out.dtype}")
-    ld = _rows2d(out, "out")
+    dev = _current()
+    ld = _rows2d(out, "out", dev)
     rows, cols = out.shape
-    pe = _want(elem, "elem", torch.uint8, (rows, cols // 2))
-    ps = _want(scale, "scale", torch.uint8, (rows, mx4_scale_stride(cols)))
+    pe = _want(elem, "elem", torch.uint8, (rows, cols // 2), dev)
+    ps = _want(scale, "scale", torch.uint8, (rows, mx4_scale_stride(cols)), dev)
     _check(_lib.uw_dequantize_mx4(pe, ps, rows, cols, out.data_ptr(), ld, _stream(stream)), "uw_dequantize_mx4")
 
 
@@ -631,61 +639,80 @@ def uw_matmul_mx4(elem: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: t
     """y [batch][n] FP32 = x [batch][k] BF16 times the MXFP4 matrix (elem [n][k/2], scale [n][stride])."""
     if x.dim() != 2 or elem.dim() != 2:
         raise ValueError("x and elem: two dimensions expected")
+    dev = _current()
     (batch, k), n = x.shape, elem.shape[0]
-    pe = _want(elem, "elem", torch.uint8, (n, k // 2))
-    ps = _want(scale, "scale", torch.uint8, (n, mx4_scale_stride(k)))
-    px = _want(x, "x", torch.bfloat16)
-    py = _want(y, "y", torch.float32, (batch, n))
-    pw, nb = _ws(ws)
+    pe = _want(elem, "elem", torch.uint8, (n, k // 2), dev)
+    ps = _want(scale, "scale", torch.uint8, (n, mx4_scale_stride(k)), dev)
+    px = _want(x, "x", torch.bfloat16, None, dev)
+    py = _want(y, "y", torch.float32, (batch, n), dev)
+    pw, nb = _ws(ws, dev)
     _check(_lib.uw_matmul_mx4(pe, ps, n, k, px, batch, py, act, pw, nb, _stream(stream)), "uw_matmul_mx4")
 
 
 # ---- mixture of experts ------------------------------------------------------
 
 class Routing:
-    """The buffers of a router's choice and of the plan that sorts its pairs by expert (see unweight.h)."""
+    """The buffers of a router's choice and of the plan that sorts its pairs by expert (see unweight.h).
+
+    ids, weights, slots [tokens][topk], offsets [experts + 1], rows [tokens * topk]; read-only attributes
+    (their contents may be written), so that a call need not ask each tensor for its pointer again.
+    """
 
     def __init__(self, tokens: int, experts: int, topk: int, device="cuda"):
-        self.tokens, self.experts, self.topk = tokens, experts, topk
         n = ctypes.c_size_t()
         _check(_lib.uw_workspace_size_route(tokens, experts, topk, ctypes.byref(n)), "uw_workspace_size_route")
-        pairs = tokens * topk
-        self.ids = torch.empty(tokens, topk, dtype=torch.int32, device=device)
-        self.weights = torch.empty(tokens, topk, dtype=torch.float32, device=device)
-        self.offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
-        self.rows = torch.zeros(pairs, dtype=torch.int32, device=device)
-        self.slots = torch.empty(tokens, topk, dtype=torch.int32, device=device)
-        self.ws = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+        self._shape = tokens, experts, topk
+        pair = lambda dtype: torch.empty(tokens, topk, dtype=dtype, device=device)  # noqa: E731
+        self._t = (pair(torch.int32), pair(torch.float32),
+                   torch.empty(experts + 1, dtype=torch.int32, device=device),
+                   torch.zeros(tokens * topk, dtype=torch.int32, device=device), pair(torch.int32))
+        self._ws = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
+        self._ptrs = tuple(t.data_ptr() for t in self._t)
+        self._ws_args = (self._ws.data_ptr(), n.value) if n.value else (None, 0)
+        self._dev = self._t[2].get_device()
+
+    tokens = property(lambda self: self._shape[0])
+    experts = property(lambda self: self._shape[1])
+    topk = property(lambda self: self._shape[2])
+    ids = property(lambda self: self._t[0])
+    weights = property(lambda self: self._t[1])
+    offsets = property(lambda self: self._t[2])
+    rows = property(lambda self: self._t[3])
+    slots = property(lambda self: self._t[4])
+
+    def _check_device(self, dev: int) -> None:
+        if self._dev != dev:
+            raise ValueError(f"routing: must be on the current device, is on {self._t[2].device}")
 
 
 def uw_route_experts(logits: torch.Tensor, routing: Routing, scoring: str = "softmax_topk",
                      bias: torch.Tensor | None = None, stream=None) -> None:
     """logits [tokens][experts] FP32 or BF16 (rows may be strided) -> routing's ids, weights and plan."""
-    r = routing
-    if logits.dtype not in _TYPES:
+    tokens, experts, topk = routing._shape
+    kind = _TYPES.get(logits.dtype)
+    if kind is None:
         raise ValueError(f"logits: float32 or bfloat16 expected, got {logits.dtype}")
-    if scoring not in SCORE:
+    score = SCORE.get(scoring)
+    if score is None:
         raise ValueError(f"scoring: one of {sorted(SCORE)} expected, got {scoring!r}")
-    ld = _rows2d(logits, "logits")
-    if logits.shape != (r.tokens, r.experts):
-        raise ValueError(f"logits: shape {(r.tokens, r.experts)} expected, got {tuple(logits.shape)}")
-    pb = _want(bias, "bias", torch.float32, (r.experts,)) if bias is not None else None
-    _on_device(r.ids, "routing")
-    pw, nb = _ws(r.ws)
-    _check(_lib.uw_route_experts(logits.data_ptr(), _TYPES[logits.dtype], r.tokens, r.experts, ld, pb, r.topk,
-                                 SCORE[scoring], r.ids.data_ptr(), r.weights.data_ptr(), r.offsets.data_ptr(),
-                                 r.rows.data_ptr(), r.slots.data_ptr(), pw, nb, _stream(stream)),
-           "uw_route_experts")
+    dev = _current()
+    ld = _rows2d(logits, "logits", dev)
+    if logits.shape != (tokens, experts):
+        raise ValueError(f"logits: shape {(tokens, experts)} expected, got {tuple(logits.shape)}")
+    pb = _want(bias, "bias", torch.float32, (experts,), dev) if bias is not None else None
+    routing._check_device(dev)
+    _check(_lib.uw_route_experts(logits.data_ptr(), kind, tokens, experts, ld, pb, topk, score, *routing._ptrs,
+                                 *routing._ws_args, _stream(stream)), "uw_route_experts")
 
 
 def uw_plan_experts(ids: torch.Tensor, routing: Routing, stream=None) -> None:
     """The plan for choices made elsewhere: ids [tokens][topk] int32, outside 0..experts-1 = none."""
-    r = routing
-    pi = _want(ids, "ids", torch.int32, (r.tokens, r.topk))
-    _on_device(r.ids, "routing")
-    pw, nb = _ws(r.ws)
-    _check(_lib.uw_plan_experts(pi, r.tokens, r.experts, r.topk, r.offsets.data_ptr(), r.rows.data_ptr(),
-                                r.slots.data_ptr(), pw, nb, _stream(stream)), "uw_plan_experts")
+    tokens, experts, topk = routing._shape
+    dev = _current()
+    pi = _want(ids, "ids", torch.int32, (tokens, topk), dev)
+    routing._check_device(dev)
+    _check(_lib.uw_plan_experts(pi, tokens, experts, topk, *routing._ptrs[2:], *routing._ws_args, _stream(stream)),
+           "uw_plan_experts")
 
 
 class Experts:
@@ -712,7 +739,7 @@ def uw_experts_bf16(w: torch.Tensor, count: int, n: int, k: int, stride: int = 0
     """w: BF16, expert e's [n][k] at element e * stride (0: n * k); w may be a view into a larger array."""
     if w.dtype is not torch.bfloat16:
         raise ValueError(f"w: bfloat16 expected, got {w.dtype}")
-    _on_device(w, "w")
+    _on_device(w, "w", _current())
     h = ctypes.c_void_p()
     _check(_lib.uw_experts_bf16(w.data_ptr(), count, n, k, stride, ctypes.byref(h)), "uw_experts_bf16")
     try:
@@ -736,7 +763,7 @@ def uw_experts_mx4(elem: torch.Tensor, scale: torch.Tensor, count: int, n: int, 
     for t, what in ((elem, "elem"), (scale, "scale")):
         if t.dtype is not torch.uint8:
             raise ValueError(f"{what}: uint8 expected, got {t.dtype}")
-        _on_device(t, what)
+        _on_device(t, what, _current())
     h = ctypes.c_void_p()
     _check(_lib.uw_experts_mx4(elem.data_ptr(), scale.data_ptr(), count, n, k, elem_stride, scale_stride,
                                ctypes.byref(h)), "uw_experts_mx4")
@@ -768,10 +795,10 @@ def _ragged(w: Experts, offsets: torch.Tensor, rows, x: torch.Tensor, y: torch.T
         raise ValueError(f"x: shape [rows, {w.k}] expected, got {tuple(x.shape)}")
     if y.dim() != 2 or y.shape[1] != w.n:
         raise ValueError(f"output: shape [slots, {w.n}] expected, got {tuple(y.shape)}")
-    slots = y.shape[0]
-    po = _want(offsets, "offsets", torch.int32, (w.count + 1,))
-    pr = _want(rows, "rows", torch.int32, (slots,)) if rows is not None else None
-    return po, pr, slots, _want(x, "x", torch.bfloat16), x.shape[0], _want(y, "output", dtype)
+    slots, dev = y.shape[0], _current()
+    po = _want(offsets, "offsets", torch.int32, (w.count + 1,), dev)
+    pr = _want(rows, "rows", torch.int32, (slots,), dev) if rows is not None else None
+    return po, pr, slots, _want(x, "x", torch.bfloat16, None, dev), x.shape[0], _want(y, "output", dtype, None, dev)
 
 
 def uw_matmul_experts(w: Experts, offsets: torch.Tensor, rows: torch.Tensor | None, x: torch.Tensor,
@@ -798,13 +825,13 @@ def uw_workspace_size_expert_mlp(gate: Experts, down: Experts, tokens: int, topk
 def uw_expert_mlp(gate: Experts, up: Experts, down: Experts, routing: Routing, x: torch.Tensor, out: torch.Tensor,
                   ws: torch.Tensor, stream=None) -> None:
     """out [tokens][k] BF16: the layer's MLP on a routing made by uw_route_experts (or a plan and weights)."""
-    r = routing
-    if r.experts != gate.count:
-        raise ValueError(f"routing: {gate.count} experts expected, got {r.experts}")
-    px = _want(x, "x", torch.bfloat16, (r.tokens, gate.k))
-    po = _want(out, "out", torch.bfloat16, (r.tokens, gate.k))
-    _on_device(r.ids, "routing")
-    pw, nb = _ws(ws)
-    _check(_lib.uw_expert_mlp(gate.handle, up.handle, down.handle, r.tokens, r.topk, r.offsets.data_ptr(),
-                              r.rows.data_ptr(), r.slots.data_ptr(), r.weights.data_ptr(), px, po, pw, nb,
-                              _stream(stream)), "uw_expert_mlp")
+    tokens, experts, topk = routing._shape
+    if experts != gate.count:
+        raise ValueError(f"routing: {gate.count} experts expected, got {experts}")
+    dev = _current()
+    px = _want(x, "x", torch.bfloat16, (tokens, gate.k), dev)
+    po = _want(out, "out", torch.bfloat16, (tokens, gate.k), dev)
+    routing._check_device(dev)
+    _, weights, offsets, rows, slots = routing._ptrs
+    _check(_lib.uw_expert_mlp(gate.handle, up.handle, down.handle, tokens, topk, offsets, rows, slots, weights, px, po,
+                              *_ws(ws, dev), _stream(stream)), "uw_expert_mlp")
