@@ -153,14 +153,14 @@ __device__ __forceinline__ void tile_of(uint32_t l, uint32_t chunks, uint32_t nt
 }
 
 // The same for tiles of ntiles columns, dealt so that each XCD works on one
-// contiguous run of the list: blocks go to the 8 XCDs round robin, so block b
-// takes entry b / 8 of XCD b % 8's eighth of the list that really exists (its
-// length follows from the offsets).  What it returns is in scalar registers:
+// contiguous run of the list: entry `turn` of XCD `xcd`'s eighth of the list that
+// really exists (its length follows from the offsets); blocks go to the XCDs
+// round robin, so block b is on XCD b % 8.  What it returns is in scalar registers:
 // buffer resources built from it then need no loop over a wave's lanes (a
 // division done in vector registers would leave it there).  The list runs over experts, then column
 // tiles, then an expert's row chunks, so neighbours share weights and x in
 // one L2.  Returns the column tile, or -1: nothing to do.
-__device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, unsigned block, int ntiles, int chunk,
+__device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, int xcd, int64_t turn, int ntiles, int chunk,
                                          Share& out) {
   out = Share{0, 0, 0};
   const int lane = threadIdx.x & 63;
@@ -196,8 +196,8 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, unsig
     }
   }
   const int64_t tiles = total * ntiles, share = (tiles + 7) / 8;
-  const int64_t at = (block & 7) * share + (block >> 3);
-  if ((int64_t)(block >> 3) >= share || at >= tiles) return -1;
+  const int64_t at = xcd * share + turn;
+  if (turn >= share || at >= tiles) return -1;
   if (!r.offsets) {
     int m, nt;
     tile_of((uint32_t)at, (uint32_t)total, (uint32_t)ntiles, m, nt);   // (at < 2^31: the grid is)
@@ -279,7 +279,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 
 // g / (1 + exp(-g)): exp(-g) overflows to infinity for g below -88.7, where
 // the quotient is -0, as it should round
-__device__ __forceinline__ float silu(float g) { return g / (1.0f + __expf(-g)); }
+// (the reciprocal instruction is within one unit in the last place)
+__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
 
 // ---- launchers ----------------------------------------------------------------
 // y (fp32, mode 0) or h = silu(W x) * (U x) (BF16, mode 1; u the second

@@ -20,11 +20,12 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 uint64_t pad256(uint64_t n) { return (n + 255) / 256 * 256; }
 
 // A shape the expert and MXFP4 kernels take: k in whole blocks of 32.  The
-// tile kernels address 256 rows of a matrix with 30-bit byte offsets (512 k of
-// BF16), and every byte count of one matrix stays far inside 63 bits.
+// tile kernels address 256 rows of a matrix, and of the output, with 31-bit byte
+// offsets, so k and n stay up to 2^20; every byte count of one matrix is far
+// inside 63 bits.
 uw_status check_shape(int64_t n, int64_t k) {
   if (n <= 0 || k <= 0) return UW_ERR_INVALID;
-  if (k % 32 != 0 || n > INT32_MAX || k > (1 << 21)) return UW_ERR_UNSUPPORTED;
+  if (k % 32 != 0 || n > (1 << 20) || k > (1 << 20)) return UW_ERR_UNSUPPORTED;
   return UW_OK;
 }
 

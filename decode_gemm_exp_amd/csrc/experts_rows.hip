@@ -374,9 +374,12 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
 // every CU: with fewer, smaller tiles, and below three quarters of the CUs the
 // register-fed kernel again, up to the rows where its reloading of weights
 // costs more.  Measured (us, register-fed / 64 / 128 / 256):
-//   BF16, 32 experts 2048x2048, 16 rows: 73 / 70 / 72 / 74
-//   BF16 gated, 64 experts 1408x2048, 512 rows: 1985 / 581 / 529 / 450
-//   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1438 / 772 / 495 / 409
+//   BF16, 32 experts 2048x2048, 16 rows: 73 / 68 / 68 / 69
+//   BF16, 16 experts 2048x2048, 64 rows: 69 / 42 / 44 / 49
+//   BF16, 24 experts 1500x1024, 167 rows: 114 / 40 / 33 / 33
+//   BF16 layer, 64 experts 1408x2048, 281 rows: 1902 / 628 / 489 / 469
+//   BF16 gated, 64 experts 1408x2048, 512 rows: 1985 / 600 / 441 / 402
+//   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1438 / 579 / 464 / 356
 //   UWF1, 32 experts 2048x4096, 3 rows: 75 / 106 / 110 / 135
 //   MXFP4 14336x4096: 64 rows 35 / 52 / 59 / 69, 128 rows 66 / 53 / 63 / 73
 //   MXFP4, few tiles: 5001x8224, 200 rows 84 / 109 / 125 / 179; 4096x4096, 256 rows 34 / 52 / 63 / 95
@@ -386,7 +389,7 @@ hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
   if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_experts_tile(c, 256, s);   // x past 2 GiB: by pointers
   const int64_t cus = device_cus(), ntiles = (c.w.n + (c.gated ? 127 : 255)) / (c.gated ? 128 : 256);
   auto blocks = [&](int rows) { return ntiles * max_chunks(c.r.slots, c.w.count, rows, c.r.offsets != nullptr); };
-  int rows = avg <= 96 ? 64 : avg <= 160 ? 128 : 256;
+  int rows = avg <= 48 ? 64 : avg <= 256 ? 128 : 256;
   while (rows > 64 && blocks(rows) < cus) rows /= 2;
   if (avg <= 12 || (avg <= 256 && blocks(rows) < cus * 3 / 4)) return launch_experts_rows(c, s);
   return launch_experts_tile(c, rows, s);

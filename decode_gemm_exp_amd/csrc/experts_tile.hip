@@ -5,15 +5,14 @@
 // A block computes BM slots of one expert times 256 weight rows (gated: 128
 // gate rows and the same 128 up rows, 32 by 32 interleaved so that a wave
 // holds both factors of its outputs).  Eight waves, two along the slots and
-// four along the columns, each BM/2 x 64.  K advances 64 at a time through two
-// LDS buffers:
-//   * step s runs its MFMAs from one buffer, fragments one 16-wide slice ahead
+// four along the columns, each BM/2 x 64.  K advances 64 at a time:
+//   * K goes through a ring of LDS buffers; step s runs its MFMAs from one, fragments one 16-wide slice ahead
 //     of use.  x and BF16 weights go straight from memory to LDS (16 bytes a
 //     lane, no registers); UWF1 and MXFP4 weights through registers, rebuilt
 //     to BF16 once per block, loaded two steps ahead and stored one ahead;
 //   * the one barrier of a step stands before its last slice's MFMAs, so the
 //     next step's first fragments travel while those run, and the buffer the
-//     step leaves is refilled for the step after the next right behind it;
+//     step leaves is refilled right behind it;
 //   * LDS rows are 128 bytes without padding; 16-byte piece c of row r sits at
 //     c ^ (r / 2 % 8).  LDS has 64 banks, two rows' worth, and serves 16 lanes of
 //     a 16-byte read at a time: 16 rows of one fragment column then meet all
@@ -24,8 +23,21 @@
 // index outside x) lies past the resource's end.  Beyond 2 GiB of x the rows go
 // by 64-bit pointers instead (BIG, 256-row tiles only): those loads are of the
 // flat kind, whose counters the compiler must drain before any LDS read, about
-// 10 % of the time.  Waves whose slots all lie behind the expert's last row skip their
-// MFMAs.
+// 10 % of the time.
+//
+// A wave's row tiles alternate with the other's along the slots, and what lies
+// behind the expert's last row is skipped by halves of a wave's rows, so a partly
+// filled block costs both waves of a SIMD about what it holds.
+//
+// Where x and weights both go straight to LDS (BF16), as many steps as LDS holds
+// are on their way at once: four buffers of 64-row tiles, three of 128-row ones,
+// and for 256 rows three of weights, which come from HBM, and two of x, which
+// mostly comes from L2, together all 160 KiB.  Gated, 64 experts 1408x2048 of 512
+// rows each, us: 128-row tiles with two buffers 515, three 441; 256-row tiles
+// with two 414, three of weights 402 (0.94 PFLOP/s; 8192^3 in one matrix 1.28,
+// a library's BF16 product of that size 1.35 on the same card).  Without any
+// loads in the loop (a timing copy) it took 347: the rest is LDS reads, barriers
+// and the matrix unit at the clock it holds.
 #include <type_traits>
 
 #include "experts.h"
@@ -59,6 +71,16 @@ __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0
 
 typedef __attribute__((address_space(3))) char lds_char;
 
+// A block barrier without a fence: a fence would wait for everything that is on
+// its way to LDS.  The caller has waited for what must have landed.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
+}
+
 // the piece of its LDS row that lands at this thread's place (see piece_at)
 __device__ __forceinline__ int own_piece() { return (threadIdx.x ^ (threadIdx.x >> 4)) & 7; }
 
@@ -68,6 +90,7 @@ struct Weights<kFormBf16> {
   static constexpr bool kDirect = true;
   __amdgpu_buffer_rsrc_t r;
   uint32_t off[4], col;
+  // (off and col are the same for every tile)
   template <typename RowOf>
   __device__ __forceinline__ void init(const ExpertsView& w, const ExpertsView& u, int e, int64_t n0, RowOf&& row_of) {
     const int tid = threadIdx.x;
@@ -79,11 +102,9 @@ struct Weights<kFormBf16> {
     const int64_t rows = m.n - n0 < kBN ? m.n - n0 : kBN;
     r = rsrc_of(m.w + (int64_t)e * m.w_stride + n0 * 2 * m.k, (uint64_t)rows * 2 * m.k);
   }
-  __device__ __forceinline__ void direct(int64_t k0, int64_t K, lds_char* to) const {
-    const uint32_t ko = k0 + col < K ? (uint32_t)(2 * k0) : kOutside;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + 8192 * i, 16, (int)(off[i] + ko), 0, 0, 0);
+  __device__ __forceinline__ void direct(int k0, int K, lds_char* to, int i) const {   // piece i of four
+    const uint32_t ko = k0 + (int)col < K ? 2u * (uint32_t)k0 : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, to + 8192 * i, 16, (int)(off[i] + ko), 0, 0, 0);
   }
 };
 
@@ -108,8 +129,8 @@ struct Weights<kFormMx4> {
     r = rsrc_of(m.w + (int64_t)e * m.w_stride + n0 * (m.k / 2), (uint64_t)rows * (m.k / 2));
     rs = rsrc_of(m.scale + (int64_t)e * m.scale_stride + n0 * mx4_scale_stride(m.k), (uint64_t)rows * mx4_scale_stride(m.k));
   }
-  __device__ __forceinline__ void load(int64_t k0, int64_t K, int set) {
-    const bool in = k0 + col < K;
+  __device__ __forceinline__ void load(int k0, int K, int set) {
+    const bool in = k0 + (int)col < K;
     d[set] = bload16(r, off + (in ? (uint32_t)(k0 / 2) : kOutside));
     sc[set] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(soff + (in ? (uint32_t)(k0 / 32) : kOutside)), 0, 0);
   }
@@ -150,9 +171,9 @@ struct WeightsPal {
       el[i] = (uint32_t)(n * w.k) + 16u * (tid & 3);
     }
     t = (__builtin_amdgcn_readfirstlane((int)up) ? u : w).table[e];
-    flags(0, w.k);
+    flags(0, (int)w.k);
   }
-  __device__ __forceinline__ void flags(int64_t k0, int64_t K) {
+  __device__ __forceinline__ void flags(int k0, int K) {
     const uint32_t k = k0 < K ? (uint32_t)k0 : 0u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -160,7 +181,7 @@ struct WeightsPal {
       rw[i] = gload<uint32_t>(t.vrank + ((el[i] + k) >> 11));
     }
   }
-  __device__ __forceinline__ void load(int64_t k0, int64_t K, int set) {   // K % 64 == 0: a step is whole or absent
+  __device__ __forceinline__ void load(int k0, int K, int set) {   // K % 64 == 0: a step is whole or absent
     const uint32_t k = k0 < K ? (uint32_t)k0 : 0u;
     verb[set] = 0;
 #pragma unroll
@@ -197,183 +218,255 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   constexpr int XP = BM / 64;                 // pieces of x a thread moves per step
   using W = Weights<FORM>;
   constexpr int OUT = GATED ? 128 : 256;      // output columns of a block
+  // buffers of x and of weights
+  constexpr int SX = !W::kDirect || BM == 256 ? 2 : BM == 128 ? 3 : 4;
+  constexpr int SW = W::kDirect && BM == 256 && !BIG ? 3 : SX;
   // objects of their own rather than parts of one, so that the compiler sees that
   // what is read from or stored to one does not wait for what travels into
   // another
-  __shared__ __attribute__((aligned(128))) char xa[BM * 128], xb[BM * 128];
-  __shared__ __attribute__((aligned(128))) char wa[kBN * 128], wb[kBN * 128];
+  constexpr int kX = BM * 128, kW = kBN * 128;
+  __shared__ __attribute__((aligned(128))) char x0[kX], x1[kX], w0[kW], w1[kW];
+  __shared__ __attribute__((aligned(16))) char x2[SX > 2 ? kX : 16], x3[SX > 3 ? kX : 16], w2[SW > 2 ? kW : 16],
+      w3[SW > 3 ? kW : 16];   // (those of 16 bytes are never touched and take no space)
+  char* const xbufs[4] = {x0, x1, x2, x3};
+  char* const wbufs[4] = {w0, w1, w2, w3};
 
-  Share sh;
-  const int nt = find_tile(rr, vw.count, blockIdx.x, ntiles, BM, sh);
-  if (nt < 0) return;
+  // row tiles come in groups of G, a wave's groups alternating with the other's
+  constexpr int G = TM == 4 ? 2 : 1;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
-  const int64_t N = vw.n, K = vw.k;
-  const int64_t n0 = (int64_t)nt * OUT;
-
-  // x: LDS rows tid / 8 + 64 i
+  const int K = (int)vw.k;
   const int xcol = 8 * own_piece();
-  uint32_t xo[XP];          // byte offset of the row
-  const uint16_t* xp[XP];   // BIG: its address, NULL for a row of zeros
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, BIG ? 0 : (uint64_t)rr.x_rows * 2 * K);
+
+  // The block's tile: its slots and columns, and where its x and weights lie.
+  struct Tile {
+    Share sh;
+    int nt;
+    uint32_t xo[XP];          // x, LDS rows tid / 8 + 64 i: byte offset of the row
+    const uint16_t* xp[XP];   // BIG: its address, NULL for a row of zeros
+    W w;
+  } t;
+  t.nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, ntiles, BM, t.sh);
+  if (t.nt < 0) return;
 #pragma unroll
   for (int i = 0; i < XP; ++i) {
     const int b = tid / 8 + 64 * i;
-    int64_t row = sh.first + (b < sh.count ? b : 0);
+    int64_t row = t.sh.first + (b < t.sh.count ? b : 0);
     if (rr.rows) row = rr.rows[row];
     const bool in = row >= 0 && row < rr.x_rows;
-    xo[i] = in ? (uint32_t)(2 * (row * K + xcol)) : kOutside;
-    xp[i] = in ? x + row * K + xcol : nullptr;
+    t.xo[i] = in ? (uint32_t)(2 * (row * K + xcol)) : kOutside;
+    t.xp[i] = in ? x + row * K + xcol : nullptr;
   }
-  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, BIG ? 0 : (uint64_t)rr.x_rows * 2 * K);
-  auto direct_x = [&](int64_t k0, lds_char* to) __attribute__((always_inline)) {
-    if constexpr (BIG) {
-#pragma unroll
-      for (int i = 0; i < XP; ++i) {
-        const void* p = xp[i] && k0 + xcol < K ? (const void*)(xp[i] + k0) : (const void*)g_zero16;
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, to + 8192 * i, 16, 0, 0);
-      }
-    } else {
-      const uint32_t ko = k0 + xcol < K ? (uint32_t)(2 * k0) : kOutside;
-#pragma unroll
-      for (int i = 0; i < XP; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to + 8192 * i, 16, (int)(xo[i] + ko), 0, 0, 0);
-    }
-  };
-  // the step from k0, as far as it goes straight to LDS
-  W w;
-  auto direct = [&](int64_t k0, char* xbuf, char* wbuf) __attribute__((always_inline)) {
-    direct_x(k0, (lds_char*)(xbuf + wave * 1024));
-    if constexpr (W::kDirect) w.direct(k0, K, (lds_char*)(wbuf + wave * 1024));
-  };
-  w.init(vw, vu, sh.expert, n0, [](int c, bool& up) __attribute__((always_inline)) {
+  t.w.init(vw, vu, t.sh.expert, (int64_t)t.nt * OUT, [](int c, bool& up) __attribute__((always_inline)) {
     up = GATED && (c & 32);
     return GATED ? (c >> 6) * 32 + (c & 31) : c;
   });
 
+  // what goes straight to LDS of the step from k0: x's piece i of XP, the weights' of WP
+  constexpr int WP = W::kDirect ? 4 : 0;
+  auto direct_x = [&](int k0, char* buf, int i) __attribute__((always_inline)) {
+    lds_char* to = (lds_char*)(buf + wave * 1024 + 8192 * i);
+    if constexpr (BIG) {
+      const void* p = t.xp[i] && k0 + xcol < K ? (const void*)(t.xp[i] + k0) : (const void*)g_zero16;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, to, 16, 0, 0);
+    } else {
+      const uint32_t ko = k0 + xcol < K ? 2u * (uint32_t)k0 : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, (int)(t.xo[i] + ko), 0, 0, 0);
+    }
+  };
+  auto direct_w = [&](int k0, char* buf, int i) __attribute__((always_inline)) {
+    if constexpr (W::kDirect) t.w.direct(k0, K, (lds_char*)(buf + wave * 1024), i);
+  };
+
   f32x16_t acc[TM][2];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
   bf16x8_t fa[2][TM], fb[2][2];
   const int frow = lane & 31, fpiece = lane >> 5;
+  // first slot, within the tile, of the wave's row tile i
+  auto slot_of = [&](int i) __attribute__((always_inline)) { return ((i / G) * 2 + wm) * (32 * G) + (i % G) * 32; };
   // Piece 2 slice + lane / 32 of row r lies at r * 128 + 16 ((lane / 32 ^ r / 2 % 8)
   // ^ 2 slice): one base for x and one for the weights, the slice flipping
-  // two of its bits, a row tile 4096 bytes further.  (The empty asm makes a base
+  // two of its bits, a row tile a constant further.  (The empty asm makes a base
   // opaque, or the compiler keeps all sixteen addresses of two buffers in
   // registers, and spills.)
-  const uint32_t base_a = piece_at(wm * (BM / 2) + frow, fpiece), base_b = piece_at(wn * 64 + frow, fpiece);
-  auto read = [&](const char* xbuf, const char* wbuf, int slice, int p) __attribute__((always_inline)) {
+  const uint32_t base_a = piece_at(wm * (32 * G) + frow, fpiece), base_b = piece_at(wn * 64 + frow, fpiece);
+  auto read = [&](const char* xbuf, const char* wbuf, int slice, int p, auto TA) __attribute__((always_inline)) {
     uint32_t a = base_a, b = base_b;
     asm volatile("" : "+v"(a), "+v"(b));
     a ^= 32u * slice;
     b ^= 32u * slice;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) fa[p][i] = *reinterpret_cast<const bf16x8_t*>(xbuf + a + 4096 * i);
+    for (int i = 0; i < decltype(TA)::value; ++i)
+      fa[p][i] = *reinterpret_cast<const bf16x8_t*>(xbuf + a + (i / G) * (64 * G * 128) + (i % G) * 4096);
 #pragma unroll
     for (int j = 0; j < 2; ++j) fb[p][j] = *reinterpret_cast<const bf16x8_t*>(wbuf + b + 4096 * j);
   };
-  auto mma = [&](int p) __attribute__((always_inline)) {
+  auto mma_one = [&](int p, int t) __attribute__((always_inline)) {
+    acc[t / 2][t % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[p][t / 2], fb[p][t % 2], acc[t / 2][t % 2], 0, 0, 0);
+  };
+  auto mma = [&](int p, auto TA) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[p][i], fb[p][j], acc[i][j], 0, 0, 0);
+    for (int t = 0; t < 2 * decltype(TA)::value; ++t) mma_one(p, t);
   };
 
-  const int steps = (int)((K + kBK - 1) / kBK);
+  const int steps = (K + kBK - 1) / kBK;
   auto store = [&](char* wbuf, int part, int set) __attribute__((always_inline)) {
-    if constexpr (!W::kDirect) w.store(wbuf, part, set);
+    if constexpr (!W::kDirect) t.w.store(wbuf, part, set);
   };
-  auto load = [&](int64_t k0, int set) __attribute__((always_inline)) {
-    if constexpr (!W::kDirect) w.load(k0, K, set);
+  auto load = [&](int k0, int set) __attribute__((always_inline)) {
+    if constexpr (!W::kDirect) t.w.load(k0, K, set);
   };
-  direct(0, xa, wa);
-  load(0, 0);
-  load(kBK, 1);
-  store(wa, 0, 0);
-  store(wa, 1, 0);
-  direct(kBK, xb, wb);
-  load(2 * kBK, 0);
-  asm volatile("" : : "s"(y));   // its scalar load ends here: pending, it would make the loop's first LDS wait a full one
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  const bool active = wm * (BM / 2) < sh.count;
-  if (active) read(xa, wa, 0, 0);
-  // two steps an iteration, so that buffers and register sets are constants;
-  // step s of parity q finds its data in xcur and wcur, that of s + 1 in set
-  // 1 - q and on its way to xnxt and wnxt
-  auto step = [&](int s, char* xcur, char* wcur, char* xnxt, char* wnxt, auto Q, auto Active) __attribute__((always_inline)) {
-    constexpr int q = decltype(Q)::value;
-    constexpr bool kActive = decltype(Active)::value;
+  // Step s: its data is in buffers J % SX and J % SW, that of s + 1 in register
+  // set (J + 1) % 2 (what goes through registers) and on its way to the next
+  // buffers.  TA: the wave's row tiles that hold slots (0: it moves data for the
+  // others).
+  auto step = [&](int s, auto J, auto TA) __attribute__((always_inline)) {
+    constexpr int j = decltype(J)::value;
+    constexpr bool kActive = decltype(TA)::value > 0;
+    char* const xcur = xbufs[j % SX];
+    char* const wcur = wbufs[j % SW];
+    char* const xnxt = xbufs[(j + 1) % SX];
+    char* const wnxt = wbufs[(j + 1) % SW];
     if constexpr (kActive) {
       // (the scheduling barriers keep each slice's reads ahead of the MFMAs of
       // the slice before, which cover their latency)
-      read(xcur, wcur, 1, 1);
+      read(xcur, wcur, 1, 1, TA);
       __builtin_amdgcn_sched_barrier(0);
-      store(wnxt, 0, 1 - q);
-      mma(0);
+      store(wnxt, 0, (j + 1) % 2);
+      mma(0, TA);
       __builtin_amdgcn_sched_barrier(0);
-      read(xcur, wcur, 2, 0);
+      read(xcur, wcur, 2, 0, TA);
       __builtin_amdgcn_sched_barrier(0);
-      store(wnxt, 1, 1 - q);
-      mma(1);
+      store(wnxt, 1, (j + 1) % 2);
+      mma(1, TA);
       __builtin_amdgcn_sched_barrier(0);
-      read(xcur, wcur, 3, 1);
+      read(xcur, wcur, 3, 1, TA);
       __builtin_amdgcn_sched_barrier(0);
-      mma(0);
+      mma(0, TA);
       __builtin_amdgcn_sched_barrier(0);
-    } else {   // moves data for the other waves
-      store(wnxt, 0, 1 - q);
-      store(wnxt, 1, 1 - q);
+    } else {
+      store(wnxt, 0, (j + 1) % 2);
+      store(wnxt, 1, (j + 1) % 2);
     }
-    // this thread's part of step s + 1 has landed, and this wave has read all
-    // of step s: after the barrier both hold for the block
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    direct((int64_t)kBK * (s + 2), xcur, wcur);
-    load((int64_t)kBK * (s + 3), 1 - q);
+    // This thread's part of step s + 1 has landed, and this wave has read all
+    // of step s: after the barrier both hold for the block.  What may still
+    // travel, all of it issued after s + 1's pieces: with SX = SW the S - 2
+    // later steps, with one buffer more of weights the weights of s + 2.
+    constexpr int kLater = !W::kDirect ? 0 : SX == SW ? (XP + WP) * (SX - 2) : WP;
+    static_assert(kLater < 16 && (SX == SW || (SX == 2 && SW == 3)), "the counter's low field; what is issued when");
+    __builtin_amdgcn_s_waitcnt(0x70 | kLater);   // vmcnt kLater, lgkmcnt 0
+    bare_barrier();
     if constexpr (kActive) {
-      read(xnxt, wnxt, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      mma(1);
+      read(xnxt, wnxt, 0, 0, TA);
       __builtin_amdgcn_sched_barrier(0);
     }
-  };
-  auto run = [&](auto Active) __attribute__((always_inline)) {
-    int s = 0;
-    for (; s + 1 < steps; s += 2) {
-      step(s, xa, wa, xb, wb, std::integral_constant<int, 0>{}, Active);
-      step(s + 1, xb, wb, xa, wa, std::integral_constant<int, 1>{}, Active);
+    // The pieces that refill this step's buffers, x first, one behind each MFMA:
+    // all at once they fill the memory pipe, and what the wave issues next waits.
+    constexpr int kMma = 2 * decltype(TA)::value, kPieces = XP + WP;
+#pragma unroll
+    for (int i = 0; i < (kMma > kPieces ? kMma : kPieces); ++i) {
+      if (i < kMma) mma_one(1, i);
+      if (i < XP) direct_x(kBK * (s + SX), xcur, i);
+      else if (i < kPieces) direct_w(kBK * (s + SW), wcur, i - XP);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    if (s < steps) step(s, xa, wa, xb, wb, std::integral_constant<int, 0>{}, Active);
+    load(kBK * (s + 3), (j + 1) % 2);
   };
-  // (a wave takes one of the two loops as a whole; both pass the same barriers)
-  if (!active) {
-    run(std::false_type{});
-    return;
-  }
-  run(std::true_type{});
-
   // D of the MFMA: lane l, register r: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
+  // The tile's rows of y are one buffer resource, so rows behind the last slot
+  // are dropped by its bound, as are columns past N, by an offset outside.
+  auto write = [&](auto TA) __attribute__((always_inline)) {
+    constexpr int kSize = GATED ? 2 : 4, kCols = GATED ? 1 : 2;
+    const __amdgpu_buffer_rsrc_t ry =
+        rsrc_of(static_cast<char*>(y) + t.sh.first * vw.n * kSize, (uint64_t)t.sh.count * (uint64_t)vw.n * kSize);
+    int N = (int)vw.n;
+    asm volatile("" : "+s"(N));   // or every row's offset is kept in registers over all tiles
+    uint32_t at[kCols];
 #pragma unroll
-  for (int i = 0; i < TM; ++i)
+    for (int j = 0; j < kCols; ++j) {
+      const int n = t.nt * OUT + (GATED ? wn * 32 : wn * 64 + 32 * j) + frow;
+      at[j] = n < N ? (uint32_t)(4 * (lane >> 5) * N + n) * kSize : kOutside;
+    }
 #pragma unroll
-    for (int r = 0; r < 16; ++r) {
-      const int b = wm * (BM / 2) + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-      if (b >= sh.count) continue;
-      if constexpr (GATED) {
-        const int64_t n = n0 + wn * 32 + frow;
-        const float h = silu(acc[i][0][r]) * acc[i][1][r];
-        if (n < N) static_cast<uint16_t*>(y)[(sh.first + b) * N + n] = (uint16_t)bf16_pair(h, h);
-      } else {
+    for (int i = 0; i < decltype(TA)::value; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int64_t n = n0 + wn * 64 + 32 * j + frow;
-          if (n < N) static_cast<float*>(y)[(sh.first + b) * N + n] = acc[i][j][r];
+      for (int r = 0; r < 16; ++r) {
+        const uint32_t row = (uint32_t)((slot_of(i) + 8 * (r >> 2) + (r & 3)) * N) * kSize;
+        if constexpr (GATED) {
+          const float h = silu(acc[i][0][r]) * acc[i][1][r];
+          __builtin_amdgcn_raw_buffer_store_b16((short)bf16_pair(h, h), ry, (int)(at[0] + row), 0, 0);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float v = acc[i][j][r];   // (a bit cast of the vector's element itself takes element 0)
+            __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v), ry, (int)(at[j] + row), 0, 0);
+          }
         }
       }
-    }
+  };
+  // a whole tile
+  auto run = [&](auto TA) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < decltype(TA)::value; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = f32x16_t{};
+    if constexpr (decltype(TA)::value > 0) read(x0, w0, 0, 0, TA);
+    // Whole rounds of the buffers, then what is left (breaks inside the loop
+    // would cost a full wait at its head).  What the last steps fetch lies
+    // past K: zeros.
+    constexpr int kRound = SX == SW ? SX : SX * SW;
+    auto steps_from = [&](int s, auto J, auto self) __attribute__((always_inline)) {
+      step(s, J, TA);
+      constexpr int j = decltype(J)::value + 1;
+      if constexpr (j < kRound) self(s + 1, std::integral_constant<int, j>{}, self);
+    };
+    auto rest_from = [&](int s, auto J, auto self) __attribute__((always_inline)) {
+      if (s >= steps) return;
+      step(s, J, TA);
+      constexpr int j = decltype(J)::value + 1;
+      if constexpr (j + 1 < kRound) self(s + 1, std::integral_constant<int, j>{}, self);
+    };
+    int s = 0;
+    for (; s + kRound <= steps; s += kRound) steps_from(s, std::integral_constant<int, 0>{}, steps_from);
+    rest_from(s, std::integral_constant<int, 0>{}, rest_from);
+    write(TA);   // (here, so that the loops' accumulators need not meet in the same registers)
+  };
+
+  // the buffers' first filling, in the order in which the steps go on
+  auto fill = [&](int i) __attribute__((always_inline)) {
+    if (SX != SW && i < SW)
+#pragma unroll
+      for (int p = 0; p < WP; ++p) direct_w(kBK * i, wbufs[i], p);
+    if (i < SX)
+#pragma unroll
+      for (int p = 0; p < XP; ++p) direct_x(kBK * i, xbufs[i], p);
+    if (SX == SW && i < SW)
+#pragma unroll
+      for (int p = 0; p < WP; ++p) direct_w(kBK * i, wbufs[i], p);
+  };
+  fill(0);
+  load(0, 0);
+  load(kBK, 1);
+  store(w0, 0, 0);
+  store(w0, 1, 0);
+  fill(1);
+  if constexpr (SW > 2) fill(2);
+  if constexpr (SW > 3) fill(3);
+  load(2 * kBK, 0);
+  asm volatile("" : : "s"(y));   // its scalar load ends here: pending, it would make the loop's first LDS wait a full one
+  // step 0 has landed
+  constexpr int kAhead = !W::kDirect ? 0 : WP * (SW - 1) + XP * (SX - 1);
+  __builtin_amdgcn_s_waitcnt(0x70 | (kAhead < 16 ? kAhead : 15));
+  bare_barrier();
+  // (a wave takes one of the loops as a whole; all pass the same barriers)
+  if (t.sh.count > (TM > 1 ? (2 + wm) * (32 * G) : wm * 32)) {
+    run(std::integral_constant<int, TM>{});
+  } else if (TM > 1 && t.sh.count > wm * (32 * G)) {
+    run(std::integral_constant<int, TM == 1 ? 1 : TM / 2>{});
+  } else {
+    run(std::integral_constant<int, 0>{});
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more when the block gives it back
 }
 
 // x up to here goes through a buffer resource (an offset past it plus a K tail's

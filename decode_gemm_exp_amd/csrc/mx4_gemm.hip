@@ -45,7 +45,7 @@ __global__ __launch_bounds__(kNT) void k_mx4_tile(const uint8_t* __restrict__ we
   __shared__ __attribute__((aligned(128))) char scales_a[kRows * 8], scales_b[kRows * 8];
 
   Share sh;
-  const int nt = find_tile(RaggedRows{nullptr, nullptr, B, B}, 1, blockIdx.x, ntiles, BM, sh);
+  const int nt = find_tile(RaggedRows{nullptr, nullptr, B, B}, 1, blockIdx.x & 7, blockIdx.x >> 3, ntiles, BM, sh);
   if (nt < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3;
@@ -198,9 +198,11 @@ __global__ __launch_bounds__(kNT) void k_mx4_tile(const uint8_t* __restrict__ we
   // (a wave takes one of the two loops as a whole; both pass the same barriers)
   if (!active) {
     run(std::false_type{});
+    __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more when the block gives it back
     return;
   }
   run(std::true_type{});
+  __builtin_amdgcn_s_waitcnt(0);
 #undef UW_MX4_MMA
 
 #pragma unroll
