@@ -32,53 +32,62 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   return e == 255u ? 255u : e > 2u ? e - 2u : 0u;
 }
 
-// |v| / scale as a code 0..7 by its definition: scale is a power of two, so
-// the quotient is exact (below 2^-126 it may lose bits, but there it is far
-// under the first midpoint 0.25)
-__device__ __forceinline__ uint32_t code_of(float v, uint32_t byte) {
-  const float a = __builtin_fabsf(ldexpf(v, 127 - (int)byte));
-  const uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
-  return c | ((__builtin_bit_cast(uint32_t, v) >> 31) << 3);
-}
-
+// Eight values as loaded: BF16 pairs, or floats.
+template <bool F32>
 struct Eight {
-  float v[8];
+  uint32_t w[F32 ? 8 : 4];
 };
 
 template <bool F32>
-__device__ __forceinline__ Eight load8(const void* src, int64_t at) {
-  Eight e;
+__device__ __forceinline__ Eight<F32> load8(const void* src, int64_t at) {
+  Eight<F32> e;
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + at * (F32 ? 4 : 2));
+  const uint4 a = p[0];
+  e.w[0] = a.x; e.w[1] = a.y; e.w[2] = a.z; e.w[3] = a.w;
   if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(src) + at);
-    const float4 a = p[0], b = p[1];
-    e.v[0] = a.x; e.v[1] = a.y; e.v[2] = a.z; e.v[3] = a.w;
-    e.v[4] = b.x; e.v[5] = b.y; e.v[6] = b.z; e.v[7] = b.w;
-  } else {
-    const uint4 a = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(src) + at);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e.v[2 * i] = __builtin_bit_cast(float, w[i] << 16);
-      e.v[2 * i + 1] = __builtin_bit_cast(float, w[i] & 0xFFFF0000u);
-    }
+    const uint4 b = p[1];
+    e.w[4] = b.x; e.w[5] = b.y; e.w[6] = b.z; e.w[7] = b.w;
   }
   return e;
 }
 
-__device__ __forceinline__ uint32_t top8(const Eight& e) {
+// the largest magnitude's bits, as of a float
+template <bool F32>
+__device__ __forceinline__ uint32_t top8(const Eight<F32>& e) {
   uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, e.v[i]) & 0x7FFFFFFFu;
-    m = m > b ? m : b;
+  for (int i = 0; i < (F32 ? 8 : 4); ++i) {
+    if constexpr (F32) {
+      m = max(m, e.w[i] & 0x7FFFFFFFu);
+    } else {
+      m = max(m, max((e.w[i] & 0x7FFFu) << 16, e.w[i] & 0x7FFF0000u));
+    }
   }
   return m;
 }
 
-__device__ __forceinline__ uint32_t pack8(const Eight& e, uint32_t byte) {
+// Codes of eight values over the block's scale.  The scaled conversion divides by
+// the power of two in its scale operand's exponent field, rounds to nearest even
+// and saturates; seven comparisons an element instead took 1.6 times the whole
+// kernel's time.
+template <bool F32>
+__device__ __forceinline__ uint32_t pack8(const Eight<F32>& e, uint32_t byte) {
+  const float s = e8m0_float(byte);
   uint32_t q = 0;
+  if constexpr (F32) {
+    float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) q |= code_of(e.v[i], byte) << (4 * i);
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_bit_cast(float, e.w[i]);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[0], v[1], s, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[2], v[3], s, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[4], v[5], s, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, v[6], v[7], s, 3);
+  } else {
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2_t, e.w[0]), s, 0);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2_t, e.w[1]), s, 1);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2_t, e.w[2]), s, 2);
+    q = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(q, __builtin_bit_cast(bf16x2_t, e.w[3]), s, 3);
+  }
   return byte == 255u ? 0u : q;
 }
 
@@ -88,7 +97,7 @@ __global__ __launch_bounds__(256) void k_quantize_mx4(const void* __restrict__ s
                                                       int64_t ld, uint8_t* __restrict__ elem,
                                                       uint8_t* __restrict__ scale, int64_t stride) {
   const int64_t base = (int64_t)blockIdx.x * (256 * kUnroll) + threadIdx.x;
-  Eight e[kUnroll];
+  Eight<F32> e[kUnroll];
   int64_t row[kUnroll];
   uint32_t col[kUnroll];
 #pragma unroll
@@ -144,7 +153,7 @@ __global__ __launch_bounds__(256) void k_dequantize_mx4(const uint8_t* __restric
 __global__ __launch_bounds__(256) void k_round_mx4(const uint16_t* __restrict__ x, int64_t pieces,
                                                    uint16_t* __restrict__ out) {
   const int64_t p = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const Eight e = load8<false>(x, 8 * (p < pieces ? p : pieces - 1));
+  const Eight<false> e = load8<false>(x, 8 * (p < pieces ? p : pieces - 1));
   const uint32_t byte = scale_byte(quad_max(top8(e)));
   if (p < pieces) reinterpret_cast<uint4*>(out)[p] = unpack8(pack8(e, byte), byte);
 }
