@@ -294,7 +294,8 @@ struct ExpertsCall {
 };
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s);
 hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s);
-hipError_t launch_experts_tile(const ExpertsCall& c, int rows, hipStream_t s);   // rows of a tile: 64, 128 or 256
+// rows of a tile: 64, 128 or 256; spread: blocks start along K at different places
+hipError_t launch_experts_tile(const ExpertsCall& c, int rows, bool spread, hipStream_t s);
 
 hipError_t launch_quantize_mx4(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* elem,
                                uint8_t* scale, hipStream_t s);

@@ -368,31 +368,34 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
 }
 
 // Which kernel: by the rows an expert has on average if every slot is used
-// (the counts themselves are on the device) and the blocks that makes.  The
-// register-fed kernel streams weights for few rows; the LDS tiles rebuild and
-// read each weight once per tile of 64, 128 or 256 rows, but need a block on
-// every CU: with fewer, smaller tiles, and below three quarters of the CUs the
-// register-fed kernel again, up to the rows where its reloading of weights
-// costs more.  Measured (us, register-fed / 64 / 128 / 256):
-//   BF16, 32 experts 2048x2048, 16 rows: 73 / 68 / 68 / 69
-//   BF16, 16 experts 2048x2048, 64 rows: 69 / 42 / 44 / 49
+// (the counts themselves are on the device) and the blocks that makes.  The LDS
+// tiles read each weight once per tile of 64, 128 or 256 rows, but need a block
+// on every CU: with fewer, smaller tiles, and below three quarters of the CUs
+// the register-fed kernel, up to the rows where its reloading of weights costs
+// more.  It also takes UWF1 and MXFP4 weights, which the tiles pass through
+// registers, of experts with few rows.  Measured (us, register-fed / 64 / 128 / 256):
+//   BF16 gated, one token, 2 of 8 experts 14336x4096: 85 / 82 / 82 / 83
+//   BF16, 32 experts 2048x2048, 16 rows: 73 / 51 / 51 / 52
+//   BF16, 16 experts 2048x2048, 64 rows: 69 / 38 / 41 / 46
 //   BF16, 24 experts 1500x1024, 167 rows: 114 / 40 / 33 / 33
 //   BF16 layer, 64 experts 1408x2048, 281 rows: 1902 / 628 / 489 / 469
 //   BF16 gated, 64 experts 1408x2048, 512 rows: 1985 / 600 / 441 / 402
 //   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1438 / 579 / 464 / 356
-//   UWF1, 32 experts 2048x4096, 3 rows: 75 / 106 / 110 / 135
+//   UWF1, 32 experts 2048x4096, 3 rows: 75 / 108 / 109 / 114
 //   MXFP4 14336x4096: 64 rows 35 / 52 / 59 / 69, 128 rows 66 / 53 / 63 / 73
 //   MXFP4, few tiles: 5001x8224, 200 rows 84 / 109 / 125 / 179; 4096x4096, 256 rows 34 / 52 / 63 / 95
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
   const int64_t e = c.r.offsets ? c.w.count : 1;
   const int64_t avg = (c.r.slots + e - 1) / e;
-  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_experts_tile(c, 256, s);   // x past 2 GiB: by pointers
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_experts_tile(c, 256, false, s);   // x past 2 GiB: by pointers
   const int64_t cus = device_cus(), ntiles = (c.w.n + (c.gated ? 127 : 255)) / (c.gated ? 128 : 256);
   auto blocks = [&](int rows) { return ntiles * max_chunks(c.r.slots, c.w.count, rows, c.r.offsets != nullptr); };
-  int rows = avg <= 48 ? 64 : avg <= 256 ? 128 : 256;
+  const bool spread = avg <= 96;   // few rows: the weights' way from memory is what counts
+  int rows = spread ? 64 : avg <= 256 ? 128 : 256;
   while (rows > 64 && blocks(rows) < cus) rows /= 2;
-  if (avg <= 12 || (avg <= 256 && blocks(rows) < cus * 3 / 4)) return launch_experts_rows(c, s);
-  return launch_experts_tile(c, rows, s);
+  if ((avg <= 12 && c.w.form != kFormBf16) || (avg <= 256 && blocks(rows) < cus * 3 / 4))
+    return launch_experts_rows(c, s);
+  return launch_experts_tile(c, rows, spread, s);
 }
 
 }  // namespace uw

@@ -129,7 +129,9 @@ struct Weights<kFormMx4> {
     r = rsrc_of(m.w + (int64_t)e * m.w_stride + n0 * (m.k / 2), (uint64_t)rows * (m.k / 2));
     rs = rsrc_of(m.scale + (int64_t)e * m.scale_stride + n0 * mx4_scale_stride(m.k), (uint64_t)rows * mx4_scale_stride(m.k));
   }
-  __device__ __forceinline__ void load(int k0, int K, int set) {
+  __device__ __forceinline__ void first(int, int) {}
+  // the step from k0 (the one after it begins at k1)
+  __device__ __forceinline__ void load(int k0, int, int K, int set) {
     const bool in = k0 + (int)col < K;
     d[set] = bload16(r, off + (in ? (uint32_t)(k0 / 2) : kOutside));
     sc[set] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)(soff + (in ? (uint32_t)(k0 / 32) : kOutside)), 0, 0);
@@ -171,7 +173,6 @@ struct WeightsPal {
       el[i] = (uint32_t)(n * w.k) + 16u * (tid & 3);
     }
     t = (__builtin_amdgcn_readfirstlane((int)up) ? u : w).table[e];
-    flags(0, (int)w.k);
   }
   __device__ __forceinline__ void flags(int k0, int K) {
     const uint32_t k = k0 < K ? (uint32_t)k0 : 0u;
@@ -181,7 +182,8 @@ struct WeightsPal {
       rw[i] = gload<uint32_t>(t.vrank + ((el[i] + k) >> 11));
     }
   }
-  __device__ __forceinline__ void load(int k0, int K, int set) {   // K % 64 == 0: a step is whole or absent
+  __device__ __forceinline__ void first(int k0, int K) { flags(k0, K); }
+  __device__ __forceinline__ void load(int k0, int k1, int K, int set) {   // K % 64 == 0: a step is whole or absent
     const uint32_t k = k0 < K ? (uint32_t)k0 : 0u;
     verb[set] = 0;
 #pragma unroll
@@ -194,7 +196,7 @@ struct WeightsPal {
       b[set][i] = gload8(p + (v ? 8 : 0));
       verb[set] |= (v ? 1u : 0u) << i;
     }
-    flags(k0 + kBK, K);
+    flags(k1, K);
   }
   __device__ __forceinline__ void store(char* lds, int part, int set) const {
     const int tid = threadIdx.x, i = part;
@@ -213,7 +215,7 @@ template <> struct Weights<kFormPalRun> : WeightsPal<true> {};
 template <int FORM, int BM, bool GATED, bool BIG>
 __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsView vu, RaggedRows rr,
                                                       const uint16_t* __restrict__ x, void* __restrict__ y,
-                                                      int ntiles) {
+                                                      int ntiles, int spread) {
   constexpr int TM = BM / 64;                 // 32-row tiles of a wave; two column tiles
   constexpr int XP = BM / 64;                 // pieces of x a thread moves per step
   using W = Weights<FORM>;
@@ -310,11 +312,22 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   };
 
   const int steps = (K + kBK - 1) / kBK;
+  // spread: each block starts its walk along K elsewhere.  Rows are a power of two
+  // apart as a rule, and blocks that all read the same columns at once meet on
+  // the same memory channels: 32 BF16 experts 2048x2048 of 16 rows 67 -> 51 us
+  // (5.3 TB/s).  With many rows an expert, blocks in step share more through L2
+  // than that costs (8192^3: 856 -> 972 us), so the launcher decides.  Steps past
+  // the last lie past K and fetch zeros.
+  const int rot = spread ? (int)((blockIdx.x * 5u) % (unsigned)steps) : 0;
+  auto step_k = [&](int s) __attribute__((always_inline)) {
+    const int ss = s + rot;
+    return kBK * (s >= steps ? steps : ss >= steps ? ss - steps : ss);
+  };
   auto store = [&](char* wbuf, int part, int set) __attribute__((always_inline)) {
     if constexpr (!W::kDirect) t.w.store(wbuf, part, set);
   };
-  auto load = [&](int k0, int set) __attribute__((always_inline)) {
-    if constexpr (!W::kDirect) t.w.load(k0, K, set);
+  auto load = [&](int s, int set) __attribute__((always_inline)) {
+    if constexpr (!W::kDirect) t.w.load(step_k(s), step_k(s + 1), K, set);
   };
   // Step s: its data is in buffers J % SX and J % SW, that of s + 1 in register
   // set (J + 1) % 2 (what goes through registers) and on its way to the next
@@ -366,11 +379,11 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
 #pragma unroll
     for (int i = 0; i < (kMma > kPieces ? kMma : kPieces); ++i) {
       if (i < kMma) mma_one(1, i);
-      if (i < XP) direct_x(kBK * (s + SX), xcur, i);
-      else if (i < kPieces) direct_w(kBK * (s + SW), wcur, i - XP);
+      if (i < XP) direct_x(step_k(s + SX), xcur, i);
+      else if (i < kPieces) direct_w(step_k(s + SW), wcur, i - XP);
       __builtin_amdgcn_sched_barrier(0);
     }
-    load(kBK * (s + 3), (j + 1) % 2);
+    load(s + 3, (j + 1) % 2);
   };
   // D of the MFMA: lane l, register r: row 8 (r / 4) + 4 (l / 32) + r % 4, column l % 32
   // The tile's rows of y are one buffer resource, so rows behind the last slot
@@ -436,23 +449,24 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   auto fill = [&](int i) __attribute__((always_inline)) {
     if (SX != SW && i < SW)
 #pragma unroll
-      for (int p = 0; p < WP; ++p) direct_w(kBK * i, wbufs[i], p);
+      for (int p = 0; p < WP; ++p) direct_w(step_k(i), wbufs[i], p);
     if (i < SX)
 #pragma unroll
-      for (int p = 0; p < XP; ++p) direct_x(kBK * i, xbufs[i], p);
+      for (int p = 0; p < XP; ++p) direct_x(step_k(i), xbufs[i], p);
     if (SX == SW && i < SW)
 #pragma unroll
-      for (int p = 0; p < WP; ++p) direct_w(kBK * i, wbufs[i], p);
+      for (int p = 0; p < WP; ++p) direct_w(step_k(i), wbufs[i], p);
   };
   fill(0);
+  if constexpr (!W::kDirect) t.w.first(step_k(0), K);
   load(0, 0);
-  load(kBK, 1);
+  load(1, 1);
   store(w0, 0, 0);
   store(w0, 1, 0);
   fill(1);
   if constexpr (SW > 2) fill(2);
   if constexpr (SW > 3) fill(3);
-  load(2 * kBK, 0);
+  load(2, 0);
   asm volatile("" : : "s"(y));   // its scalar load ends here: pending, it would make the loop's first LDS wait a full one
   // step 0 has landed
   constexpr int kAhead = !W::kDirect ? 0 : WP * (SW - 1) + XP * (SX - 1);
@@ -474,37 +488,38 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
 constexpr int64_t kBigBytes = kOutside;
 
 template <int FORM, int BM, bool GATED, bool BIG = false>
-hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
+hipError_t launch_one(const ExpertsCall& c, bool spread, hipStream_t s) {
   const int64_t out = GATED ? 128 : 256, ntiles = (c.w.n + out - 1) / out;
   // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
   const int64_t tiles = max_chunks(c.r.slots, c.w.count, BM, c.r.offsets != nullptr) * ntiles;
   const int64_t grid = (tiles + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_experts_tile<FORM, BM, GATED, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles);
+  hipLaunchKernelGGL((k_experts_tile<FORM, BM, GATED, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x,
+                     c.y, (int)ntiles, (int)spread);
   return hipGetLastError();
 }
 
 template <int FORM, bool GATED>
-hipError_t launch_rows(const ExpertsCall& c, int rows, hipStream_t s) {
-  if (c.r.x_rows * 2 * c.w.k > kBigBytes) return launch_one<FORM, 256, GATED, true>(c, s);
-  if (rows <= 64) return launch_one<FORM, 64, GATED>(c, s);
-  if (rows <= 128) return launch_one<FORM, 128, GATED>(c, s);
-  return launch_one<FORM, 256, GATED>(c, s);
+hipError_t launch_rows(const ExpertsCall& c, int rows, bool spread, hipStream_t s) {
+  if (c.r.x_rows * 2 * c.w.k > kBigBytes) return launch_one<FORM, 256, GATED, true>(c, spread, s);
+  if (rows <= 64) return launch_one<FORM, 64, GATED>(c, spread, s);
+  if (rows <= 128) return launch_one<FORM, 128, GATED>(c, spread, s);
+  return launch_one<FORM, 256, GATED>(c, spread, s);
 }
 
 template <int FORM>
-hipError_t launch_form(const ExpertsCall& c, int rows, hipStream_t s) {
-  return c.gated ? launch_rows<FORM, true>(c, rows, s) : launch_rows<FORM, false>(c, rows, s);
+hipError_t launch_form(const ExpertsCall& c, int rows, bool spread, hipStream_t s) {
+  return c.gated ? launch_rows<FORM, true>(c, rows, spread, s) : launch_rows<FORM, false>(c, rows, spread, s);
 }
 
 }  // namespace
 
-hipError_t launch_experts_tile(const ExpertsCall& c, int rows, hipStream_t s) {
+hipError_t launch_experts_tile(const ExpertsCall& c, int rows, bool spread, hipStream_t s) {
   switch (c.w.form) {
-    case kFormBf16: return launch_form<kFormBf16>(c, rows, s);
-    case kFormPal: return launch_form<kFormPal>(c, rows, s);
-    case kFormPalRun: return launch_form<kFormPalRun>(c, rows, s);
-    default: return launch_form<kFormMx4>(c, rows, s);
+    case kFormBf16: return launch_form<kFormBf16>(c, rows, spread, s);
+    case kFormPal: return launch_form<kFormPal>(c, rows, spread, s);
+    case kFormPalRun: return launch_form<kFormPalRun>(c, rows, spread, s);
+    default: return launch_form<kFormMx4>(c, rows, spread, s);
   }
 }
 
