@@ -39,6 +39,8 @@ struct ExpertsView {
   const ExpertEntry* table;   // UWF1
 };
 
+typedef __attribute__((address_space(3))) char lds_char;
+
 // A load the compiler knows to be from global memory.  Pointers read from the
 // device table have no address space of their own, and flat loads would
 // count with the LDS reads: every wait for one would wait for all.

@@ -7,9 +7,9 @@
 // reuses nothing but x:
 //   * a block owns 16 R rows of one expert's weights and up to 16 Q of its
 //     slots; its four waves walk interleaved windows of K, each loading its
-//     weights straight into registers, two windows deep, and feeding
-//     v_mfma_f32_16x16x32_bf16 with the weights as A (16 output features) and
-//     x as B (16 slots);
+//     weights two windows deep, BF16 and UWF1 straight into registers, MXFP4
+//     through LDS, and feeding v_mfma_f32_16x16x32_bf16 with the weights as A
+//     (16 output features) and x as B (16 slots);
 //   * the order of k inside an MFMA is free as long as A and B agree.  BF16:
 //     MFMA m of a 128-wide window takes k 32 m + 8 g .. +7 in lane group g, so
 //     a load reads 64 contiguous bytes of each of 16 rows.  The byte and
@@ -40,22 +40,19 @@ __device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t byte
 
 __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
-// units of 32 weights a lane takes of a window, and the window's width
-template <int FORM> constexpr int units() { return FORM == kFormMx4 ? 2 : 1; }
-template <int FORM> constexpr int window() { return 128 * units<FORM>(); }
-
-// k of MFMA (u, m)'s eight weights in lane group g, from the window's start
+// BF16 and UWF1: k of MFMA m's eight weights in lane group g, from the start of
+// a window of 128
 template <int FORM>
-__device__ __forceinline__ int k_off(int u, int m, int g) {
-  return FORM == kFormBf16 ? 32 * m + 8 * g : 32 * units<FORM>() * g + 32 * u + 8 * m;
+__device__ __forceinline__ int k_off(int m, int g) {
+  return FORM == kFormBf16 ? 32 * m + 8 * g : 32 * g + 8 * m;
 }
 
 // A block's rows [n0, n0 + rows) of one expert's matrix.
 template <int FORM>
 struct Mat {
-  __amdgpu_buffer_rsrc_t w, scale;   // BF16, MXFP4: from row n0
-  ExpertEntry t;                     // UWF1
-  uint32_t el0, el_end;              // ... its elements [n0 K, (n0 + rows) K)
+  __amdgpu_buffer_rsrc_t w;   // BF16: from row n0
+  ExpertEntry t;              // UWF1
+  uint32_t el0, el_end;       // ... its elements [n0 K, (n0 + rows) K)
 };
 
 template <int FORM>
@@ -68,20 +65,15 @@ __device__ __forceinline__ Mat<FORM> matrix_of(const ExpertsView& v, int e, int6
     m.el_end = (uint32_t)((n0 + rows) * v.k);
     m.w = rsrc_of(m.t.sm + n0 * v.k, (uint64_t)(rows * v.k));
   } else {
-    const int64_t bytes = FORM == kFormBf16 ? 2 * v.k : v.k / 2;
-    m.w = rsrc_of(v.w + (int64_t)e * v.w_stride + n0 * bytes, (uint64_t)(rows * bytes));
-    if constexpr (FORM == kFormMx4) {
-      const int64_t st = mx4_scale_stride(v.k);
-      m.scale = rsrc_of(v.scale + (int64_t)e * v.scale_stride + n0 * st, (uint64_t)(rows * st));
-    }
+    m.w = rsrc_of(v.w + (int64_t)e * v.w_stride + n0 * 2 * v.k, (uint64_t)(rows * 2 * v.k));
   }
   return m;
 }
 
 // A lane's weights of one window of one row, as loaded:
-//   BF16: d[m] = the eight of MFMA m;  MXFP4: d[u] = 32 elements, f = the two
-//   scale bytes;  UWF1: d[0], d[1] = 32 sign+mantissa bytes, d[2] = 32 index
-//   nibbles, or d[2], d[3] = 32 exponent bytes when f (verbatim group)
+//   BF16: d[m] = the eight of MFMA m;  UWF1: d[0], d[1] = 32 sign+mantissa
+//   bytes, d[2] = 32 index nibbles, or d[2], d[3] = 32 exponent bytes when f
+//   (verbatim group)
 struct Raw {
   uint4 d[4];
   uint32_t f;
@@ -109,20 +101,11 @@ __device__ __forceinline__ void load_raw(const Mat<FORM>& m, int row, int K, int
   if constexpr (FORM == kFormBf16) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int k = k0 + k_off<FORM>(0, i, g);
+      const int k = k0 + k_off<FORM>(i, g);
       r.d[i] = bload16(m.w, k < K ? (uint32_t)(row * K + k) * 2u : kOutside);
     }
-  } else if constexpr (FORM == kFormMx4) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int k = k0 + k_off<FORM>(u, 0, g);
-      r.d[u] = bload16(m.w, k < K ? (uint32_t)(row * (K / 2) + k / 2) : kOutside);
-    }
-    const int k = k0 + k_off<FORM>(0, 0, g);   // a multiple of 64: the pair of scales is aligned
-    r.f = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(
-        m.scale, (int)(k < K ? (uint32_t)(row * (int)mx4_scale_stride(K) + k / 32) : kOutside), 0, 0);
   } else {
-    const int k = k0 + k_off<FORM>(0, 0, g);
+    const int k = k0 + k_off<FORM>(0, g);
     const uint32_t at = (uint32_t)row * (uint32_t)K + (uint32_t)k, el = m.el0 + at;
     const bool in = k < K && el < m.el_end;
     r.d[0] = bload16(m.w, in ? at : kOutside);
@@ -139,14 +122,12 @@ __device__ __forceinline__ void load_raw(const Mat<FORM>& m, int row, int K, int
   }
 }
 
-// A operand of MFMA (u, m); scale: of unit u (MXFP4)
+// A operand of MFMA m
 template <int FORM>
-__device__ __forceinline__ bf16x8_t a_frag(const Mat<FORM>& mt, const Raw& r, float scale, int u, int m) {
+__device__ __forceinline__ bf16x8_t a_frag(const Mat<FORM>& mt, const Raw& r, int m) {
   uint4 o;
   if constexpr (FORM == kFormBf16) {
     o = r.d[m];
-  } else if constexpr (FORM == kFormMx4) {
-    o = mx4_unpack8(word4(r.d[u], m), scale);
   } else {
     const int wi = 2 * (m & 1);
     uint32_t e0, e1;
@@ -159,127 +140,25 @@ __device__ __forceinline__ bf16x8_t a_frag(const Mat<FORM>& mt, const Raw& r, fl
   return __builtin_bit_cast(bf16x8_t, o);
 }
 
-// R weight tiles of 16 rows (gated: the first half from W, the second the
-// same rows of U), Q groups of 16 slots
-template <int FORM, int R, int Q, bool GATED>
-__global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsView vu, RaggedRows rr,
-                                                      const uint16_t* __restrict__ x, void* __restrict__ y,
-                                                      int ntiles) {
-  constexpr int U = units<FORM>(), W = window<FORM>();
-  constexpr int RT = GATED ? R / 2 : R;   // distinct output tiles
-  __shared__ f32x4_t red[4 * R * Q * 64];
-  const Share sh = find_share(rr, vw.count, blockIdx.x / (unsigned)ntiles, 16 * Q);
-  if (sh.count == 0) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, g = lane >> 4;
-  const int64_t N = vw.n;
-  const int K = (int)vw.k;
-  const int64_t n0 = (int64_t)(blockIdx.x % (unsigned)ntiles) * (16 * RT);
-  const Mat<FORM> mw = matrix_of<FORM>(vw, sh.expert, n0, 16 * RT);
-  Mat<FORM> mu = mw;
-  if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert, n0, 16 * RT);
-  auto mat = [&](int t) __attribute__((always_inline)) -> const Mat<FORM>& { return GATED && t >= RT ? mu : mw; };
-  auto row_of = [&](int t) __attribute__((always_inline)) { return 16 * (t % RT) + i16; };
+// A block's tile of output rows and chunk of slots.  The chunks of one matrix
+// read the same weights, so a tile's chunks follow each other on one XCD and
+// share them in its L2 (MXFP4 5001x8224, 45 rows: 18.1 -> 15.2 us).  Experts'
+// chunks share little, and all XCDs walking through an expert together do
+// better (MXFP4 layer of 37 tokens over 32 experts: 109 us against 118).
+struct Place {
+  unsigned tile, chunk;
+};
+__device__ __forceinline__ Place place_of(const RaggedRows& rr, unsigned ntiles, unsigned chunks) {
+  if (rr.offsets) return {blockIdx.x % ntiles, blockIdx.x / ntiles};
+  const unsigned turn = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);   // (the grid is a multiple of 8)
+  return {turn / chunks, turn % chunks};
+}
 
-  // x rows of this lane's slots
-  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
-  uint32_t xrow[Q];
-#pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const int b = 16 * q + i16;
-    int64_t row = sh.first + (b < sh.count ? b : 0);
-    if (rr.rows) row = rr.rows[row];
-    xrow[q] = b < sh.count && row >= 0 && row < rr.x_rows ? (uint32_t)(row * K) * 2u : kOutside;
-  }
-
-  const int nwin = (K + W - 1) / W;
-  f32x4_t acc[R][Q];
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  uint32_t top[R] = {};   // MXFP4: the largest scale byte of the lane's rows
-
-  struct Win {
-    Raw r[R];
-    uint4 xv[Q][4 * U];
-  };
-  auto flags = [&](int j, Flags (&f)[R]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < R; ++t) load_flags<FORM>(mat(t), row_of(t), K, W * j + k_off<FORM>(0, 0, g), f[t]);
-  };
-  // windows past the last (whole rounds of four) lie past K and load zeros
-  auto load = [&](int j, const Flags (&f)[R], Win& w) __attribute__((always_inline)) {
-    const int k0 = W * j;
-#pragma unroll
-    for (int t = 0; t < R; ++t) load_raw<FORM>(mat(t), row_of(t), K, k0, g, f[t], w.r[t]);
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-      for (int i = 0; i < 4 * U; ++i) {
-        const int k = k0 + k_off<FORM>(i / 4, i % 4, g);
-        w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
-      }
-  };
-  auto compute = [&](int j, const Win& w) __attribute__((always_inline)) {
-    float scale[R][U] = {};
-    if constexpr (FORM == kFormMx4) {
-      // (the second of a lane's two blocks may lie past K: its scale is padding)
-      const bool second = W * j + k_off<FORM>(1, 0, g) < K;
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const uint32_t lo = w.r[t].f & 255u, hi = second ? w.r[t].f >> 8 : 0u;
-        scale[t][0] = e8m0_float(lo);
-        scale[t][1] = e8m0_float(hi);
-        top[t] = max(top[t], max(lo, hi));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4 * U; ++i)
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const bf16x8_t a = a_frag<FORM>(mat(t), w.r[t], scale[t][i / 4], i / 4, i % 4);
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, w.xv[q][i]), acc[t][q],
-                                                              0, 0, 0);
-      }
-  };
-
-  Win wa, wb;
-  Flags fa[R], fb[R];
-  flags(wave, fa);
-  flags(wave + 4, fb);
-  load(wave, fa, wa);
-  flags(wave + 8, fa);
-  for (int j = wave; j < nwin; j += 8) {
-    load(j + 4, fb, wb);
-    flags(j + 12, fb);
-    compute(j, wa);
-    load(j + 8, fa, wa);
-    flags(j + 16, fa);
-    compute(j + 4, wb);
-  }
-  if constexpr (FORM == kFormMx4) {
-    // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      const uint32_t n = top[t] == 255u ? 0x7FC07FC0u : 0u;
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-        acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(n, n, n, n)),
-                                                            __builtin_bit_cast(bf16x8_t, zero), acc[t][q], 0, 0, 0);
-    }
-  }
-
-  // the waves' sums, added in wave order.  D of the MFMA: lane l holds output
-  // features 4 (l / 16) .. +3 of slot l % 16
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
-  __syncthreads();
+// The four waves' sums, added in wave order and stored.  red: per wave and tile
+// the MFMA's D: lane l holds output features 4 (l / 16) .. +3 of slot l % 16.
+template <int R, int Q, bool GATED>
+__device__ __forceinline__ void finish(const f32x4_t* red, const Share& sh, int64_t n0, int64_t N, void* __restrict__ y) {
+  constexpr int RT = GATED ? R / 2 : R;
   for (int i = threadIdx.x; i < RT * Q * 64; i += 256) {
     const int ln = i & 63, q = (i >> 6) % Q, t = (i >> 6) / Q;
     auto sum = [&](int tt) __attribute__((always_inline)) {
@@ -319,28 +198,293 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   }
 }
 
+// R weight tiles of 16 rows (gated: the first half from W, the second the
+// same rows of U), Q groups of 16 slots
+template <int FORM, int R, int Q, bool GATED>
+__global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsView vu, RaggedRows rr,
+                                                      const uint16_t* __restrict__ x, void* __restrict__ y,
+                                                      int ntiles, int chunks) {
+  constexpr int W = 128;
+  constexpr int RT = GATED ? R / 2 : R;   // distinct output tiles
+  __shared__ f32x4_t red[4 * R * Q * 64];
+  const Place at = place_of(rr, (unsigned)ntiles, (unsigned)chunks);
+  if (at.tile >= (unsigned)ntiles || at.chunk >= (unsigned)chunks) return;
+  const Share sh = find_share(rr, vw.count, at.chunk, 16 * Q);
+  if (sh.count == 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i16 = lane & 15, g = lane >> 4;
+  const int64_t N = vw.n;
+  const int K = (int)vw.k;
+  const int64_t n0 = (int64_t)at.tile * (16 * RT);
+  const Mat<FORM> mw = matrix_of<FORM>(vw, sh.expert, n0, 16 * RT);
+  Mat<FORM> mu = mw;
+  if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert, n0, 16 * RT);
+  auto mat = [&](int t) __attribute__((always_inline)) -> const Mat<FORM>& { return GATED && t >= RT ? mu : mw; };
+  auto row_of = [&](int t) __attribute__((always_inline)) { return 16 * (t % RT) + i16; };
+
+  // x rows of this lane's slots
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
+  uint32_t xrow[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int b = 16 * q + i16;
+    int64_t row = sh.first + (b < sh.count ? b : 0);
+    if (rr.rows) row = rr.rows[row];
+    xrow[q] = b < sh.count && row >= 0 && row < rr.x_rows ? (uint32_t)(row * K) * 2u : kOutside;
+  }
+
+  const int nwin = (K + W - 1) / W;
+  f32x4_t acc[R][Q];
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  struct Win {
+    Raw r[R];
+    uint4 xv[Q][4];
+  };
+  auto flags = [&](int j, Flags (&f)[R]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < R; ++t) load_flags<FORM>(mat(t), row_of(t), K, W * j + k_off<FORM>(0, g), f[t]);
+  };
+  // windows past the last (whole rounds of four) lie past K and load zeros
+  auto load = [&](int j, const Flags (&f)[R], Win& w) __attribute__((always_inline)) {
+    const int k0 = W * j;
+#pragma unroll
+    for (int t = 0; t < R; ++t) load_raw<FORM>(mat(t), row_of(t), K, k0, g, f[t], w.r[t]);
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int k = k0 + k_off<FORM>(i, g);
+        w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+      }
+  };
+  auto compute = [&](const Win& w) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const bf16x8_t a = a_frag<FORM>(mat(t), w.r[t], i);
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, w.xv[q][i]), acc[t][q],
+                                                              0, 0, 0);
+      }
+  };
+
+  Win wa, wb;
+  Flags fa[R], fb[R];
+  flags(wave, fa);
+  flags(wave + 4, fb);
+  load(wave, fa, wa);
+  flags(wave + 8, fa);
+  for (int j = wave; j < nwin; j += 8) {
+    load(j + 4, fb, wb);
+    flags(j + 12, fb);
+    compute(wa);
+    load(j + 8, fa, wa);
+    flags(j + 16, fa);
+    compute(wb);
+  }
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
+  __syncthreads();
+  finish<R, Q, GATED>(red, sh, n0, N, y);
+}
+
+// MXFP4.  Its weights are few bytes a lane, and a wave that loads operands
+// straight into registers asks for 16 pieces of one K position in 16 rows at a
+// time: the load unit takes them one by one and was what the kernel waited for
+// (70 % busy).  So a wave sends its weights and scales to a ring of its own in
+// LDS, rows in whole lines, and reads its operands there; nothing but the wave's
+// own loads is waited for (layer of 37 tokens over 32 experts: 128 -> 109 us;
+// 4096x4096, 256 rows: 34 -> 25 us).
+// A window is 256 k wide: 64 rows of 128 bytes, piece p of row r at 16 (p ^
+// (r / 2 % 8)), so that the 16 lanes of a read hit all banks.
+// XL: x goes the same way, 16 rows of 512 bytes, piece p of row r at 16 (p ^ r).
+// That leaves room for one block a CU instead of two, which one matrix does not
+// mind (14336x4096, without / with: 4 rows 8.5 / 9.1 us, 7 rows 8.9 / 9.1, 10 rows
+// 9.8 / 9.1, 32 rows 17.9 / 15.1), but layers do (32 experts 2048x2048 of 8 rows: 22 / 31 us).
+template <int Q, bool GATED, bool XL>
+__global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView vu, RaggedRows rr,
+                                                     const uint16_t* __restrict__ x, void* __restrict__ y,
+                                                     int ntiles, int chunks) {
+  constexpr int R = 4, RT = GATED ? 2 : 4, kRows = 16 * RT;
+  constexpr int kW = 64 * 128, kS = 64 * 8;   // a wave's weights and scales of a window
+  __shared__ __attribute__((aligned(128))) char w0[4 * kW], w1[4 * kW], s0[4 * kS], s1[4 * kS];
+  constexpr int kX = XL ? 16 * 512 : 4;
+  __shared__ __attribute__((aligned(128))) char x0[4 * kX], x1[4 * kX];
+  const Place at = place_of(rr, (unsigned)ntiles, (unsigned)chunks);
+  if (at.tile >= (unsigned)ntiles || at.chunk >= (unsigned)chunks) return;
+  const Share sh = find_share(rr, vw.count, at.chunk, 16 * Q);
+  if (sh.count == 0) return;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int i16 = lane & 15, g = lane >> 4;
+  const int64_t N = vw.n;
+  const int K = (int)vw.k, st = (int)mx4_scale_stride(K);
+  const int64_t n0 = (int64_t)at.tile * kRows;
+  const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
+  auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
+    return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * (K / 2), (uint64_t)(rows * (K / 2)));
+  };
+  auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {
+    return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + n0 * st, (uint64_t)(rows * st));
+  };
+  const __amdgpu_buffer_rsrc_t ww = weights(vw), ws = scales(vw);
+  const __amdgpu_buffer_rsrc_t uw = GATED ? weights(vu) : ww, us = GATED ? scales(vu) : ws;
+
+  // x rows of this lane's slots
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
+  constexpr int XR = XL ? 8 : Q;
+  uint32_t xrow[XR];
+#pragma unroll
+  for (int q = 0; q < XR; ++q) {
+    const int b = XL ? 2 * q + (lane >> 5) : 16 * q + i16;
+    int64_t row = sh.first + (b < sh.count ? b : 0);
+    if (rr.rows) row = rr.rows[row];
+    xrow[q] = b < sh.count && row >= 0 && row < rr.x_rows ? (uint32_t)(row * K) * 2u : kOutside;
+  }
+
+  f32x4_t acc[R][Q];
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  uint32_t top[R] = {};   // the largest scale byte of the lane's rows
+
+  // Load i of eight takes rows 8 i .. 8 i + 7, eight lanes a row; of the 64 rows
+  // the gated form has W's first, then U's.
+  const int pr = lane >> 3;                                   // row of the eight
+  auto load = [&](int j, char* wbuf, char* sbuf, char* xbuf, uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
+    const int k0 = 256 * j;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool u = GATED && i >= 4;
+      const int r = 8 * (u ? i - 4 : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
+      const uint32_t off = k0 + 32 * piece < K ? (uint32_t)(r * (K / 2) + (k0 / 2 + 16 * piece)) : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(u ? uw : ww, (lds_char*)(wbuf + wave * kW + 1024 * i), 16, (int)off, 0,
+                                               0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {   // scales, two lanes a row (the second four may be the next row's: not used)
+      const int r = GATED ? lane >> 1 : 32 * i + (lane >> 1);
+      const uint32_t off = k0 + 128 * (lane & 1) < K ? (uint32_t)(r * st + 8 * j + 4 * (lane & 1)) : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(GATED && i ? us : ws, (lds_char*)(sbuf + wave * kS + 256 * i), 4,
+                                               (int)off, 0, 0, 0);
+    }
+    if constexpr (XL) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = k0 + 8 * ((lane & 31) ^ (2 * i + (lane >> 5)));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char*)(xbuf + wave * kX + 1024 * i), 16,
+                                                 (int)(k < K ? xrow[i] + 2u * (uint32_t)k : kOutside), 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int k = k0 + 64 * g + 8 * i;
+          xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+        }
+    }
+  };
+  auto compute = [&](int j, const char* wbuf, const char* sbuf, const char* xbuf, const uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
+    const bool in0 = 256 * j + 64 * g < K, in1 = 256 * j + 64 * g + 32 < K;
+    float scale[R][2];
+    uint4 d[R][2];
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      const int r = 16 * t + i16;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        d[t][u] = *reinterpret_cast<const uint4*>(wbuf + wave * kW + r * 128 + (((2 * g + u) ^ (r >> 1 & 7)) << 4));
+      const uint32_t f = *reinterpret_cast<const uint16_t*>(sbuf + wave * kS + r * 8 + 2 * g);
+      const uint32_t lo = in0 ? f & 255u : 0u, hi = in1 ? f >> 8 : 0u;
+      scale[t][0] = e8m0_float(lo);
+      scale[t][1] = e8m0_float(hi);
+      top[t] = max(top[t], max(lo, hi));
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      uint4 xl;
+      if constexpr (XL) xl = *reinterpret_cast<const uint4*>(xbuf + wave * kX + i16 * 512 + (((8 * g + i) ^ i16) << 4));
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, mx4_unpack8(word4(d[t][i / 4], i % 4), scale[t][i / 4]));
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+          acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, XL ? xl : xv[q][i]), acc[t][q],
+                                                              0, 0, 0);
+      }
+    }
+  };
+
+  // windows past the last (whole rounds of four) lie past K and load zeros
+  const int nwin = (K + 255) / 256;
+  uint4 xa[Q][8], xb[Q][8];
+  load(wave, w0, s0, x0, xa);
+  for (int j = wave; j < nwin; j += 8) {
+    load(j + 4, w1, s1, x1, xb);
+    compute(j, w0, s0, x0, xa);
+    load(j + 8, w0, s0, x0, xa);
+    compute(j + 4, w1, s1, x1, xb);
+  }
+  // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int t = 0; t < R; ++t) {
+    const uint32_t n = top[t] == 255u ? 0x7FC07FC0u : 0u;
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+      acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(n, n, n, n)),
+                                                          __builtin_bit_cast(bf16x8_t, zero), acc[t][q], 0, 0, 0);
+  }
+
+  __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
+  __syncthreads();
+  f32x4_t* red = reinterpret_cast<f32x4_t*>(w0);
+  static_assert(4 * R * Q * 64 * 16 <= 4 * kW, "the sums fit one ring buffer");
+#pragma unroll
+  for (int t = 0; t < R; ++t)
+#pragma unroll
+    for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
+  __syncthreads();
+  finish<R, Q, GATED>(red, sh, n0, N, y);
+}
+
 template <int FORM, int R, int Q, bool GATED>
 hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   const int64_t rows = 16 * (GATED ? R / 2 : R), ntiles = (c.w.n + rows - 1) / rows;
-  const int64_t grid = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr) * ntiles;
+  const int64_t chunks = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr);
+  const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,
-                     c.y, (int)ntiles);
+  if constexpr (FORM == kFormMx4) {
+    // one matrix and slots mostly filled: x through LDS
+    auto k = Q == 1 && !c.r.offsets && c.r.slots > 7 ? k_experts_mx4<1, GATED, true> : k_experts_mx4<Q, GATED, false>;
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
+  } else {
+    hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,
+                       c.y, (int)ntiles, (int)chunks);
+  }
   return hipGetLastError();
 }
 
-// MXFP4 weights are few bytes a tile beside x's: four tiles a wave share each x
-// fragment.  The other forms do better with two and more waves (one token,
-// two of eight experts, us with 2 / 4: BF16 84 / 115, UWF1 70 / 75, MXFP4 37 / 36; MXFP4
-// layer of 37 tokens over 32 experts 158 / 128).
+// Tiles a wave: two and more waves for BF16 and UWF1 (one token, two of eight
+// experts, us with 2 / 4: BF16 84 / 115, UWF1 70 / 75).
 template <int FORM, int Q, bool GATED>
 hipError_t launch_r(const ExpertsCall& c, hipStream_t s) {
   return launch_one<FORM, FORM == kFormMx4 ? 4 : 2, Q, GATED>(c, s);
 }
 
 // Two groups of 16 slots where experts have more than 16 rows as a rule and the
-// blocks still fill the chip (MXFP4 14336x4096, 32 rows: 22.4 / 18.8 us; 5001x8224, 45 rows,
-// half the blocks: 23 / 34 us).
+// blocks still fill the chip (us with one / two:
+// MXFP4 14336x4096, 64 rows 27.5 / 25.3; 5001x8224, 200 rows 65 / 58; BF16 5120x5120, 64 rows 57 / 40).
 template <int FORM, bool GATED>
 hipError_t launch_form(const ExpertsCall& c, int64_t avg, hipStream_t s) {
   const int64_t rows = 16 * (FORM == kFormMx4 ? 4 : 2) / (GATED ? 2 : 1);
@@ -381,9 +525,10 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
 //   BF16 layer, 64 experts 1408x2048, 281 rows: 1902 / 628 / 489 / 469
 //   BF16 gated, 64 experts 1408x2048, 512 rows: 1985 / 600 / 441 / 402
 //   UWF1 gated, 16 experts 2048x2048, 1024 rows: 1438 / 579 / 464 / 356
-//   UWF1, 32 experts 2048x4096, 3 rows: 75 / 108 / 109 / 114
-//   MXFP4 14336x4096: 64 rows 35 / 52 / 59 / 69, 128 rows 66 / 53 / 63 / 73
-//   MXFP4, few tiles: 5001x8224, 200 rows 84 / 109 / 125 / 179; 4096x4096, 256 rows 34 / 52 / 63 / 95
+//   UWF1, 32 experts 2048x4096, 3 rows: 75 / 106 / 108 / 114;  16 experts 2048x2048, 48 rows 62 / 53 / 54
+//   MXFP4, 16 experts 2048x2048: 32 rows 25 / 29 / 31, 64 rows 38 / 33 / 35, 128 rows 61 / 46 / 37
+//   MXFP4 14336x4096: 64 rows 25 / 52 / 59, 128 rows 45 / 55 / 60, 256 rows 74 / 58 / 61
+//   MXFP4, few tiles: 5001x8224, 200 rows 58 / 109 / 125; 4096x4096, 256 rows 25 / 52 / 63
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
   const int64_t e = c.r.offsets ? c.w.count : 1;
   const int64_t avg = (c.r.slots + e - 1) / e;
@@ -393,7 +538,8 @@ hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
   const bool spread = avg <= 96;   // few rows: the weights' way from memory is what counts
   int rows = spread ? 64 : avg <= 256 ? 128 : 256;
   while (rows > 64 && blocks(rows) < cus) rows /= 2;
-  if ((avg <= 12 && c.w.form != kFormBf16) || (avg <= 256 && blocks(rows) < cus * 3 / 4))
+  const int64_t few = c.w.form == kFormBf16 ? 0 : c.w.form == kFormMx4 ? 40 : 12;
+  if (avg <= few || (avg <= 256 && blocks(rows) < cus * 3 / 4))
     return launch_experts_rows(c, s);
   return launch_experts_tile(c, rows, spread, s);
 }

@@ -69,7 +69,6 @@ struct Weights;
 // what a K tail or a row index outside x reads where x goes by pointers
 __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
-typedef __attribute__((address_space(3))) char lds_char;
 
 // A block barrier without a fence: a fence would wait for everything that is on
 // its way to LDS.  The caller has waited for what must have landed.
