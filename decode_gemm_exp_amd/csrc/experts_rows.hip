@@ -465,8 +465,9 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorNotSupported;
   if constexpr (FORM == kFormMx4) {
-    // one matrix and slots mostly filled: x through LDS
-    auto k = Q == 1 && !c.r.offsets && c.r.slots > 7 ? k_experts_mx4<1, GATED, true> : k_experts_mx4<Q, GATED, false>;
+    auto k = k_experts_mx4<Q, GATED, false>;
+    if constexpr (Q == 1 && !GATED)
+      if (!c.r.offsets && c.r.slots > 7) k = k_experts_mx4<1, false, true>;   // one matrix, slots mostly filled
     hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
   } else {
     hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,

@@ -496,8 +496,8 @@ uw_status uw_sync_status(const uw_matrix* m, void* stream);
  * low nibble of byte i.  Scales are [rows][UW_MX4_SCALE_STRIDE(cols)] bytes:
  * cols / 32 of them, then padding up to a multiple of four (written as 0,
  * never used), so that a row's scales start on a 4-byte boundary; without
- * padding whenever cols is a multiple of 128.  cols must be a multiple of 32
- * (UW_ERR_UNSUPPORTED).  (saidapartage.blog, section "Un complément, pas un
+ * padding whenever cols is a multiple of 128.  cols must be a multiple of 32;
+ * rows and cols are at most 2^20 (UW_ERR_UNSUPPORTED).  (saidapartage.blog, section "Un complément, pas un
  * remplaçant": quantised weights are the other half of what is served.) */
 #define UW_MX4_SCALE_STRIDE(cols) (((cols) + 127) / 128 * 4)
 
@@ -577,8 +577,8 @@ uw_status uw_plan_experts(const int32_t* ids_dev, int64_t tokens, int32_t expert
 
 /* The experts' weights of one projection, W_e[n][k] for e < count, in one of
  * three forms.  The set keeps the pointers; the weights stay the caller's and
- * must outlive it.  k must be a multiple of 32, count <= 1024
- * (UW_ERR_UNSUPPORTED).
+ * must outlive it.  k must be a multiple of 32, n and k at most 2^20, count
+ * <= 1024 (UW_ERR_UNSUPPORTED).
  *   uw_experts_bf16   BF16, expert e at w_dev + e * stride elements (0: n * k;
  *                     a multiple of 8), rows contiguous
  *   uw_experts_mx4    MXFP4, expert e's elements and scales e * their stride

@@ -52,6 +52,8 @@ def test_mx4_product_refusals(uw):
     assert size(0, 64, 4, 0, ctypes.byref(n)) == INVALID
     assert size(64, 65, 4, 0, ctypes.byref(n)) == UNSUPPORTED
     assert size(64, 64, 1 << 31, 0, ctypes.byref(n)) == UNSUPPORTED
+    assert size((1 << 20) + 1, 64, 4, 0, ctypes.byref(n)) == UNSUPPORTED
+    assert size(64, (1 << 20) + 32, 4, 0, ctypes.byref(n)) == UNSUPPORTED
     m = uw._lib.uw_matmul_mx4
     assert m(None, P, 64, 64, P, 4, P, 0, None, 0, None) == INVALID
     assert m(P, P, 64, 64, P + 2, 4, P, 0, None, 0, None) == INVALID

@@ -404,6 +404,61 @@ def test_sets_that_do_not_fit_are_refused(uw):
         assert err.value.status == -2
 
 
+# Enough blocks for the LDS tiles of 64, 128 and 256 rows (and, of MXFP4 and UWF1, the
+# register-fed kernel's two groups of slots): counts around `per`, none for some
+# experts, a K tail, partly filled tiles of rows and of columns.
+@pytest.mark.parametrize("experts,per,n,k", [(40, 20, 1290, 192), (300, 20, 260, 64), (30, 150, 1100, 192),
+                                             (13, 300, 2500, 64), (4, 1100, 2564, 320), (12, 400, 2052, 1088)])
+@pytest.mark.parametrize("form", FORMS)
+def test_many_rows(uw, form, experts, per, n, k):
+    g = torch.Generator().manual_seed(experts + per)
+    counts = torch.randint(per // 2, per + per // 2, (experts,), generator=g).tolist()
+    counts[experts // 2] = 0
+    counts[1] = 1
+    h, wv = make_set(uw, form, weights(g, experts, n, k, outliers=form == "uwf1"))
+    h2, uv = make_set(uw, form, weights(g, experts, n, k))
+    x_rows = 500
+    x = torch.randn(x_rows, k, generator=g).bfloat16()
+    off, rows = ragged(g, counts, x_rows)
+    s, pad = len(rows), 70                     # capacity beyond the last slot
+    rows_p = torch.cat([rows, torch.full((pad,), 1 << 30, dtype=torch.int32)])
+    dev = [t.to(DEV) for t in (off, rows_p, x)]
+    y = torch.full((s + pad, n), 7.0, device=DEV)
+    uw.uw_matmul_experts(h, *dev, y)
+    assert bool((y[s:] == 7.0).all()), "rows behind the last slot were written"
+    hh = torch.full((s + pad, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    uw.uw_matmul_experts_gated(h2, h, *dev, hh)
+    assert bool((hh[s:] == 7.0).all())
+    for e in range(experts):                   # FP64 on the device, one expert at a time
+        sl = slice(int(off[e]), int(off[e + 1]))
+        xe = x[rows[sl].long()].double().to(DEV)
+        we, ue = wv[e].to(DEV), uv[e].to(DEV)
+        ref, mag = xe @ we.T.contiguous(), xe.abs() @ we.abs().T.contiguous()
+        assert bool(((y[sl].double() - ref).abs() <= k * 2.0 ** -23 * mag).all()), f"expert {e}"
+        gv, ga = xe @ ue.T.contiguous(), xe.abs() @ ue.abs().T.contiguous()
+        want, tol = h_ref(gv, ga, ref, mag, k)
+        assert bool(((hh[sl].double() - want).abs() <= tol).all()), f"gated, expert {e}"
+
+
+@pytest.mark.parametrize("form", ["bf16", "mx4"])
+@pytest.mark.parametrize("per", [2, 300])
+def test_x_past_two_gib(uw, form, per):
+    """Row indices whose bytes pass 2^31 and 2^32."""
+    g = torch.Generator().manual_seed(per)
+    n, k, x_rows = 40, 8192, 270000            # 4.4 GB
+    h, wv = make_set(uw, form, weights(g, 2, n, k))
+    x = torch.zeros(x_rows, k, dtype=torch.bfloat16, device=DEV)
+    off = torch.tensor([0, per, 2 * per + 1], dtype=torch.int32)
+    rows = torch.randint(0, x_rows, (2 * per + 1,), generator=g, dtype=torch.int32)
+    rows[0], rows[1], rows[-1] = x_rows - 1, 131072, 0
+    part = torch.randn(x_rows // 1000, k, generator=g).bfloat16()
+    x.view(x_rows // 1000, 1000, k).copy_(part.view(-1, 1, k).to(DEV))   # row r holds part[r // 1000]
+    y = torch.empty(2 * per + 1, n, device=DEV)
+    uw.uw_matmul_experts(h, off.to(DEV), rows.to(DEV), x, y)
+    ref, mag = grouped_ref(off, rows // 1000, part, wv)
+    assert bool(((y.double().cpu() - ref).abs() <= k * 2.0 ** -23 * mag).all())
+
+
 # ------------------------------------------------------------ the layer -----
 
 def layer_ref(r_ids, r_w, experts, x, gv, uv, dv, topk):
@@ -491,6 +546,38 @@ def test_layer_captured(uw, tokens):
         assert torch.equal(replayed, out)
         seen.append(replayed)
     assert not torch.equal(seen[0], seen[1])
+
+
+def test_two_graphs_share_a_workspace(uw):
+    """Two captured layers of different sizes with one workspace, replayed in turn on one stream."""
+    g = torch.Generator().manual_seed(17)
+    experts, topk, n, k = 5, 2, 96, 160
+    sets = [make_set(uw, "mx4", weights(g, experts, *s))[0] for s in ((n, k), (n, k), (k, n))]
+    nb = uw.uw_workspace_size_expert_mlp(sets[0], sets[2], 500, topk)
+    ws = torch.empty(nb, dtype=torch.uint8, device=DEV)
+    jobs = []
+    for tokens in (3, 500):
+        l, x = torch.randn(tokens, experts, generator=g).to(DEV), torch.randn(tokens, k, generator=g).bfloat16().to(DEV)
+        r, out = uw.Routing(tokens, experts, topk, DEV), torch.empty(tokens, k, dtype=torch.bfloat16, device=DEV)
+
+        def step(l=l, x=x, r=r, out=out):
+            uw.uw_route_experts(l, r)
+            uw.uw_expert_mlp(*sets, r, x, out, ws)
+
+        step()
+        torch.cuda.synchronize()
+        want = out.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step()
+        jobs.append((graph, out, want, step))  # (step holds what the graph reads)
+    for _ in range(3):
+        for graph, out, _, _ in jobs:
+            out.zero_()
+            graph.replay()
+        torch.cuda.synchronize()
+        for _, out, want, _ in jobs:
+            assert torch.equal(out, want)
 
 
 def test_two_streams_at_once(uw):
