@@ -10,7 +10,9 @@
 //
 // Bound: HBM, 2 (or 4) + 0.53 bytes an element.  Four lanes share a block,
 // eight elements each, so every load and store of a wave is contiguous, and
-// the block's maximum takes two lane permutes.
+// the block's maximum takes two lane permutes.  The scaled conversion
+// instructions round as the definition does.  14336x4096: quantise 23 us, dequantise
+// 22 us (149 MB each, 6.5 TB/s, part of it cached; by shifts and compares 47 us).
 #include "experts.h"
 
 namespace uw {
