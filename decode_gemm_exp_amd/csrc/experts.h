@@ -79,6 +79,15 @@ struct Share {
   int count;
 };
 
+// Offsets to [0, slots].  All five are loaded before the first is touched (left
+// to itself the compiler loads and waits one by one, a microsecond each at the
+// start of every block).
+__device__ __forceinline__ void clamp_all(int32_t (&o)[5], int64_t slots) {
+  asm volatile("" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]), "+v"(o[4]));
+#pragma unroll
+  for (int i = 0; i < 5; ++i) o[i] = o[i] < 0 ? 0 : (int64_t)o[i] < slots ? o[i] : (int32_t)slots;
+}
+
 // Chunk `j` of the experts' slots cut into chunks of at most `chunk`: expert
 // e has ceil(rows_e / chunk).  Every wave searches by itself, without a
 // barrier: a lane holds four consecutive experts, one wave-wide prefix sum
@@ -101,9 +110,9 @@ __device__ __forceinline__ Share find_share(const RaggedRows& r, int experts, in
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
       const int e = e0 + 4 * lane + i;
-      const int32_t v = r.offsets[e < experts ? e : experts];
-      o[i] = v < 0 ? 0 : (int64_t)v < r.slots ? v : (int32_t)r.slots;
+      o[i] = r.offsets[e < experts ? e : experts];
     }
+    clamp_all(o, r.slots);
     int c[4], mine = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -172,9 +181,9 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, int x
 #pragma unroll
     for (int i = 0; i < 5; ++i) {
       const int e = e0 + 4 * lane + i;
-      const int32_t v = r.offsets[e < experts ? e : experts];
-      o[i] = v < 0 ? 0 : (int64_t)v < r.slots ? v : (int32_t)r.slots;
+      o[i] = r.offsets[e < experts ? e : experts];
     }
+    clamp_all(o, r.slots);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       c[i] = o[i + 1] > o[i] ? (int)(((int64_t)o[i + 1] - o[i] + chunk - 1) / chunk) : 0;
@@ -188,13 +197,14 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, int x
     }
     return sum;   // inclusive over lanes
   };
+  int32_t o[5] = {};
+  int c[4] = {}, sum = 0;
   if (!r.offsets) {
     total = (r.slots + chunk - 1) / chunk;
   } else {
     for (int e0 = 0; e0 < experts; e0 += 256) {
-      int32_t o[5];
-      int c[4];
-      total += __builtin_amdgcn_readlane(round(e0, o, c), 63);
+      sum = round(e0, o, c);
+      total += __builtin_amdgcn_readlane(sum, 63);
     }
   }
   const int64_t tiles = total * ntiles, share = (tiles + 7) / 8;
@@ -209,9 +219,7 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, int x
   }
   int64_t before = 0;   // chunks of the experts before this round's
   for (int e0 = 0; e0 < experts; e0 += 256) {
-    int32_t o[5];
-    int c[4];
-    const int sum = round(e0, o, c);
+    if (experts > 256) sum = round(e0, o, c);   // (else as it was)
     const int mine = c[0] + c[1] + c[2] + c[3];
     const int64_t lo = (before + sum - mine) * ntiles, hi = (before + sum) * ntiles;
     const uint64_t hit = __ballot(at >= lo && at < hi);

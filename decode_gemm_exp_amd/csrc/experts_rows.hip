@@ -225,12 +225,17 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   // x rows of this lane's slots
   const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
   uint32_t xrow[Q];
+  int32_t row[Q];   // (fewer than 2^31 slots)
+#pragma unroll
+  for (int q = 0; q < Q; ++q) row[q] = (int32_t)sh.first + (16 * q + i16 < sh.count ? 16 * q + i16 : 0);
+  if (rr.rows) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) row[q] = rr.rows[row[q]];
+  }
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    const int b = 16 * q + i16;
-    int64_t row = sh.first + (b < sh.count ? b : 0);
-    if (rr.rows) row = rr.rows[row];
-    xrow[q] = b < sh.count && row >= 0 && row < rr.x_rows ? (uint32_t)(row * K) * 2u : kOutside;
+    const bool in = (16 * q + i16 < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
+    xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
   }
 
   const int nwin = (K + W - 1) / W;
@@ -341,12 +346,13 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
   const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
   constexpr int XR = XL ? 8 : Q;
   uint32_t xrow[XR];
+  int32_t row[XR];
+  auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 2 * q + (lane >> 5) : 16 * q + i16; };
 #pragma unroll
-  for (int q = 0; q < XR; ++q) {
-    const int b = XL ? 2 * q + (lane >> 5) : 16 * q + i16;
-    int64_t row = sh.first + (b < sh.count ? b : 0);
-    if (rr.rows) row = rr.rows[row];
-    xrow[q] = b < sh.count && row >= 0 && row < rr.x_rows ? (uint32_t)(row * K) * 2u : kOutside;
+  for (int q = 0; q < XR; ++q) row[q] = (int32_t)sh.first + (slot(q) < sh.count ? slot(q) : 0);   // (fewer than 2^31 slots)
+  if (rr.rows) {
+#pragma unroll
+    for (int q = 0; q < XR; ++q) row[q] = rr.rows[row[q]];
   }
 
   f32x4_t acc[R][Q];
@@ -359,7 +365,7 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
   // Load i of eight takes rows 8 i .. 8 i + 7, eight lanes a row; of the 64 rows
   // the gated form has W's first, then U's.
   const int pr = lane >> 3;                                   // row of the eight
-  auto load = [&](int j, char* wbuf, char* sbuf, char* xbuf, uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
+  auto load_w = [&](int j, char* wbuf, char* sbuf) __attribute__((always_inline)) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
     const int k0 = 256 * j;
 #pragma unroll
@@ -371,12 +377,15 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
                                                0, 0);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {   // scales, two lanes a row (the second four may be the next row's: not used)
+    for (int i = 0; i < 2; ++i) {   // scales, two lanes a row
       const int r = GATED ? lane >> 1 : 32 * i + (lane >> 1);
       const uint32_t off = k0 + 128 * (lane & 1) < K ? (uint32_t)(r * st + 8 * j + 4 * (lane & 1)) : kOutside;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(GATED && i ? us : ws, (lds_char*)(sbuf + wave * kS + 256 * i), 4,
                                                (int)off, 0, 0, 0);
     }
+  };
+  auto load_x = [&](int j, char* xbuf, uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
+    const int k0 = 256 * j;
     if constexpr (XL) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -428,11 +437,19 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
   // windows past the last (whole rounds of four) lie past K and load zeros
   const int nwin = (K + 255) / 256;
   uint4 xa[Q][8], xb[Q][8];
-  load(wave, w0, s0, x0, xa);
+  load_w(wave, w0, s0);   // (on its way while the row indices arrive)
+#pragma unroll
+  for (int q = 0; q < XR; ++q) {
+    const bool in = (slot(q) < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
+    xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
+  }
+  load_x(wave, x0, xa);
   for (int j = wave; j < nwin; j += 8) {
-    load(j + 4, w1, s1, x1, xb);
+    load_w(j + 4, w1, s1);
+    load_x(j + 4, x1, xb);
     compute(j, w0, s0, x0, xa);
-    load(j + 8, w0, s0, x0, xa);
+    load_w(j + 8, w0, s0);
+    load_x(j + 8, x0, xa);
     compute(j + 4, w1, s1, x1, xb);
   }
   // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero

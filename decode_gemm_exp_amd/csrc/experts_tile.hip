@@ -250,12 +250,17 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   } t;
   t.nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, ntiles, BM, t.sh);
   if (t.nt < 0) return;
+  int32_t rows[XP];   // (fewer than 2^31 slots); all indices loaded before one is used
+#pragma unroll
+  for (int i = 0; i < XP; ++i) rows[i] = (int32_t)t.sh.first + (tid / 8 + 64 * i < t.sh.count ? tid / 8 + 64 * i : 0);
+  if (rr.rows) {
+#pragma unroll
+    for (int i = 0; i < XP; ++i) rows[i] = rr.rows[rows[i]];
+  }
 #pragma unroll
   for (int i = 0; i < XP; ++i) {
-    const int b = tid / 8 + 64 * i;
-    int64_t row = t.sh.first + (b < t.sh.count ? b : 0);
-    if (rr.rows) row = rr.rows[row];
-    const bool in = row >= 0 && row < rr.x_rows;
+    const int64_t row = rows[i];
+    const bool in = (row >= 0) & (row < rr.x_rows);
     t.xo[i] = in ? (uint32_t)(2 * (row * K + xcol)) : kOutside;
     t.xp[i] = in ? x + row * K + xcol : nullptr;
   }

@@ -185,12 +185,13 @@ def _ptr(t) -> int | None:
 # torch's current stream as a raw handle: a tenth of the time of building a
 # Stream object, which small calls notice
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)   # once torch's GPU state is there
 
 
 def _stream(stream) -> int | None:
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -573,7 +574,9 @@ def _want(t: torch.Tensor, what: str, dtype, shape, dev: int) -> int:
 
 def _current() -> int:
     """The current device; without one every tensor is refused as being elsewhere."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() or torch.cuda.is_available() else -2
+    if torch.cuda.is_initialized():
+        return _device()
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
 
 
 def _on_device(t: torch.Tensor, what: str, dev: int) -> None:
@@ -583,10 +586,16 @@ def _on_device(t: torch.Tensor, what: str, dev: int) -> None:
 
 def _rows2d(t: torch.Tensor, what: str, dev: int) -> int:
     """Row stride in elements of a 2-D tensor whose rows are contiguous."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: two dimensions with contiguous rows expected")
-    _on_device(t, what, dev)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    if t.get_device() != dev:
+        _on_device(t, what, dev)
+    shape = t.shape
+    if len(shape) == 2:
+        if t.is_contiguous():
+            return shape[1]
+        ld, step = t.stride()
+        if shape[1] <= 1 or step == 1:
+            return ld if shape[0] > 1 else shape[1]
+    raise ValueError(f"{what}: two dimensions with contiguous rows expected")
 
 
 def _ws(ws: torch.Tensor | None, dev: int) -> tuple[int | None, int]:
@@ -667,8 +676,8 @@ class Routing:
                    torch.empty(experts + 1, dtype=torch.int32, device=device),
                    torch.zeros(tokens * topk, dtype=torch.int32, device=device), pair(torch.int32))
         self._ws = torch.empty(n.value, dtype=torch.uint8, device=device) if n.value else None
-        self._ptrs = tuple(t.data_ptr() for t in self._t)
-        self._ws_args = (self._ws.data_ptr(), n.value) if n.value else (None, 0)
+        self._ptrs = tuple(_vp(t.data_ptr()) for t in self._t)
+        self._ws_args = (_vp(self._ws.data_ptr()), n.value) if n.value else (None, 0)
         self._dev = self._t[2].get_device()
 
     tokens = property(lambda self: self._shape[0])
