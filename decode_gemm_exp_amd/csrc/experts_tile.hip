@@ -6,10 +6,11 @@
 // gate rows and the same 128 up rows, 32 by 32 interleaved so that a wave
 // holds both factors of its outputs).  Eight waves, two along the slots and
 // four along the columns, each BM/2 x 64.  K advances 64 at a time:
-//   * K goes through a ring of LDS buffers; step s runs its MFMAs from one, fragments one 16-wide slice ahead
-//     of use.  x and BF16 weights go straight from memory to LDS (16 bytes a
-//     lane, no registers); UWF1 and MXFP4 weights through registers, rebuilt
-//     to BF16 once per block, loaded two steps ahead and stored one ahead;
+//   * K goes through a ring of LDS buffers; step s runs its MFMAs from one,
+//     fragments one 16-wide slice ahead of use.  x and BF16 weights go straight
+//     from memory to LDS (16 bytes a lane, no registers); UWF1 and MXFP4 weights
+//     through registers, rebuilt to BF16 once per block, loaded two steps ahead
+//     and stored one ahead;
 //   * the one barrier of a step stands before its last slice's MFMAs, so the
 //     next step's first fragments travel while those run, and the buffer the
 //     step leaves is refilled right behind it;
