@@ -6,7 +6,7 @@
 // experts that have rows, so the kernel keeps many bytes of them in flight and
 // reuses nothing but x:
 //   * a block owns 16 R rows of one expert's weights and up to 16 Q of its
-//     slots; its four waves walk interleaved windows of K, each loading its
+//     slots; its waves (four as a rule) walk interleaved windows of K, each loading its
 //     weights two windows deep, BF16 and UWF1 straight into registers, MXFP4
 //     through LDS, and feeding v_mfma_f32_16x16x32_bf16 with the weights as A
 //     (16 output features) and x as B (16 slots);
@@ -15,7 +15,7 @@
 //     a load reads 64 contiguous bytes of each of 16 rows.  The byte and
 //     nibble forms give lane group g a run of 32 (MXFP4: 64) consecutive k, so
 //     that a lane's weights lie in one UWF1 group or whole MXFP4 blocks;
-//   * the four waves' sums meet in LDS and are added in a fixed order.
+//   * the waves' sums meet in LDS and are added in a fixed order.
 #include "experts.h"
 
 namespace uw {
@@ -154,17 +154,17 @@ __device__ __forceinline__ Place place_of(const RaggedRows& rr, unsigned ntiles,
   return {turn / chunks, turn % chunks};
 }
 
-// The four waves' sums, added in wave order and stored.  red: per wave and tile
+// The waves' sums, added in wave order and stored.  red: per wave and tile
 // the MFMA's D: lane l holds output features 4 (l / 16) .. +3 of slot l % 16.
-template <int R, int Q, bool GATED>
+template <int R, int Q, bool GATED, int NW>
 __device__ __forceinline__ void finish(const f32x4_t* red, const Share& sh, int64_t n0, int64_t N, void* __restrict__ y) {
   constexpr int RT = GATED ? R / 2 : R;
-  for (int i = threadIdx.x; i < RT * Q * 64; i += 256) {
+  for (int i = threadIdx.x; i < RT * Q * 64; i += 64 * NW) {
     const int ln = i & 63, q = (i >> 6) % Q, t = (i >> 6) / Q;
     auto sum = [&](int tt) __attribute__((always_inline)) {
       f32x4_t s = red[(tt * Q + q) * 64 + ln];
 #pragma unroll
-      for (int v = 1; v < 4; ++v) s += red[((v * R + tt) * Q + q) * 64 + ln];
+      for (int v = 1; v < NW; ++v) s += red[((v * R + tt) * Q + q) * 64 + ln];
       return s;
     };
     f32x4_t s = sum(t);
@@ -298,7 +298,7 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
 #pragma unroll
     for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
   __syncthreads();
-  finish<R, Q, GATED>(red, sh, n0, N, y);
+  finish<R, Q, GATED, 4>(red, sh, n0, N, y);
 }
 
 // MXFP4.  Its weights are few bytes a lane, and a wave that loads operands
@@ -311,18 +311,22 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
 // A window is 256 k wide: 64 rows of 128 bytes, piece p of row r at 16 (p ^
 // (r / 2 % 8)), so that the 16 lanes of a read hit all banks.
 // XL: x goes the same way, 16 rows of 512 bytes, piece p of row r at 16 (p ^ r).
-// That leaves room for one block a CU instead of two, which one matrix does not
+// That leaves room for one block of four waves a CU instead of two, which one matrix does not
 // mind (14336x4096, without / with: 4 rows 8.5 / 9.1 us, 7 rows 8.9 / 9.1, 10 rows
 // 9.8 / 9.1, 32 rows 17.9 / 15.1), but layers do (32 experts 2048x2048 of 8 rows: 22 / 31 us).
-template <int Q, bool GATED, bool XL>
-__global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView vu, RaggedRows rr,
+// With more blocks than CUs it runs two waves a block, two blocks a CU (us with
+// four / two waves: 5120x5120, 64 rows, 320 blocks 18.5 / 14.4; 14336x4096, 32 rows, 448
+// blocks 15.1 / 13.0; 14 rows, 224 blocks 9.5 / 11.5).  Without XL four waves it is (two /
+// four / eight: one row of 14336x4096 9.7 / 8.0 / 9.3, layer of 37 tokens 111 / 104 / 146).
+template <int Q, bool GATED, bool XL, int NW>
+__global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, ExpertsView vu, RaggedRows rr,
                                                      const uint16_t* __restrict__ x, void* __restrict__ y,
                                                      int ntiles, int chunks) {
   constexpr int R = 4, RT = GATED ? 2 : 4, kRows = 16 * RT;
   constexpr int kW = 64 * 128, kS = 64 * 8;   // a wave's weights and scales of a window
-  __shared__ __attribute__((aligned(128))) char w0[4 * kW], w1[4 * kW], s0[4 * kS], s1[4 * kS];
+  __shared__ __attribute__((aligned(128))) char w0[NW * kW], w1[NW * kW], s0[NW * kS], s1[NW * kS];
   constexpr int kX = XL ? 16 * 512 : 4;
-  __shared__ __attribute__((aligned(128))) char x0[4 * kX], x1[4 * kX];
+  __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
   const Place at = place_of(rr, (unsigned)ntiles, (unsigned)chunks);
   if (at.tile >= (unsigned)ntiles || at.chunk >= (unsigned)chunks) return;
   const Share sh = find_share(rr, vw.count, at.chunk, 16 * Q);
@@ -434,7 +438,7 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
     }
   };
 
-  // windows past the last (whole rounds of four) lie past K and load zeros
+  // windows past the last (whole rounds of the waves) lie past K and load zeros
   const int nwin = (K + 255) / 256;
   uint4 xa[Q][8], xb[Q][8];
   load_w(wave, w0, s0);   // on its way while the row indices arrive
@@ -444,13 +448,13 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
     xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
   }
   load_x(wave, x0, xa);
-  for (int j = wave; j < nwin; j += 8) {
-    load_w(j + 4, w1, s1);
-    load_x(j + 4, x1, xb);
+  for (int j = wave; j < nwin; j += 2 * NW) {
+    load_w(j + NW, w1, s1);
+    load_x(j + NW, x1, xb);
     compute(j, w0, s0, x0, xa);
-    load_w(j + 8, w0, s0);
-    load_x(j + 8, x0, xa);
-    compute(j + 4, w1, s1, x1, xb);
+    load_w(j + 2 * NW, w0, s0);
+    load_x(j + 2 * NW, x0, xa);
+    compute(j + NW, w1, s1, x1, xb);
   }
   // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
@@ -466,13 +470,13 @@ __global__ __launch_bounds__(256) void k_experts_mx4(ExpertsView vw, ExpertsView
   __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
   __syncthreads();
   f32x4_t* red = reinterpret_cast<f32x4_t*>(w0);
-  static_assert(4 * R * Q * 64 * 16 <= 4 * kW, "the sums fit one ring buffer");
+  static_assert(R * Q * 64 * 16 <= kW, "the sums fit one ring buffer");
 #pragma unroll
   for (int t = 0; t < R; ++t)
 #pragma unroll
     for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
   __syncthreads();
-  finish<R, Q, GATED>(red, sh, n0, N, y);
+  finish<R, Q, GATED, NW>(red, sh, n0, N, y);
 }
 
 template <int FORM, int R, int Q, bool GATED>
@@ -482,10 +486,15 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (grid > INT32_MAX) return hipErrorNotSupported;
   if constexpr (FORM == kFormMx4) {
-    auto k = k_experts_mx4<Q, GATED, false>;
-    if constexpr (Q == 1 && !GATED)
-      if (!c.r.offsets && c.r.slots > 7) k = k_experts_mx4<1, false, true>;   // one matrix, slots mostly filled
-    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
+    auto k = k_experts_mx4<Q, GATED, false, 4>;
+    int waves = 4;
+    if constexpr (Q == 1 && !GATED) {
+      if (!c.r.offsets && c.r.slots > 7) {   // one matrix, slots mostly filled
+        waves = grid > device_cus() ? 2 : 4;
+        k = waves == 2 ? k_experts_mx4<1, false, true, 2> : k_experts_mx4<1, false, true, 4>;
+      }
+    }
+    hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * waves), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
   } else {
     hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,
                        c.y, (int)ntiles, (int)chunks);

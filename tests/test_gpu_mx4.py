@@ -170,7 +170,8 @@ def test_product_larger(uw, batch, n, k, act):
 
 # enough blocks for the tiles of 256 and 128 rows (4-bit x) and of 64 rows (BF16 x)
 @pytest.mark.parametrize("batch,n,k,act", [(700, 16500, 160, 1), (300, 23001, 96, 1), (130, 23001, 288, 1),
-                                           (300, 16500, 160, 0), (45, 20000, 288, 0), (8, 20000, 544, 0)])
+                                           (300, 16500, 160, 0), (45, 20000, 288, 0), (8, 20000, 544, 0),
+                                           (9, 700, 2080, 0), (40, 8000, 1120, 0), (16, 16500, 96, 0)])
 def test_product_many_blocks(uw, batch, n, k, act):
     check_product(*product_case(uw, batch, n, k, act, 6))
 
