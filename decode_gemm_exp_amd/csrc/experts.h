@@ -67,7 +67,7 @@ __host__ __device__ constexpr int64_t mx4_scale_stride(int64_t k) { return (k + 
 struct RaggedRows {
   const int32_t* offsets;
   const int32_t* rows;
-  int64_t slots;      // capacity: offsets are clamped to it
+  int64_t slots;      // capacity: offsets are clamped to it, and to their predecessors
   int64_t x_rows;     // rows of x; a row index outside selects a row of zeros
 };
 
@@ -79,20 +79,59 @@ struct Share {
   int count;
 };
 
-// Offsets to [0, slots].  All five are loaded before the first is touched (left
-// to itself the compiler loads and waits one by one, a microsecond each at the
-// start of every block).
-__device__ __forceinline__ void clamp_all(int32_t (&o)[5], int64_t slots) {
+// A lane's four experts of the 256 from e0: their slots' bounds o, their numbers of
+// chunks c; returns the chunks up to and with this lane's.  Every wave of a
+// block does this by itself, without a barrier.  Bounds are the running maximum of
+// the offsets clamped to [0, slots], so that whatever the array holds, the experts'
+// slots are disjoint and inside the capacity (and max_chunks holds); high: the
+// last bound of the experts before e0, 0 at first, and afterwards that of the 256.
+__device__ __forceinline__ int four_experts(const RaggedRows& r, int experts, int e0, int chunk, int32_t& high,
+                                            int32_t (&o)[5], int (&c)[4]) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {
+    const int e = e0 + 4 * lane + i;
+    o[i] = r.offsets[e < experts ? e : experts];
+  }
+  // all five are loaded before the first is touched (left to itself the compiler
+  // loads and waits one by one, a microsecond each at the start of every block)
   asm volatile("" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]), "+v"(o[4]));
 #pragma unroll
-  for (int i = 0; i < 5; ++i) o[i] = o[i] < 0 ? 0 : (int64_t)o[i] < slots ? o[i] : (int32_t)slots;
+  for (int i = 0; i < 5; ++i) o[i] = o[i] < 0 ? 0 : (int64_t)o[i] < r.slots ? o[i] : (int32_t)r.slots;
+  // (a plan ascends, so the maximum is taken only where one does not)
+  bool down = o[0] < high;
+#pragma unroll
+  for (int i = 1; i < 5; ++i) down |= o[i] < o[i - 1];
+  if (__ballot(down)) {
+#pragma unroll
+    for (int i = 1; i < 5; ++i) o[i] = max(o[i], o[i - 1]);
+    int32_t top = max(o[4], high);   // of the lanes up to this one
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int32_t up = __shfl_up(top, d);
+      top = lane >= d ? max(top, up) : top;
+    }
+    const int32_t up = __shfl_up(top, 1), before = lane ? up : high;
+#pragma unroll
+    for (int i = 0; i < 5; ++i) o[i] = max(o[i], before);
+  }
+  high = __builtin_amdgcn_readlane(o[4], 63);
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = (int)(((int64_t)o[i + 1] - o[i] + chunk - 1) / chunk);
+    sum += c[i];
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int up = __shfl_up(sum, d);
+    sum += lane >= d ? up : 0;
+  }
+  return sum;
 }
 
 // Chunk `j` of the experts' slots cut into chunks of at most `chunk`: expert
-// e has ceil(rows_e / chunk).  Every wave searches by itself, without a
-// barrier: a lane holds four consecutive experts, one wave-wide prefix sum
-// per 256 experts.  Offsets are clamped to [0, slots] and to their
-// predecessor, so no content of the array leads outside the slots.
+// e has ceil(rows_e / chunk).
 __device__ __forceinline__ Share find_share(const RaggedRows& r, int experts, int64_t j, int chunk) {
   Share out{0, 0, 0};
   if (!r.offsets) {
@@ -105,26 +144,11 @@ __device__ __forceinline__ Share find_share(const RaggedRows& r, int experts, in
   }
   const int lane = threadIdx.x & 63;
   int64_t before = 0;   // chunks of the experts before this round's
+  int32_t high = 0;
   for (int e0 = 0; e0 < experts; e0 += 256) {
     int32_t o[5];
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const int e = e0 + 4 * lane + i;
-      o[i] = r.offsets[e < experts ? e : experts];
-    }
-    clamp_all(o, r.slots);
-    int c[4], mine = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = o[i + 1] > o[i] ? (int)(((int64_t)o[i + 1] - o[i] + chunk - 1) / chunk) : 0;
-      mine += c[i];
-    }
-    int sum = mine;   // inclusive prefix over lanes
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      sum += lane >= d ? up : 0;
-    }
+    int c[4];
+    const int sum = four_experts(r, experts, e0, chunk, high, o, c), mine = c[0] + c[1] + c[2] + c[3];
     const int64_t lo = before + sum - mine;
     const uint64_t hit = __ballot(j >= lo && j < lo + mine);
     if (hit) {
@@ -176,34 +200,13 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, int x
   out = Share{0, 0, 0};
   const int lane = threadIdx.x & 63;
   int64_t total = 0;
-  auto round = [&](int e0, int32_t (&o)[5], int (&c)[4]) __attribute__((always_inline)) {
-    int mine = 0;
-#pragma unroll
-    for (int i = 0; i < 5; ++i) {
-      const int e = e0 + 4 * lane + i;
-      o[i] = r.offsets[e < experts ? e : experts];
-    }
-    clamp_all(o, r.slots);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = o[i + 1] > o[i] ? (int)(((int64_t)o[i + 1] - o[i] + chunk - 1) / chunk) : 0;
-      mine += c[i];
-    }
-    int sum = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const int up = __shfl_up(sum, d);
-      sum += lane >= d ? up : 0;
-    }
-    return sum;   // inclusive over lanes
-  };
-  int32_t o[5] = {};
+  int32_t o[5] = {}, high = 0;
   int c[4] = {}, sum = 0;
   if (!r.offsets) {
     total = (r.slots + chunk - 1) / chunk;
   } else {
     for (int e0 = 0; e0 < experts; e0 += 256) {
-      sum = round(e0, o, c);
+      sum = four_experts(r, experts, e0, chunk, high, o, c);
       total += __builtin_amdgcn_readlane(sum, 63);
     }
   }
@@ -218,8 +221,9 @@ __device__ __forceinline__ int find_tile(const RaggedRows& r, int experts, int x
     return nt;
   }
   int64_t before = 0;   // chunks of the experts before this round's
+  high = 0;
   for (int e0 = 0; e0 < experts; e0 += 256) {
-    if (experts > 256) sum = round(e0, o, c);   // (else as it was)
+    if (experts > 256) sum = four_experts(r, experts, e0, chunk, high, o, c);   // (else as it was)
     const int mine = c[0] + c[1] + c[2] + c[3];
     const int64_t lo = (before + sum - mine) * ntiles, hi = (before + sum) * ntiles;
     const uint64_t hit = __ballot(at >= lo && at < hi);

@@ -603,9 +603,10 @@ void uw_free_experts(uw_experts* w);
  *   y[s][n] = sum_k x[rows[s]][k] W_e[n][k]                       (fp32)
  *   h[s][n] = silu(g) * u, g and u the products with gate and up   (BF16)
  * with fp32 sums; silu(g) = g / (1 + exp(-g)), and h is rounded once.
- * offsets_dev as above (values outside 0 .. slots and descending ones are
- * clamped); slots is the capacity of rows_dev, y_dev and h_dev: rows from
- * offsets[experts] on are left as they were.  rows_dev NULL: slot s
+ * offsets_dev as above (values are clamped to 0 .. slots, and a value below an
+ * earlier one counts as that earlier one, so that no slot has two experts);
+ * slots is the capacity of rows_dev, y_dev and h_dev: rows before offsets[0] and
+ * from offsets[experts] on are left as they were.  rows_dev NULL: slot s
  * multiplies row s of x.  x_dev is [x_rows][k]; a row index outside it selects
  * a row of zeros.  gate and up have the same form, count and shape.  x_dev,
  * y_dev, h_dev 16-byte aligned.  Needs no workspace; results repeat bit for
