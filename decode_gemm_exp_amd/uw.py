@@ -745,18 +745,45 @@ class Experts:
 
 
 def uw_experts_bf16(w: torch.Tensor, count: int, n: int, k: int, stride: int = 0) -> Experts:
-    """w: BF16, expert e's [n][k] at element e * stride (0: n * k); w may be a view into a larger array."""
+    """w: BF16, expert e's [n][k] at element e * stride (0: n * k); w may be a view into a larger array, whose
+    rows are k long and adjacent (see _stack)."""
     if w.dtype is not torch.bfloat16:
         raise ValueError(f"w: bfloat16 expected, got {w.dtype}")
     _on_device(w, "w", _current())
     h = ctypes.c_void_p()
     _check(_lib.uw_experts_bf16(w.data_ptr(), count, n, k, stride, ctypes.byref(h)), "uw_experts_bf16")
     try:
+        _stack(w, "w", count, n, k, stride)
         _holds(w, 2 * (((stride or n * k) * (count - 1)) + n * k), "w")
     except ValueError:
         _lib.uw_free_experts(h)
         raise
     return Experts(h.value, count, n, k, w)
+
+
+def _stack(t: torch.Tensor, what: str, count: int, n: int, cols: int, stride: int) -> None:
+    """t's own shape and strides agree with `count` matrices [n][cols], `stride` elements apart (0: n * cols).
+
+    In one dimension t is contiguous.  In two or more its rows are the matrices' rows, adjacent.  A stack that
+    is not contiguous as a whole, like [:, 0] of [experts][2][n][cols], is walked along its first dimension, so
+    stride has to be a multiple of that dimension's; without a stride a stack is [experts][n][cols] or holds
+    nothing but the matrices.
+    """
+    if t.dim() < 2:
+        ok = t.is_contiguous()
+    else:
+        shape, total = t.shape, count * n * cols
+        ok = shape[-1] == cols and t.stride(-1) == 1 and (shape[-2] <= 1 or t.stride(-2) == cols)
+        if t.dim() > 2 and t.is_contiguous():
+            ok &= stride != 0 or t.numel() == total or (t.dim() == 3 and shape[1] == n and t.numel() > total)
+        elif t.dim() > 2:
+            ok &= shape[-2] >= n
+            if count > 1:
+                m, rest = divmod(stride or n * cols, t.stride(0)) if t.stride(0) else (0, 1)
+                ok &= rest == 0 and (count - 1) * m < shape[0]
+    if not ok:
+        raise ValueError(f"{what}: {count} matrices [{n}][{cols}], {stride or n * cols} elements apart, are not a tensor "
+                         f"of shape {tuple(t.shape)} and strides {t.stride()}")
 
 
 def _holds(t: torch.Tensor, nbytes: int, what: str) -> None:
@@ -768,7 +795,8 @@ def _holds(t: torch.Tensor, nbytes: int, what: str) -> None:
 
 def uw_experts_mx4(elem: torch.Tensor, scale: torch.Tensor, count: int, n: int, k: int, elem_stride: int = 0,
                    scale_stride: int = 0) -> Experts:
-    """elem, scale: uint8, expert e's [n][k/2] and [n][mx4_scale_stride(k)] at byte e * their stride (0: contiguous)."""
+    """elem, scale: uint8, expert e's [n][k/2] and [n][mx4_scale_stride(k)] at byte e * their stride (0: contiguous);
+    views as for uw_experts_bf16."""
     for t, what in ((elem, "elem"), (scale, "scale")):
         if t.dtype is not torch.uint8:
             raise ValueError(f"{what}: uint8 expected, got {t.dtype}")
@@ -778,6 +806,8 @@ def uw_experts_mx4(elem: torch.Tensor, scale: torch.Tensor, count: int, n: int, 
                                ctypes.byref(h)), "uw_experts_mx4")
     eb, sb = n * (k // 2), n * mx4_scale_stride(k)
     try:
+        _stack(elem, "elem", count, n, k // 2, elem_stride)
+        _stack(scale, "scale", count, n, mx4_scale_stride(k), scale_stride)
         _holds(elem, (elem_stride or eb) * (count - 1) + eb, "elem")
         _holds(scale, (scale_stride or sb) * (count - 1) + sb, "scale")
     except ValueError:

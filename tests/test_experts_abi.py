@@ -165,3 +165,41 @@ def test_binding_refuses_what_pointers_cannot_say(uw):
         uw.uw_route_experts(torch.zeros(4, 8), r, "top")
     with pytest.raises(uw.UwError):
         uw.Routing(4, 8, 9, device="cpu")
+
+
+def test_expert_sets_refuse_views_that_pointers_cannot_say(uw, monkeypatch):
+    """A transposed, sliced or expanded stack is no stack of [n][k]; views that are one are taken."""
+    monkeypatch.setattr(uw, "_on_device", lambda *a: None)   # host tensors: the sets are never multiplied by
+    e, n, k = 3, 8, 64
+    w = torch.zeros(e, n, k, dtype=torch.bfloat16)
+    both = torch.zeros(e, 2, n, k, dtype=torch.bfloat16)
+    fused = both.view(e, 2 * n, k)
+    taken = [(w, 0), (w.view(e * n, k), 0), (w.view(-1), 0), (w.view(1, e * n, k), 0), (both, 2 * n * k), (both[:, 1], 2 * n * k),
+             (both[:, :1], 2 * n * k), (fused, 2 * n * k), (fused[:, n:], 2 * n * k), (both[0, 1], 2 * n * k),
+             (torch.zeros(e + 2, n, k, dtype=torch.bfloat16), 0), (torch.zeros(2 * e, n, k, dtype=torch.bfloat16)[::2], 2 * n * k)]
+    for t, stride in taken:
+        uw.uw_experts_bf16(t, e, n, k, stride).free()
+    square = torch.zeros(e, k, k, dtype=torch.bfloat16)
+    refused = [(torch.zeros(e, k, n, dtype=torch.bfloat16).transpose(1, 2), n, 0),       # [K][N], transposed
+               (torch.zeros(e, k, n, dtype=torch.bfloat16), n, 0),                       # ... or as it is
+               (square.transpose(1, 2), k, 0), (square.permute(1, 0, 2), k, 0),
+               (torch.zeros(e, n, 2 * k, dtype=torch.bfloat16)[:, :, :k], n, 0),         # gaps between rows
+               (torch.zeros(e, n, 2 * k, dtype=torch.bfloat16)[:, :, ::2], n, 0),        # gaps inside rows
+               (torch.zeros(e * n, 2 * k, dtype=torch.bfloat16)[:, :k], n, 0),
+               (torch.zeros(2 * e * n * k, dtype=torch.bfloat16)[::2], n, 0),
+               (both[:, 1], n, 0),                                                       # experts 2 n k apart
+               (both[:, 1], n, 3 * n * k), (both[:2, 1], n, 2 * n * k),                  # not its stride, too few
+               (both, n, 0), (fused, n, 0),                                              # which half?
+               (w[:2], n, 0), (w[:1].expand(e, n, k), n, 0)]
+    for t, rows, stride in refused:
+        with pytest.raises(ValueError):
+            uw.uw_experts_bf16(t, e, rows, k, stride)
+    el, sc = torch.zeros(e, n, k // 2, dtype=torch.uint8), torch.zeros(e, n, 4, dtype=torch.uint8)
+    uw.uw_experts_mx4(el, sc, e, n, k).free()
+    el2, sc2 = torch.zeros(e, 2, n, k // 2, dtype=torch.uint8), torch.zeros(e, 2, n, 4, dtype=torch.uint8)
+    uw.uw_experts_mx4(el2[:, 1], sc2[:, 1], e, n, k, n * k, 2 * n * 4).free()
+    for a, b in ((el.transpose(1, 2), sc), (el, sc.transpose(1, 2)), (el2[:, 1], sc), (el, sc2[:, 1]),
+                 (torch.zeros(e, k // 2, n, dtype=torch.uint8).transpose(1, 2), sc),
+                 (el, torch.zeros(e, n, 8, dtype=torch.uint8)[:, :, :4])):
+        with pytest.raises(ValueError):
+            uw.uw_experts_mx4(a, b, e, n, k)
