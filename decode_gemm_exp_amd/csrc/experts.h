@@ -327,6 +327,7 @@ struct RouteCall {
   int64_t tokens, ld;
   int experts, topk, scoring;
   const float* bias;
+  bool on_score;        // the bias is added to the logit's sigmoid, not to the logit
   int32_t* ids;
   const int32_t* ids_in;
   float* weights;

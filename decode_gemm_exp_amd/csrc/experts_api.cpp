@@ -328,7 +328,8 @@ uw_status uw_route_experts(const void* logits_dev, uw_type type, int64_t tokens,
                            void* ws_dev, size_t ws_bytes, void* stream) {
   if (ld < experts || (tokens != 0 && (!logits_dev || !ids_dev || !weights_dev))) return UW_ERR_INVALID;
   if (type != UW_TYPE_BF16 && type != UW_TYPE_F32) return UW_ERR_INVALID;
-  if (scoring != UW_SCORE_SOFTMAX && scoring != UW_SCORE_SOFTMAX_TOPK && scoring != UW_SCORE_SIGMOID)
+  if (scoring != UW_SCORE_SOFTMAX && scoring != UW_SCORE_SOFTMAX_TOPK && scoring != UW_SCORE_SIGMOID &&
+      scoring != UW_SCORE_SIGMOID_BIASED)
     return UW_ERR_INVALID;
   RouteCall c{};
   c.logits = logits_dev;
@@ -337,8 +338,9 @@ uw_status uw_route_experts(const void* logits_dev, uw_type type, int64_t tokens,
   c.ld = ld;
   c.experts = experts;
   c.topk = topk;
-  c.scoring = (int)scoring;
+  c.scoring = (int)(scoring == UW_SCORE_SIGMOID_BIASED ? UW_SCORE_SIGMOID : scoring);
   c.bias = bias_dev;
+  c.on_score = scoring == UW_SCORE_SIGMOID_BIASED && bias_dev;   // (the logits' order is their sigmoids')
   c.ids = ids_dev;
   c.weights = weights_dev;
   c.offsets = offsets_dev;

@@ -1,8 +1,8 @@
 // route.hip -- a router's choice of experts and the plan that groups rows by
 // expert, and the weighted sum that undoes the grouping.
 //
-// Choice.  key[e] = logit[e] (+ bias[e]) in FP32; NaN and -inf are never
-// chosen.  The topk largest keys, larger first, equal keys by the lower index;
+// Choice.  key[e] = logit[e] (+ bias[e]), or sigmoid(logit[e]) + bias[e], in FP32;
+// NaN and -inf, of the logit too, are never chosen.  The topk largest keys, larger first, equal keys by the lower index;
 // a token with fewer selectable experts gets id -1 and weight 0 for the rest.
 // Weights come from the logits without the bias: softmax over every selectable
 // expert, softmax over the chosen, or sigmoids divided by their sum over the
@@ -103,6 +103,13 @@ __device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live,
   for (int i = 0; i < NV; ++i) {
     const bool in = live && i * L + l < c.experts;
     key[i] = in ? order_key(v[i] + bias[i]) : 0u;
+  }
+  if (c.on_score) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = live && i * L + l < c.experts && order_key(v[i]);
+      key[i] = in ? order_key(1.0f / (1.0f + expf(-v[i])) + bias[i]) : 0u;
+    }
   }
   float top = -__builtin_inff(), sum = 0.0f;
   if (c.scoring == 0) {

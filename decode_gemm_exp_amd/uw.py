@@ -555,7 +555,7 @@ class TorchAllocator:
 # contiguity, device -- and raise ValueError before the library sees them.
 
 ACT_BF16, ACT_MX4 = 0, 1
-SCORE = {"softmax": 0, "softmax_topk": 1, "sigmoid": 2}
+SCORE = {"softmax": 0, "softmax_topk": 1, "sigmoid": 2, "sigmoid_biased": 4}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -696,7 +696,11 @@ class Routing:
 
 def uw_route_experts(logits: torch.Tensor, routing: Routing, scoring: str = "softmax_topk",
                      bias: torch.Tensor | None = None, stream=None) -> None:
-    """logits [tokens][experts] FP32 or BF16 (rows may be strided) -> routing's ids, weights and plan."""
+    """logits [tokens][experts] FP32 or BF16 (rows may be strided) -> routing's ids, weights and plan.
+
+    bias [experts] FP32 is added to the logits for the choice, with "sigmoid_biased" to their sigmoids; the
+    weights are without it.
+    """
     tokens, experts, topk = routing._shape
     kind = _TYPES.get(logits.dtype)
     if kind is None:

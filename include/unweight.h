@@ -549,19 +549,28 @@ uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64
  * Within an expert, slots keep the order of their pairs.
  *
  * Router.  logits_dev is [tokens][experts], rows `ld` elements apart, FP32 or
- * BF16.  A choice is by key = logit + bias (bias_dev [experts] FP32, may be
- * NULL), larger first, equal keys by the lower index; experts whose key is
- * NaN or -inf are never chosen.  A token with fewer selectable experts than
- * topk (a padded token's row of -inf has none) gets id -1 and weight 0 for
- * the rest.  Weights use the logits without the bias:
- *   UW_SCORE_SOFTMAX        softmax over the selectable experts
- *   UW_SCORE_SOFTMAX_TOPK   softmax over the chosen ones
- *   UW_SCORE_SIGMOID        sigmoids divided by their sum over the chosen ones
+ * BF16.  A choice is by key, larger first, equal keys by the lower index:
+ * key = logit + bias (bias_dev [experts] FP32, may be NULL), with
+ * UW_SCORE_SIGMOID_BIASED sigmoid(logit) + bias, both in FP32; the latter is how
+ * a router balanced by its bias instead of a loss chooses (without a bias it
+ * chooses by logit as well).  Experts whose logit or key is NaN or -inf are
+ * never chosen.  A token with fewer selectable experts than topk (a padded
+ * token's row of -inf has none) gets id -1 and weight 0 for the rest.  Weights
+ * use the logits without the bias:
+ *   UW_SCORE_SOFTMAX         softmax over the selectable experts
+ *   UW_SCORE_SOFTMAX_TOPK    softmax over the chosen ones
+ *   UW_SCORE_SIGMOID, UW_SCORE_SIGMOID_BIASED
+ *                            sigmoids divided by their sum over the chosen ones
  * ids_dev and weights_dev are [tokens][topk].  experts <= 1024 and topk <= 16
  * (UW_ERR_UNSUPPORTED), topk <= experts.  Results repeat bit for bit.  The
  * workspace (uw_workspace_size_route bytes, may be 0) serves one call at a
  * time. */
-typedef enum { UW_SCORE_SOFTMAX = 0, UW_SCORE_SOFTMAX_TOPK = 1, UW_SCORE_SIGMOID = 2 } uw_scoring;
+typedef enum {
+  UW_SCORE_SOFTMAX = 0,
+  UW_SCORE_SOFTMAX_TOPK = 1,
+  UW_SCORE_SIGMOID = 2,
+  UW_SCORE_SIGMOID_BIASED = 4
+} uw_scoring;
 uw_status uw_workspace_size_route(int64_t tokens, int32_t experts, int32_t topk, size_t* bytes);
 uw_status uw_route_experts(const void* logits_dev, uw_type type, int64_t tokens, int32_t experts, int64_t ld,
                            const float* bias_dev, int32_t topk, uw_scoring scoring, int32_t* ids_dev,
