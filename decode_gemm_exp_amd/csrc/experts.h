@@ -98,11 +98,11 @@ __device__ __forceinline__ int four_experts(const RaggedRows& r, int experts, in
   asm volatile("" : "+v"(o[0]), "+v"(o[1]), "+v"(o[2]), "+v"(o[3]), "+v"(o[4]));
 #pragma unroll
   for (int i = 0; i < 5; ++i) o[i] = o[i] < 0 ? 0 : (int64_t)o[i] < r.slots ? o[i] : (int32_t)r.slots;
-  // (a plan ascends, so the maximum is taken only where one does not)
+  // (a plan ascends, so the maximum is taken, and its code laid, out of the way)
   bool down = o[0] < high;
 #pragma unroll
   for (int i = 1; i < 5; ++i) down |= o[i] < o[i - 1];
-  if (__ballot(down)) {
+  if (__builtin_expect(__ballot(down) != 0, 0)) {
 #pragma unroll
     for (int i = 1; i < 5; ++i) o[i] = max(o[i], o[i - 1]);
     int32_t top = max(o[4], high);   // of the lanes up to this one
