@@ -291,10 +291,16 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, bf16x2_t));
 }
 
-// g / (1 + exp(-g)): exp(-g) overflows to infinity for g below -88.7, where
-// the quotient is -0, as it should round
-// (the reciprocal instruction is within one unit in the last place)
-__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+// g / (1 + exp(-g)) as g e^2 / (1 + e^2) with e = exp(g / 2): exp(-g) itself would
+// overflow below -88.7, where the value, -2.6e-37 there, is a normal BF16 number
+// still, while e is normal down to -174 (the value leaves BF16 at -100).  Beyond
+// 2^43, g > 59, e^2 / (1 + e^2) is 1 in FP32.  The products' order keeps every
+// partial one in range.  The exponential's argument is off by half a unit, 2^-18 of
+// the value at |g| = 88; the reciprocal instruction is within one unit in the last place.
+__device__ __forceinline__ float silu(float g) {
+  const float e = __builtin_amdgcn_exp2f(fminf(g * 0.72134752f, 43.0f));
+  return g * (e * __builtin_amdgcn_rcpf(__builtin_fmaf(e, e, 1.0f))) * e;
+}
 
 // ---- launchers ----------------------------------------------------------------
 // y (fp32, mode 0) or h = silu(W x) * (U x) (BF16, mode 1; u the second

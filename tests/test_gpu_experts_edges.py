@@ -1,4 +1,5 @@
-"""Products grouped by expert where their inputs are odd, in each of the kernels: plans that do not ascend.
+"""Products grouped by expert where their inputs are odd, in each of the kernels: plans that do not ascend,
+gates over the whole range of BF16.
 
 Which kernel runs follows from the average rows an expert (all slots used) and
 the blocks that tiles of 256 columns (gated: 128) make, 192 of them at least on
@@ -93,3 +94,36 @@ def test_offsets_that_descend_among_many_experts(uw, form, per, n):
         off = up.clone()
         off[at] = torch.randint(-5, e * per, (len(at),), generator=g) // 2
         check_plan_products(uw, sets, vals, off.tolist(), x, rows, n, k)
+
+
+@pytest.mark.parametrize("per,n", [(300, 33), (50, 33000), (150, 33000), (300, 33000)])
+@pytest.mark.parametrize("form", FORMS)
+def test_gates_over_the_whole_range(uw, form, per, n):
+    """silu(g) u where g and u are single elements of x, so that nothing but the epilogue rounds.
+
+    The exponential's argument g log2(e) (or half of it, counted twice) is off by 2^-24 of itself and by its
+    constant's 2^-25 of at most 150, 2^-17.2 of the value together; exponential, sum, reciprocal and the
+    products add 2^-23 each: 2^-17 in all.  Subnormal FP32 silu (below g = -91) rounds by 2^-150, and so does its
+    product with u; BF16 rounds by half a step, 2^-8 of the value or 2^-134.
+    """
+    k = 64
+    pick = torch.zeros(2, 1, n, k)
+    pick[0, 0, :, 0] = pick[1, 0, :, 1] = 1.0
+    gate, up = (make_set(uw, form, w)[0] for w in pick)
+    g = torch.cat([torch.linspace(-104.0, -80.0, per // 2), torch.linspace(-80.0, 90.0, per - per // 2 - 12),
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1e-40, -1e-40, 1e30, -1e30, 3e38, -3e38, -110.0, -1000.0])])
+    x = torch.zeros(per, k)
+    x[:, 0] = g[torch.randperm(per, generator=torch.Generator().manual_seed(1))]
+    off = torch.tensor([0, per], dtype=torch.int32, device=DEV)
+    for u in (1.0, -3.5, 1e-3):
+        x[:, 1] = u
+        b = x.bfloat16()
+        h = torch.empty(per, n, dtype=torch.bfloat16, device=DEV)
+        uw.uw_matmul_experts_gated(gate, up, off, None, b.to(DEV), h)
+        assert bool((h == h[:, :1]).all())
+        gv, uv = b[:, 0].double(), b[:, 1].double()
+        want = gv * torch.sigmoid(gv) * uv
+        tol = (2.0 ** -8 + 2.0 ** -17) * want.abs() + 2.0 ** -149 * (uv.abs() + 1) + 2.0 ** -134
+        big = want.abs() > torch.finfo(torch.bfloat16).max
+        got = h[:, 0].double().cpu()
+        assert bool((((got - want).abs() <= tol) | (big & torch.isinf(got))).all())
