@@ -99,7 +99,8 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
 }
 
 // Up to this many rows x's 4-bit values go through the register-fed kernel as
-// BF16; beyond, both operands stay in 4 bits.
+// BF16; beyond, both operands stay in 4 bits.  (The header names this number: the
+// two differ where a weight's value overflows BF16.)
 constexpr int64_t kMx4RowsMax = 8;
 
 uw_status check_route(int64_t tokens, int32_t experts, int32_t topk) {

@@ -524,9 +524,10 @@ uw_status uw_dequantize_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, i
 /* y[b][n] = sum_k x[b][k] W[n][k] for b < batch with W in MXFP4 ([n][k]), fp32
  * sums and output.  act: UW_ACT_BF16 takes x as it is, UW_ACT_MX4 its MXFP4
  * quantisation (uw_quantize_mx4's, made inside the call), so that both
- * operands have 4 bits.  Elements times scale are what is multiplied; a
- * weight whose value overflows BF16 (scale bytes 253 and 254) counts as
- * infinite.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
+ * operands have 4 bits.  Elements times scale are what is multiplied, except
+ * that a weight whose value overflows BF16 (scale bytes 253 and 254, which
+ * uw_quantize_mx4 never writes) counts as infinite with UW_ACT_BF16, and with
+ * UW_ACT_MX4 up to 8 rows; beyond, UW_ACT_MX4 multiplies it as it is.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
  * 16-byte aligned.  The workspace (uw_workspace_size_mx4 bytes, 16-byte
  * aligned) serves one call at a time. */
 typedef enum { UW_ACT_BF16 = 0, UW_ACT_MX4 = 1 } uw_activation;
@@ -591,7 +592,8 @@ uw_status uw_plan_experts(const int32_t* ids_dev, int64_t tokens, int32_t expert
  *   uw_experts_bf16   BF16, expert e at w_dev + e * stride elements (0: n * k;
  *                     a multiple of 8), rows contiguous
  *   uw_experts_mx4    MXFP4, expert e's elements and scales e * their stride
- *                     in bytes on (0: contiguous; multiples of 16 and 4)
+ *                     in bytes on (0: contiguous; multiples of 16 and 4); a
+ *                     weight whose value overflows BF16 counts as infinite
  *   uw_experts_uwf1   `count` compressed matrices of one shape, stored [N][K]
  *                     (UW_ERR_UNSUPPORTED otherwise), with resident palette
  *                     indices (uw_transcode_palette(m, NULL);
