@@ -171,8 +171,9 @@ __device__ __forceinline__ void choose_range(const RouteCall& c, int64_t t0, int
 __device__ __forceinline__ int valid_id(int id, int experts) { return (unsigned)id < (unsigned)experts ? id : -1; }
 
 // rank of this lane among the wave's lower lanes with the same expert, and
-// how many lanes share it; e in [0, 2048), absent lanes pass -1
+// how many lanes share it; absent lanes pass -1
 __device__ __forceinline__ void wave_rank(int e, int& rank, int& same) {
+  static_assert(kMaxExperts <= 1 << 10, "ten bits tell experts apart");
   uint64_t mask = __ballot(e >= 0);
 #pragma unroll
   for (int b = 0; b < 10; ++b) {
@@ -237,8 +238,16 @@ __device__ __forceinline__ int place_chunk(PlanLds& s, int experts, int e) {
   return slot;
 }
 
-// Everything in one wave (tokens * topk <= 64): the wave's LDS operations are
-// in order, so a fence for the compiler is all that stands between them.
+// What the wave's lanes wrote to LDS before, its lanes read after.  LDS serves a
+// wave in order, so nothing is waited for, but the compiler has to keep the order: a
+// wave barrier alone holds back no memory access.
+__device__ __forceinline__ void wave_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Everything in one wave (tokens * topk <= 64).
 template <int L, int NV>
 __global__ __launch_bounds__(64) void k_route_wave(RouteCall c) {
   __shared__ int32_t ids[64], first[kMaxExperts];
@@ -250,12 +259,12 @@ __global__ __launch_bounds__(64) void k_route_wave(RouteCall c) {
   } else if (lane < pairs) {
     ids[lane] = valid_id(c.ids_in[lane], c.experts);
   }
-  __builtin_amdgcn_wave_barrier();
+  wave_fence();
   const int e = lane < pairs ? ids[lane] : -1;
   int rank, same;
   wave_rank(e, rank, same);
   if (e >= 0 && rank == 0) first[e] = same;
-  __builtin_amdgcn_wave_barrier();
+  wave_fence();
   int mine = 0;
   for (int i = 0; i < per; ++i) mine += lane * per + i < c.experts ? first[lane * per + i] : 0;
   int sum = mine;
@@ -274,7 +283,7 @@ __global__ __launch_bounds__(64) void k_route_wave(RouteCall c) {
     at += n;
   }
   if (lane == 63) c.offsets[c.experts] = sum;
-  __builtin_amdgcn_wave_barrier();
+  wave_fence();
   if (lane < pairs) {
     const int slot = e >= 0 ? first[e] + rank : -1;
     c.slots[lane] = slot;
