@@ -17,6 +17,7 @@
 #include <tuple>
 #include <set>
 
+#include "experts.h"
 #include "uw_internal.h"
 
 using namespace uw;

@@ -27,6 +27,9 @@ struct ExpertEntry {
   PalView pal;
 };
 
+// a matrix's palette as the kernels take it (api.cpp)
+void palette_view(const uw_matrix* m, PalView* out);
+
 // All experts of one projection: expert e's W_e[N][K].
 struct ExpertsView {
   int form;

@@ -142,8 +142,6 @@ struct PalView {
   uint32_t base4;
 };
 
-void palette_view(const uw_matrix* m, PalView* out);   // api.cpp
-
 enum DecodeMode { kDecodeNibble = 0, kDecodeExponent = 1, kDecodeFull = 2, kDecodeFp8 = 3 };
 struct DecodeArgs {
   const uint32_t* stream; uint64_t stream_words;   // including slack

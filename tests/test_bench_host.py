@@ -74,3 +74,15 @@ def test_valu_floor_figures_restate_their_counts():
     for k in d["kernels"].values():
         floor = k["valu_instr"] * d["valu_cycles_per_instr"] / (d["simds"] * d["clock_ghz"] * 1e3)
         assert k["valu_floor_us"] == pytest.approx(floor, rel=1e-3)
+
+
+@pytest.mark.parametrize("name,load", [("traffic_gate8b", lambda k: bench.load_traffic(k)),
+                                       ("traffic_mlp70b", lambda k: bench.load_traffic(k, "mlp70b")),
+                                       ("decode_counters_gate8b", lambda k: bench.load_valu_floor(k))])
+def test_committed_counters_are_those_of_the_sources(name, load):
+    """Whoever changes a file that the counted kernels are built from counts again, or the bench loses its figures."""
+    with open(os.path.join(ROOT, "profiles", name + ".json")) as f:
+        kernels = json.load(f)["kernels"]
+    assert kernels
+    for k in kernels:
+        assert load(k) is not None, k
