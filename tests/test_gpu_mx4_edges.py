@@ -1,4 +1,4 @@
-"""MXFP4 products at the ends of their range, on the GPU against plain implementations."""
+"""MXFP4 products at the ends of their range, in each of the kernels, on the GPU against plain implementations."""
 import numpy as np
 import pytest
 import torch
@@ -70,3 +70,47 @@ def test_one_weight_that_overflows_bf16(uw, act, batch):
     y = product(uw, elem, scale, x, act).cpu().double()
     sign = torch.where(torch.arange(n) % 2 == 1, 1.0, -1.0) * torch.sign(x[:, :1].double())
     assert torch.equal(y, sign * (6 * 2.0 ** 87 if act and batch > 8 else float("inf")))
+
+
+# Sums of whole numbers below 2^24 are exact in FP32, in any order: one k too few or too many shows.
+@pytest.mark.parametrize("batch,n,k", [(1, 40, 1 << 20), (2, 40, 28672), (9, 40, 28640), (16, 5001, 28672), (45, 700, 8224),
+                                       (200, 300, 28640), (200, 16500, 8224), (200, 33000, 4192), (300, 33000, 4128),
+                                       (130, 16500, 4128), (1, 1 << 20, 32), (300, 1 << 20, 32)])
+@pytest.mark.parametrize("act", [0, 1])
+def test_long_rows_and_columns_exactly(uw, act, batch, n, k):
+    g = torch.Generator(device=DEV).manual_seed(n + k)
+    w = torch.randint(1, 4, (n, k), generator=g, device=DEV, dtype=torch.int8)
+    w *= 1 - 2 * torch.randint(0, 2, (n, k), generator=g, device=DEV, dtype=torch.int8)
+    x = 1 - 2 * torch.randint(0, 2, (batch, k), generator=g, device=DEV).bfloat16()
+    elem = torch.empty(n, k // 2, dtype=torch.uint8, device=DEV)
+    scale = torch.empty(n, uw.mx4_scale_stride(k), dtype=torch.uint8, device=DEV)
+    uw.uw_quantize_mx4(w.bfloat16(), elem, scale)                # (exact, as is x's)
+    y = product(uw, elem, scale, x, act)
+    for c in range(0, n, 1 << 16):
+        want = x.double() @ w[c:c + (1 << 16)].double().T.contiguous()
+        assert torch.equal(y[:, c:c + (1 << 16)].double(), want)
+
+
+@pytest.mark.parametrize("batch,n", [(3, 70), (45, 70), (200, 16500), (200, 33000), (300, 33000)])
+@pytest.mark.parametrize("act", [0, 1])
+def test_nan_and_extreme_scales_in_every_kernel(uw, act, batch, n):
+    """A NaN scale makes its row's outputs NaN and no other's, x of zero included; the smallest and large scales count in full."""
+    k = 160
+    g = torch.Generator().manual_seed(n + batch)
+    elem = torch.randint(0, 256, (n, k // 2), dtype=torch.uint8, generator=g)
+    for e in (0, 1, 127, 250):
+        scale = torch.full((n, 8), e, dtype=torch.uint8)
+        scale[:, 5:] = 255                                       # padding is never used
+        x = torch.ldexp(torch.randint(-3, 4, (batch, k), generator=g).float(), torch.tensor(min(127 - e, 120))).bfloat16()
+        y = product(uw, elem, scale, x, act)
+        xv = x.double().numpy()
+        check_product(y, values(*quantize_ref(xv)) if act else xv, values(unpack(elem), scale[:, :5].numpy()))
+    scale = torch.full((n, 8), 120, dtype=torch.uint8)
+    bad = [5, n // 2, n - 1]
+    scale[bad[0], 0], scale[bad[1], 4], scale[bad[2], 2] = 255, 255, 255
+    x = torch.randn(batch, k, generator=g).bfloat16()
+    x[batch // 2] = 0.0
+    nan = torch.isnan(product(uw, elem, scale, x, act).cpu())
+    want = torch.zeros(n, dtype=torch.bool)
+    want[bad] = True
+    assert torch.equal(nan, want.expand(batch, n))
