@@ -217,13 +217,19 @@ def test_strided_stacks_in_every_kernel(uw, kernel):
         assert bool(((h.double() - want).abs() <= tol).all())
 
 
+def two_bands(g, e, n, k):
+    """Magnitudes of two kinds, 2^40 apart: their exponents are no run."""
+    w = weights(g, e, n, k)
+    return torch.where(torch.rand(w.shape, generator=g) < 0.5, w, w * 2.0 ** -40)
+
+
 @pytest.mark.parametrize("kernel", list(KERNELS))
 def test_palettes_of_both_kinds_in_every_kernel(uw, kernel):
     """K an odd number of groups, so that rows straddle flag words; verbatim groups; gate and up of different kinds."""
     (per, n), e = KERNELS[kernel], 2
     g = torch.Generator().manual_seed(per + 4)
     for k in (64, 320):
-        plain, odd = weights(g, e, n, k), torch.cat([weights(g, 1, n, k), weights(g, 1, n, k, outliers=True)])
+        plain, odd = weights(g, e, n, k), torch.cat([weights(g, 1, n, k, outliers=True), two_bands(g, 1, n, k)])
         (a, av), (b, bv) = make_set(uw, "uwf1", plain), make_set(uw, "uwf1", odd)
         s = e * per
         off = torch.tensor([0, s // 2 - 1, s], dtype=torch.int32)
@@ -278,13 +284,15 @@ def test_extreme_mx4_scales_in_every_kernel(uw, kernel):
     assert torch.equal(torch.isnan(y), want) and torch.equal(torch.isnan(hh), want)
 
 
-@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("form", FORMS + ["two bands"])
 @pytest.mark.parametrize("per", [2, 300])
 def test_x_past_two_gib_gated(uw, form, per):
     """Rows whose bytes pass 2^31 and 2^32, and row indices outside x, through both products."""
     g = torch.Generator().manual_seed(per)
     n, k, x_rows = 40, 8192, 270000            # 4.4 GB
-    sets, vals = zip(*[make_set(uw, form, weights(g, 2, n, k)) for _ in range(2)])
+    make = (lambda: make_set(uw, "uwf1", two_bands(g, 2, n, k))) if form == "two bands" else (
+        lambda: make_set(uw, form, weights(g, 2, n, k)))
+    sets, vals = zip(*[make() for _ in range(2)])
     s = 2 * per + 1
     off = torch.tensor([0, per, s], dtype=torch.int32)
     rows = torch.randint(0, x_rows, (s,), generator=g, dtype=torch.int32)
