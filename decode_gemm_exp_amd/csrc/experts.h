@@ -306,6 +306,9 @@ __device__ __forceinline__ float silu(float g) {
 }
 
 // ---- launchers ----------------------------------------------------------------
+// A launch holds fewer than 2^32 threads.
+inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)(UINT32_MAX / (unsigned)threads); }
+
 // y (fp32, mode 0) or h = silu(W x) * (U x) (BF16, mode 1; u the second
 // projection) over ragged rows
 struct ExpertsCall {

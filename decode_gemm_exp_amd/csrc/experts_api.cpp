@@ -156,7 +156,8 @@ uw_status uw_workspace_size_mx4(int64_t n, int64_t k, int64_t batch, uw_activati
   if (!bytes || batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_MX4)) return UW_ERR_INVALID;
   const uw_status st = check_shape(n, k);
   if (st != UW_OK) return st;
-  if (batch > INT32_MAX) return UW_ERR_UNSUPPORTED;
+  // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
+  if (batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512)) return UW_ERR_UNSUPPORTED;
   const uint64_t b = (uint64_t)batch;
   *bytes = act != UW_ACT_MX4     ? 0
            : batch <= kMx4RowsMax ? pad256(2 * b * (uint64_t)k)
@@ -391,6 +392,8 @@ uw_status uw_workspace_size_expert_mlp(const uw_experts* gate, const uw_experts*
   if (down->v.k != gate->v.n || down->v.n != gate->v.k || down->v.count != gate->v.count) return UW_ERR_INVALID;
   const uw_status st = check_route(tokens, gate->v.count, topk);
   if (st != UW_OK) return st;
+  // (the weighted sum's threads take eight outputs each)
+  if (!grid_fits((tokens * (down->v.n / 8) + 255) / 256, 256)) return UW_ERR_UNSUPPORTED;
   const uint64_t pairs = (uint64_t)tokens * (uint64_t)topk;
   *bytes = pad256(2 * pairs * (uint64_t)gate->v.n) + pad256(4 * pairs * (uint64_t)down->v.n);
   return UW_OK;

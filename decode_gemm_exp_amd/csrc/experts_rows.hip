@@ -484,7 +484,7 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   const int64_t rows = 16 * (GATED ? R / 2 : R), ntiles = (c.w.n + rows - 1) / rows;
   const int64_t chunks = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr);
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!grid_fits(grid, 256)) return hipErrorNotSupported;
   if constexpr (FORM == kFormMx4) {
     auto k = k_experts_mx4<Q, GATED, false, 4>;
     int waves = 4;

@@ -498,7 +498,7 @@ hipError_t launch_one(const ExpertsCall& c, bool spread, hipStream_t s) {
   // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
   const int64_t tiles = max_chunks(c.r.slots, c.w.count, BM, c.r.offsets != nullptr) * ntiles;
   const int64_t grid = (tiles + 7) / 8 * 8;
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!grid_fits(grid, kNT)) return hipErrorNotSupported;
   hipLaunchKernelGGL((k_experts_tile<FORM, BM, GATED, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x,
                      c.y, (int)ntiles, (int)spread);
   return hipGetLastError();

@@ -160,14 +160,15 @@ __global__ __launch_bounds__(256) void k_round_mx4(const uint16_t* __restrict__ 
   if (p < pieces) reinterpret_cast<uint4*>(out)[p] = unpack8(pack8(e, byte), byte);
 }
 
-unsigned blocks_for(int64_t pieces) { return (unsigned)((pieces + 256 * kUnroll - 1) / (256 * kUnroll)); }
+int64_t blocks_for(int64_t pieces) { return (pieces + 256 * kUnroll - 1) / (256 * kUnroll); }
 
 }  // namespace
 
 hipError_t launch_quantize_mx4(const void* src, bool f32, int64_t rows, int64_t cols, int64_t ld, uint8_t* elem,
                                uint8_t* scale, hipStream_t s) {
   const int64_t pieces = rows * (cols / 8);
-  const dim3 grid(blocks_for(pieces));
+  if (!grid_fits(blocks_for(pieces), 256)) return hipErrorNotSupported;
+  const dim3 grid((unsigned)blocks_for(pieces));
   if (f32)
     hipLaunchKernelGGL(k_quantize_mx4<true>, grid, dim3(256), 0, s, src, pieces, (uint32_t)(cols / 8), ld, elem, scale,
                        mx4_scale_stride(cols));
@@ -180,7 +181,8 @@ hipError_t launch_quantize_mx4(const void* src, bool f32, int64_t rows, int64_t 
 hipError_t launch_dequantize_mx4(const uint8_t* elem, const uint8_t* scale, int64_t rows, int64_t cols, uint16_t* out,
                                  int64_t ld, hipStream_t s) {
   const int64_t pieces = rows * (cols / 8);
-  hipLaunchKernelGGL(k_dequantize_mx4, dim3(blocks_for(pieces)), dim3(256), 0, s, elem, scale, pieces,
+  if (!grid_fits(blocks_for(pieces), 256)) return hipErrorNotSupported;
+  hipLaunchKernelGGL(k_dequantize_mx4, dim3((unsigned)blocks_for(pieces)), dim3(256), 0, s, elem, scale, pieces,
                      (uint32_t)(cols / 8), mx4_scale_stride(cols), out, ld);
   return hipGetLastError();
 }

@@ -281,7 +281,7 @@ template <int BM>
 hipError_t launch_bm(const uint8_t* we, const uint8_t* ws, int64_t n, int64_t k, const uint8_t* xe, const uint8_t* xs,
                      int64_t batch, float* y, hipStream_t s) {
   const int64_t ntiles = (n + kBN - 1) / kBN, tiles = (batch + BM - 1) / BM * ntiles, grid = (tiles + 7) / 8 * 8;
-  if (grid > INT32_MAX) return hipErrorNotSupported;
+  if (!grid_fits(grid, kNT)) return hipErrorNotSupported;
   hipLaunchKernelGGL(k_mx4_tile<BM>, dim3((unsigned)grid), dim3(kNT), 0, s, we, ws, n, (int)k, xe, xs, batch, y,
                      (int)ntiles);
   return hipGetLastError();

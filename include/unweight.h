@@ -497,8 +497,10 @@ uw_status uw_sync_status(const uw_matrix* m, void* stream);
  * cols / 32 of them, then padding up to a multiple of four (written as 0,
  * never used), so that a row's scales start on a 4-byte boundary; without
  * padding whenever cols is a multiple of 128.  cols must be a multiple of 32;
- * rows and cols are at most 2^20 (UW_ERR_UNSUPPORTED).  (saidapartage.blog, section "Un complément, pas un
- * remplaçant": quantised weights are the other half of what is served.) */
+ * rows and cols are at most 2^20 (UW_ERR_UNSUPPORTED; so is, here and below, a
+ * call whose outputs would take 2^32 GPU threads, tens of GB at least).
+ * (saidapartage.blog, section "Un complément, pas un remplaçant": quantised
+ * weights are the other half of what is served.) */
 #define UW_MX4_SCALE_STRIDE(cols) (((cols) + 127) / 128 * 4)
 
 typedef enum { UW_TYPE_F32 = 0, UW_TYPE_BF16 = 1 } uw_type;

@@ -203,3 +203,25 @@ def test_expert_sets_refuse_views_that_pointers_cannot_say(uw, monkeypatch):
                  (el, torch.zeros(e, n, 8, dtype=torch.uint8)[:, :, :4])):
         with pytest.raises(ValueError):
             uw.uw_experts_mx4(a, b, e, n, k)
+
+
+def test_calls_of_more_threads_than_a_launch_holds(uw):
+    """2^32 threads are refused as unsupported before anything is launched, not as a failure of the device."""
+    n = ctypes.c_size_t()
+    size = uw._lib.uw_workspace_size_mx4
+    for act in (0, 1):
+        # 4096 tiles of columns, 512 threads each
+        assert size(1 << 20, 32, (1 << 17) - 64, act, ctypes.byref(n)) == 0
+        assert size(1 << 20, 32, 1 << 17, act, ctypes.byref(n)) == UNSUPPORTED   # 2^23 tiles
+        assert size(1 << 20, 32, 1 << 20, act, ctypes.byref(n)) == UNSUPPORTED
+        assert uw._lib.uw_matmul_mx4(P, P, 1 << 20, 32, P, 1 << 20, P, act, P, 1 << 62, None) == UNSUPPORTED
+    assert uw._lib.uw_quantize_mx4(P, 1, 1 << 20, 1 << 20, 1 << 20, P, P, None) == UNSUPPORTED
+    assert uw._lib.uw_dequantize_mx4(P, P, 1 << 20, 1 << 20, P, 1 << 20, None) == UNSUPPORTED
+    _, gate = bf16_set(uw, n=32, k=1 << 20)
+    _, down = bf16_set(uw, n=1 << 20, k=32)
+    size = uw._lib.uw_workspace_size_expert_mlp
+    assert size(gate, down, 1 << 14, 2, ctypes.byref(n)) == 0
+    assert size(gate, down, 1 << 15, 2, ctypes.byref(n)) == UNSUPPORTED
+    assert uw._lib.uw_expert_mlp(gate, gate, down, 1 << 20, 1, P, P, P, P, P, P, P, 1 << 62, None) == UNSUPPORTED
+    for h in (gate, down):
+        uw._lib.uw_free_experts(h)
