@@ -23,7 +23,6 @@ struct ExpertEntry {
   const uint32_t* vflags;
   const uint32_t* vrank;
   const uint8_t* vexp;
-  uint64_t vexp_bytes;
   PalView pal;
 };
 
@@ -60,6 +59,32 @@ __device__ __forceinline__ uint4 gload16(const void* p) {
 __device__ __forceinline__ uint2 gload8(const void* p) {
   const u32x2_t v = gload<u32x2_t>(p);
   return make_uint2(v.x, v.y);
+}
+
+// An offset past the end of every buffer resource here, also with a row's and a K
+// tail's own kOutside added: such a load reads zeros, such a store is dropped.
+// (Twice this is below 2^32; x beyond this many bytes goes by pointers.)
+constexpr uint32_t kOutside = 0x7FFF0000u;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t byte) {
+  const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)byte, 0, 0);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+// Tiles in LDS: rows of 128 bytes, 16-byte piece c of row r at c ^ (r / 2 % 8)
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ ((row >> 1) & 7)) << 4)); }
+
+// A block barrier without a fence: a fence would wait for everything that is on
+// its way to LDS.  The caller has waited for what must have landed.
+__device__ __forceinline__ void bare_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("" ::: "memory");
 }
 
 __host__ __device__ constexpr int64_t mx4_scale_stride(int64_t k) { return (k + 127) / 128 * 4; }
@@ -190,8 +215,8 @@ __device__ __forceinline__ void tile_of(uint32_t l, uint32_t chunks, uint32_t nt
   nt = __builtin_amdgcn_readfirstlane((int)(band * kBand + in - m * width));
 }
 
-// The same for tiles of ntiles columns, dealt so that each XCD works on one
-// contiguous run of the list: entry `turn` of XCD `xcd`'s eighth of the list that
+// A chunk (see find_share) and a column tile of ntiles, dealt so that each XCD works
+// on one contiguous run of the list of them: entry `turn` of XCD `xcd`'s eighth of the list that
 // really exists (its length follows from the offsets); blocks go to the XCDs
 // round robin, so block b is on XCD b % 8.  What it returns is in scalar registers:
 // buffer resources built from it then need no loop over a wave's lanes (a
@@ -309,7 +334,7 @@ __device__ __forceinline__ float silu(float g) {
 // A launch holds fewer than 2^32 threads.
 inline bool grid_fits(int64_t blocks, int threads) { return blocks <= (int64_t)(UINT32_MAX / (unsigned)threads); }
 
-// y (fp32, mode 0) or h = silu(W x) * (U x) (BF16, mode 1; u the second
+// y = W x (FP32) or, gated, h = silu(W x) * (U x) (BF16; u is then the second
 // projection) over ragged rows
 struct ExpertsCall {
   ExpertsView w, u;

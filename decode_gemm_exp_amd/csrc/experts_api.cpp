@@ -287,7 +287,6 @@ uw_status uw_experts_uwf1(const uw_matrix* const* ms, int32_t count, void* strea
     e.vflags = m->vflags;
     e.vrank = m->vrank;
     e.vexp = m->vexp;
-    e.vexp_bytes = 64 * m->V;
     palette_view(m, &e.pal);
     if (!e.pal.run) h->v.form = kFormPal;
   }

@@ -27,17 +27,7 @@ __device__ __forceinline__ uint32_t word4(const uint4& v, int i) { return i == 0
 // exponents, a selected pointer): what must count as nothing -- weights and
 // x beyond K, rows beyond N, slots beyond the share, row indices outside x --
 // has an offset past the resource's end and reads zero, so the loop holds no
-// selects.
-constexpr uint32_t kOutside = 0x7FFF0000u;
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t byte) {
-  const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)byte, 0, 0);
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
-
+// selects.  This is what a UWF1 expert's lane reads there:
 __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
 // BF16 and UWF1: k of MFMA m's eight weights in lane group g, from the start of

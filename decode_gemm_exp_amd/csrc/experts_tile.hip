@@ -49,17 +49,6 @@ namespace {
 typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 
 constexpr int kBK = 64, kBN = 256, kNT = 512;
-constexpr uint32_t kOutside = 0x7FFF0000u;   // past the end of every buffer resource here
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ uint4 bload16(__amdgpu_buffer_rsrc_t r, uint32_t byte) {
-  const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(r, (int)byte, 0, 0);
-  return make_uint4(v.x, v.y, v.z, v.w);
-}
-
-__device__ __forceinline__ uint32_t piece_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ ((row >> 1) & 7)) << 4)); }
 
 // A thread's share of the weight tile: what it loads for a step and how it
 // becomes BF16 in LDS.  Rows: LDS row c of the tile is weight row row_of(c).
@@ -70,17 +59,6 @@ struct Weights;
 // what a K tail or a row index outside x reads where x goes by pointers
 __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
-
-// A block barrier without a fence: a fence would wait for everything that is on
-// its way to LDS.  The caller has waited for what must have landed.
-__device__ __forceinline__ void bare_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
-
 // the piece of its LDS row that lands at this thread's place (see piece_at)
 __device__ __forceinline__ int own_piece() { return (threadIdx.x ^ (threadIdx.x >> 4)) & 7; }
 
@@ -90,7 +68,6 @@ struct Weights<kFormBf16> {
   static constexpr bool kDirect = true;
   __amdgpu_buffer_rsrc_t r;
   uint32_t off[4], col;
-  // (off and col are the same for every tile)
   template <typename RowOf>
   __device__ __forceinline__ void init(const ExpertsView& w, const ExpertsView& u, int e, int64_t n0, RowOf&& row_of) {
     const int tid = threadIdx.x;
@@ -398,7 +375,7 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
     const __amdgpu_buffer_rsrc_t ry =
         rsrc_of(static_cast<char*>(y) + t.sh.first * vw.n * kSize, (uint64_t)t.sh.count * (uint64_t)vw.n * kSize);
     int N = (int)vw.n;
-    asm volatile("" : "+s"(N));   // or every row's offset is kept in registers over all tiles
+    asm volatile("" : "+s"(N));   // or every row's offset is worked out before the loop and kept in registers
     uint32_t at[kCols];
 #pragma unroll
     for (int j = 0; j < kCols; ++j) {
@@ -488,10 +465,6 @@ __global__ __launch_bounds__(kNT) void k_experts_tile(ExpertsView vw, ExpertsVie
   __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more when the block gives it back
 }
 
-// x up to here goes through a buffer resource (an offset past it plus a K tail's
-// kOutside stays below 2^32)
-constexpr int64_t kBigBytes = kOutside;
-
 template <int FORM, int BM, bool GATED, bool BIG = false>
 hipError_t launch_one(const ExpertsCall& c, bool spread, hipStream_t s) {
   const int64_t out = GATED ? 128 : 256, ntiles = (c.w.n + out - 1) / out;
@@ -506,7 +479,7 @@ hipError_t launch_one(const ExpertsCall& c, bool spread, hipStream_t s) {
 
 template <int FORM, bool GATED>
 hipError_t launch_rows(const ExpertsCall& c, int rows, bool spread, hipStream_t s) {
-  if (c.r.x_rows * 2 * c.w.k > kBigBytes) return launch_one<FORM, 256, GATED, true>(c, spread, s);
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_one<FORM, 256, GATED, true>(c, spread, s);
   if (rows <= 64) return launch_one<FORM, 64, GATED>(c, spread, s);
   if (rows <= 128) return launch_one<FORM, 128, GATED>(c, spread, s);
   return launch_one<FORM, 256, GATED>(c, spread, s);

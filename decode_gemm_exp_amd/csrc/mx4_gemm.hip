@@ -26,22 +26,6 @@ typedef __attribute__((ext_vector_type(16))) float f32x16_t;
 typedef __attribute__((ext_vector_type(8))) int i32x8_t;
 
 constexpr int kStep = 256, kBN = 256, kNT = 512;
-constexpr uint32_t kOutside = 0x7FFF0000u;   // past the end of every buffer resource here
-
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc_of(const void* p, uint64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, (int)bytes, 0x00020000);
-}
-__device__ __forceinline__ uint32_t piece_at(int row, int piece) { return (uint32_t)(row * 128 + ((piece ^ ((row >> 1) & 7)) << 4)); }
-
-// A block barrier without a fence: a fence would wait for everything that is on
-// its way to LDS.  The caller has waited for what must have landed.
-__device__ __forceinline__ void bare_barrier() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_sched_barrier(0);
-  asm volatile("" ::: "memory");
-}
 
 template <int BM>
 __global__ __launch_bounds__(kNT) void k_mx4_tile(const uint8_t* __restrict__ we, const uint8_t* __restrict__ ws,
@@ -53,7 +37,6 @@ __global__ __launch_bounds__(kNT) void k_mx4_tile(const uint8_t* __restrict__ we
   constexpr int XP = BM / 64, P = XP + 4;     // pieces a thread moves per step: x, then weights
   constexpr int kRows = BM + kBN;
   constexpr int S = BM == 256 ? 2 : 3;        // buffers: as many as fit
-  typedef __attribute__((address_space(3))) char lds_char;
   // objects of their own rather than parts of one, so that the compiler sees that
   // what is read from or stored to one does not wait for what travels into
   // another
