@@ -100,7 +100,16 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
 
 // Up to this many rows x's 4-bit values go through the register-fed kernel as
 // BF16; beyond, both operands stay in 4 bits.  (The header names this number: the
-// two differ where a weight's value overflows BF16.)
+// two differ where a weight's value overflows BF16.)  Measured (us, register-fed /
+// 4-bit tiles, x's conversion included):
+//   rows           1            8            16           64            128
+//   4096x4096      10.4 / 14.4  10.8 / 15.0  11.3 / 15.4  11.3 / 19.3   16.5 / 19.9
+//   14336x4096     11.1 / 16.2  11.3 / 16.8  11.8 / 17.2  28.1 / 20.4   47.3 / 21.8
+//   5001x8224                   16.6 / 35.1  16.9 / 35.7  26.2 / 41.9   45.4 / 42.5
+//   28672x8192     30.0 / 46.1  34.5 / 47.1  37.3 / 48.1  108.2 / 55.4  123.9 / 55.5
+// (14336x4096 at 32 rows 15.4 / 17.9.)  So the register-fed kernel is the right one
+// up to this many rows, and could serve more: the border lies between 32 and 128
+// rows and moves with the blocks that the tiles make.
 constexpr int64_t kMx4RowsMax = 8;
 
 uw_status check_route(int64_t tokens, int32_t experts, int32_t topk) {

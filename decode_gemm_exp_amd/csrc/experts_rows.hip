@@ -296,7 +296,7 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
 // time: the load unit takes them one by one and was what the kernel waited for
 // (70 % busy).  So a wave sends its weights and scales to a ring of its own in
 // LDS, rows in whole lines, and reads its operands there; nothing but the wave's
-// own loads is waited for (layer of 37 tokens over 32 experts: 128 -> 109 us, 103 now;
+// own loads is waited for (layer of 37 tokens over 32 experts: 128 -> 109 us, 105 now;
 // 4096x4096, 256 rows: 34 -> 25 us).
 // A window is 256 k wide: 64 rows of 128 bytes, piece p of row r at 16 (p ^
 // (r / 2 % 8)), so that the 16 lanes of a read hit all banks.

@@ -12,7 +12,8 @@
 // topk rounds takes the largest key by lane-local maxima and a butterfly of
 // lane permutes, then the lowest index that has it the same way, so nothing
 // leaves registers.  16001 tokens, 160 experts, 6 choices: 8.5 us (12 with key,
-// index and logit searched in one pass, twice the instructions).
+// index and logit searched in one pass, twice the instructions); a bias on the
+// sigmoids costs 2 us more there.
 //
 // Plan.  A stable counting sort of the (token, choice) pairs by expert.  Up to 64
 // pairs one wave does everything, without a barrier, up to 1024 one block;
