@@ -12,8 +12,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libunweight.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
-SOURCES = ["api.cpp", "autotune.cpp", "runtime.cpp", "tables.cpp", "compress.hip", "decode.hip", "experts_api.cpp", "experts_rows.hip", "experts_tile.hip", "gemm.hip", "gemm_mfma.hip", "gemm_rf.hip", "mx4.hip", "mx4_gemm.hip", "route.hip", "static_ws.hip", "yardstick.hip"]
-HEADERS = ["uw_internal.h", "rebuild.h", "experts.h"]
+SOURCES = ["api.cpp", "autotune.cpp", "runtime.cpp", "tables.cpp", "compress.hip", "decode.hip", "experts_api.cpp", "experts_rows.hip", "experts_tile.hip", "fp8.hip", "fp8_rows.hip", "fp8_tile.hip", "gemm.hip", "gemm_mfma.hip", "gemm_rf.hip", "layer.hip", "mx4.hip", "mx4_gemm.hip", "route.hip", "static_ws.hip", "yardstick.hip"]
+HEADERS = ["uw_internal.h", "rebuild.h", "experts.h", "experts_rows.h", "fp8.h", "route.h"]
 COMMON = ["-O3", "-fPIC", "-std=c++17", "-Wall", "-Wno-unused-function"]
 # packed fp32 instructions are kept out of every kernel
 GPU = ["--offload-arch=gfx950", "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]

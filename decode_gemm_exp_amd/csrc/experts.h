@@ -9,11 +9,13 @@ namespace uw {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 16;
+// Tokens of a layer that goes in two kernels; a block of 256 threads holds all their pairs.
+constexpr int kLayerTokens = UW_LAYER_TOKENS, kLayerPairs = kLayerTokens * kMaxTopk;
 
 // Weight forms of the expert products, a template argument of the kernels.
 // kFormPal serves UWF1 matrices whose palettes differ in kind (one of them
 // not a run of consecutive exponents), kFormPalRun those that all are runs.
-enum ExpertForm { kFormBf16 = 0, kFormPal = 2, kFormPalRun = 3, kFormMx4 = 4 };
+enum ExpertForm { kFormBf16 = 0, kFormPal = 2, kFormPalRun = 3, kFormMx4 = 4, kFormFp8 = 5 };
 constexpr bool form_is_pal(int f) { return f == kFormPal || f == kFormPalRun; }
 
 // One UWF1 expert (device table).
@@ -34,8 +36,9 @@ struct ExpertsView {
   int form;
   int count;
   int64_t n, k;
-  const uint8_t* w;        // BF16 rows or packed MXFP4 elements of expert 0
-  const uint8_t* scale;    // MXFP4: scales of expert 0, mx4_scale_stride(k) bytes a row
+  const uint8_t* w;        // BF16 rows, packed MXFP4 elements or E4M3 bytes of expert 0
+  const uint8_t* scale;    // MXFP4: scales of expert 0, mx4_scale_stride(k) bytes a row;
+                           // FP8: floats, one per 128 x 128 block, row-major
   int64_t w_stride;        // bytes from one expert's weights to the next
   int64_t scale_stride;
   const ExpertEntry* table;   // UWF1
@@ -373,6 +376,12 @@ struct RouteCall {
 };
 int route_blocks(int64_t tokens, int topk);   // 1: no workspace
 hipError_t launch_route(const RouteCall& c, hipStream_t s);
+
+// A layer for at most kLayerTokens tokens (route.h): the choice, the plan and the gated
+// product h [tokens * topk][n] by slot (c.r counts for nothing but x_rows), then the down product with the weighted sum.
+hipError_t launch_layer_gated(const ExpertsCall& c, const RouteCall& r, hipStream_t s);
+hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s);
+hipError_t launch_layer_down(const ExpertsView& d, const RouteCall& r, const uint16_t* h, uint16_t* out, hipStream_t s);
 
 // out[t] = sum over j of weights[t][j] d[slots[t][j]], in the order of j
 hipError_t launch_combine(const float* d, const int32_t* slots, const float* weights, int64_t tokens, int topk,

@@ -1,11 +1,12 @@
-// experts_api.cpp -- the extern "C" entry points of the mixture-of-experts and
-// MXFP4 operators (include/unweight.h): argument checks, the experts' weight
+// experts_api.cpp -- the extern "C" entry points of the mixture-of-experts,
+// MXFP4 and FP8 operators (include/unweight.h): argument checks, the experts' weight
 // sets, workspaces.
 #include <cstring>
 #include <new>
 #include <vector>
 
 #include "experts.h"
+#include "fp8.h"
 
 using namespace uw;
 
@@ -19,7 +20,7 @@ uw_status status_of(hipError_t e) {
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 uint64_t pad256(uint64_t n) { return (n + 255) / 256 * 256; }
 
-// A shape the expert and MXFP4 kernels take: k in whole blocks of 32.  The
+// A shape the expert, MXFP4 and FP8 kernels take: k in whole blocks of 32.  The
 // tile kernels address 256 rows of a matrix, and of the output, with 31-bit byte
 // offsets, so k and n stay up to 2^20; every byte count of one matrix is far
 // inside 63 bits.
@@ -79,8 +80,8 @@ uw_status check_rows(const Ragged& r, const void* y) {
   return UW_OK;
 }
 
-uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r, void* y, hipStream_t s) {
-  ExpertsCall c{};
+// the call's weights: w, or w gated with u
+uw_status set_weights(const uw_experts* w, const uw_experts* u, ExpertsCall& c) {
   c.w = w->v;
   c.gated = u != nullptr;
   c.u = u ? u->v : w->v;
@@ -91,6 +92,13 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
       c.w.form = c.u.form = kFormPal;   // the general lookup serves a run as well
     }
   }
+  return UW_OK;
+}
+
+uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r, void* y, hipStream_t s) {
+  ExpertsCall c{};
+  const uw_status st = set_weights(w, u, c);
+  if (st != UW_OK) return st;
   if (r.slots == 0) return UW_OK;
   c.r = RaggedRows{r.offsets, r.rows, r.slots, r.x_rows};
   c.x = r.x;
@@ -115,6 +123,32 @@ constexpr int64_t kMx4RowsMax = 8;
 uw_status check_route(int64_t tokens, int32_t experts, int32_t topk) {
   if (tokens < 0 || experts <= 0 || topk <= 0 || topk > experts) return UW_ERR_INVALID;
   if (experts > kMaxExperts || topk > kMaxTopk || tokens > INT32_MAX / topk) return UW_ERR_UNSUPPORTED;
+  return UW_OK;
+}
+
+// A router's arguments, checked and as the kernels take them.
+uw_status set_route(RouteCall& c, const void* logits_dev, uw_type type, int64_t tokens, int32_t experts, int64_t ld,
+                    const float* bias_dev, int32_t topk, uw_scoring scoring, int32_t* ids_dev, float* weights_dev,
+                    int32_t* offsets_dev, int32_t* rows_dev, int32_t* slots_dev) {
+  if (ld < experts || (tokens != 0 && (!logits_dev || !ids_dev || !weights_dev))) return UW_ERR_INVALID;
+  if (type != UW_TYPE_BF16 && type != UW_TYPE_F32) return UW_ERR_INVALID;
+  if (scoring != UW_SCORE_SOFTMAX && scoring != UW_SCORE_SOFTMAX_TOPK && scoring != UW_SCORE_SIGMOID &&
+      scoring != UW_SCORE_SIGMOID_BIASED)
+    return UW_ERR_INVALID;
+  c.logits = logits_dev;
+  c.bf16 = type == UW_TYPE_BF16;
+  c.tokens = tokens;
+  c.ld = ld;
+  c.experts = experts;
+  c.topk = topk;
+  c.scoring = (int)(scoring == UW_SCORE_SIGMOID_BIASED ? UW_SCORE_SIGMOID : scoring);
+  c.bias = bias_dev;
+  c.on_score = scoring == UW_SCORE_SIGMOID_BIASED && bias_dev;   // (the logits' order is their sigmoids')
+  c.ids = ids_dev;
+  c.weights = weights_dev;
+  c.offsets = offsets_dev;
+  c.rows = rows_dev;
+  c.slots = slots_dev;
   return UW_OK;
 }
 
@@ -210,6 +244,105 @@ uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64
   c.x = x_dev;
   c.y = y_dev;
   return status_of(launch_experts(c, s));
+}
+
+uw_status uw_quantize_fp8(const void* src_dev, uw_type src_type, int64_t rows, int64_t cols, int64_t ld,
+                          int32_t block_rows, uint8_t* elem_dev, float* scale_dev, void* stream) {
+  if (rows == 0) return UW_OK;
+  if (!src_dev || !elem_dev || !scale_dev || rows < 0) return UW_ERR_INVALID;
+  if (src_type != UW_TYPE_BF16 && src_type != UW_TYPE_F32) return UW_ERR_INVALID;
+  if (block_rows != 1 && block_rows != kFp8Block) return UW_ERR_INVALID;
+  const uw_status st = check_shape(rows, cols);
+  if (st != UW_OK) return st;
+  if (ld < cols) return UW_ERR_INVALID;
+  if (ld % 8 != 0) return UW_ERR_UNSUPPORTED;
+  if (!aligned(src_dev, 16) || !aligned(elem_dev, 16) || !aligned(scale_dev, 4)) return UW_ERR_INVALID;
+  return status_of(launch_quantize_fp8(src_dev, src_type == UW_TYPE_F32, rows, cols, ld, block_rows, elem_dev,
+                                       scale_dev, static_cast<hipStream_t>(stream)));
+}
+
+uw_status uw_dequantize_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t rows, int64_t cols,
+                            int32_t block_rows, uint16_t* out_dev, int64_t ld, void* stream) {
+  if (rows == 0) return UW_OK;
+  if (!elem_dev || !scale_dev || !out_dev || rows < 0) return UW_ERR_INVALID;
+  if (block_rows != 1 && block_rows != kFp8Block) return UW_ERR_INVALID;
+  const uw_status st = check_shape(rows, cols);
+  if (st != UW_OK) return st;
+  if (ld < cols) return UW_ERR_INVALID;
+  if (ld % 8 != 0) return UW_ERR_UNSUPPORTED;
+  if (!aligned(elem_dev, 16) || !aligned(scale_dev, 4) || !aligned(out_dev, 16)) return UW_ERR_INVALID;
+  return status_of(launch_dequantize_fp8(elem_dev, scale_dev, rows, cols, block_rows, out_dev, ld,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+uw_status uw_workspace_size_fp8(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes) {
+  if (!bytes || batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_FP8)) return UW_ERR_INVALID;
+  const uw_status st = check_shape(n, k);
+  if (st != UW_OK) return st;
+  // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
+  if (batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512)) return UW_ERR_UNSUPPORTED;
+  const uint64_t b = (uint64_t)batch;
+  *bytes = act != UW_ACT_FP8 || batch <= kFp8RowsMax
+               ? 0
+               : pad256(2 * b * (uint64_t)k) + pad256(4 * b * (uint64_t)fp8_blocks(k));
+  return UW_OK;
+}
+
+uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t n, int64_t k, const uint16_t* x_dev,
+                        int64_t batch, float* y_dev, uw_activation act, void* ws_dev, size_t ws_bytes, void* stream) {
+  if (batch == 0) return UW_OK;
+  if (!elem_dev || !scale_dev || !x_dev || !y_dev) return UW_ERR_INVALID;
+  size_t need = 0;
+  const uw_status st = uw_workspace_size_fp8(n, k, batch, act, &need);
+  if (st != UW_OK) return st;
+  if (!aligned(elem_dev, 16) || !aligned(scale_dev, 4) || !aligned(x_dev, 16) || !aligned(y_dev, 16) ||
+      !aligned(ws_dev, 16))
+    return UW_ERR_INVALID;
+  if (need && (!ws_dev || ws_bytes < need)) return UW_ERR_WORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  ExpertsCall c{};
+  c.w.form = kFormFp8;
+  c.w.count = 1;
+  c.w.n = n;
+  c.w.k = k;
+  c.w.w = elem_dev;
+  c.w.scale = reinterpret_cast<const uint8_t*>(scale_dev);
+  c.u = c.w;
+  c.r = RaggedRows{nullptr, nullptr, batch, batch};
+  c.x = x_dev;
+  c.y = y_dev;
+  if (act == UW_ACT_FP8) {
+    uint8_t* xe = static_cast<uint8_t*>(ws_dev);
+    return status_of(launch_fp8_act(c, reinterpret_cast<uint16_t*>(xe),
+                                    reinterpret_cast<float*>(xe + pad256(2 * (uint64_t)batch * (uint64_t)k)), s));
+  }
+  return status_of(launch_experts(c, s));
+}
+
+uw_status uw_experts_fp8(const uint8_t* elem_dev, const float* scale_dev, int32_t count, int64_t n, int64_t k,
+                         int64_t elem_stride, int64_t scale_stride, uw_experts** out) {
+  uw_status st = new_set(count, n, k, out);
+  if (st != UW_OK) return st;
+  uw_experts* h = *out;
+  const int64_t eb = n * k, sb = fp8_blocks(n) * fp8_blocks(k);
+  if (elem_stride == 0) elem_stride = eb;
+  if (scale_stride == 0) scale_stride = sb;
+  if (!elem_dev || !scale_dev || !aligned(elem_dev, 16) || !aligned(scale_dev, 4) || elem_stride < eb ||
+      scale_stride < sb)
+    st = UW_ERR_INVALID;
+  else if (elem_stride % 16 != 0 || elem_stride > INT64_MAX / count || scale_stride > INT64_MAX / 4 / count)
+    st = UW_ERR_UNSUPPORTED;
+  if (st != UW_OK) {
+    delete h;
+    *out = nullptr;
+    return st;
+  }
+  h->v.form = kFormFp8;
+  h->v.w = elem_dev;
+  h->v.w_stride = elem_stride;
+  h->v.scale = reinterpret_cast<const uint8_t*>(scale_dev);
+  h->v.scale_stride = 4 * scale_stride;
+  return UW_OK;
 }
 
 uw_status uw_experts_bf16(const uint16_t* w_dev, int32_t count, int64_t n, int64_t k, int64_t stride,
@@ -336,26 +469,10 @@ uw_status uw_route_experts(const void* logits_dev, uw_type type, int64_t tokens,
                            const float* bias_dev, int32_t topk, uw_scoring scoring, int32_t* ids_dev,
                            float* weights_dev, int32_t* offsets_dev, int32_t* rows_dev, int32_t* slots_dev,
                            void* ws_dev, size_t ws_bytes, void* stream) {
-  if (ld < experts || (tokens != 0 && (!logits_dev || !ids_dev || !weights_dev))) return UW_ERR_INVALID;
-  if (type != UW_TYPE_BF16 && type != UW_TYPE_F32) return UW_ERR_INVALID;
-  if (scoring != UW_SCORE_SOFTMAX && scoring != UW_SCORE_SOFTMAX_TOPK && scoring != UW_SCORE_SIGMOID &&
-      scoring != UW_SCORE_SIGMOID_BIASED)
-    return UW_ERR_INVALID;
   RouteCall c{};
-  c.logits = logits_dev;
-  c.bf16 = type == UW_TYPE_BF16;
-  c.tokens = tokens;
-  c.ld = ld;
-  c.experts = experts;
-  c.topk = topk;
-  c.scoring = (int)(scoring == UW_SCORE_SIGMOID_BIASED ? UW_SCORE_SIGMOID : scoring);
-  c.bias = bias_dev;
-  c.on_score = scoring == UW_SCORE_SIGMOID_BIASED && bias_dev;   // (the logits' order is their sigmoids')
-  c.ids = ids_dev;
-  c.weights = weights_dev;
-  c.offsets = offsets_dev;
-  c.rows = rows_dev;
-  c.slots = slots_dev;
+  const uw_status st = set_route(c, logits_dev, type, tokens, experts, ld, bias_dev, topk, scoring, ids_dev, weights_dev,
+                                 offsets_dev, rows_dev, slots_dev);
+  if (st != UW_OK) return st;
   return run_route(c, ws_dev, ws_bytes, static_cast<hipStream_t>(stream));
 }
 
@@ -431,6 +548,53 @@ uw_status uw_expert_mlp(const uw_experts* gate, const uw_experts* up, const uw_e
   if (st == UW_OK) st = run_experts(down, nullptr, mid, d, s);
   if (st == UW_OK) st = status_of(launch_combine(d, slots_dev, weights_dev, tokens, topk, down->v.n, pairs, out_dev, s));
   return st;
+}
+
+uw_status uw_workspace_size_expert_layer(const uw_experts* gate, const uw_experts* down, int64_t tokens, int32_t topk,
+                                         size_t* bytes) {
+  size_t mlp = 0, route = 0;
+  uw_status st = uw_workspace_size_expert_mlp(gate, down, tokens, topk, bytes ? &mlp : nullptr);
+  if (st == UW_OK) st = uw_workspace_size_route(tokens, gate->v.count, topk, &route);
+  if (st != UW_OK) return st;
+  *bytes = tokens <= kLayerTokens ? pad256(2 * (uint64_t)(tokens * topk) * (uint64_t)gate->v.n) : mlp + route;
+  return UW_OK;
+}
+
+uw_status uw_expert_layer(const uw_experts* gate, const uw_experts* up, const uw_experts* down, const void* logits_dev,
+                          uw_type type, int64_t tokens, int64_t ld, const float* bias_dev, int32_t topk,
+                          uw_scoring scoring, int32_t* ids_dev, float* weights_dev, int32_t* offsets_dev,
+                          int32_t* rows_dev, int32_t* slots_dev, const uint16_t* x_dev, uint16_t* out_dev, void* ws_dev,
+                          size_t ws_bytes, void* stream) {
+  if (!up) return UW_ERR_INVALID;
+  size_t need = 0;
+  uw_status st = uw_workspace_size_expert_layer(gate, down, tokens, topk, &need);
+  RouteCall r{};
+  if (st == UW_OK)
+    st = set_route(r, logits_dev, type, tokens, gate->v.count, ld, bias_dev, topk, scoring, ids_dev, weights_dev,
+                   offsets_dev, rows_dev, slots_dev);
+  if (st != UW_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (tokens == 0) return run_route(r, ws_dev, ws_bytes, s);   // the offsets
+  if (!offsets_dev || !rows_dev || !slots_dev || !x_dev || !out_dev) return UW_ERR_INVALID;
+  if (need && (!ws_dev || ws_bytes < need)) return UW_ERR_WORKSPACE;
+  if (!aligned(ws_dev, 16) || !aligned(x_dev, 16) || !aligned(out_dev, 16)) return UW_ERR_INVALID;
+  for (const uw_experts* e : {gate, up, down})
+    if (st == UW_OK) st = check_set(e);
+  ExpertsCall c{};
+  if (st == UW_OK) st = set_weights(gate, up, c);
+  if (st != UW_OK) return st;
+  if (tokens > kLayerTokens) {
+    size_t mlp = 0;
+    st = uw_workspace_size_expert_mlp(gate, down, tokens, topk, &mlp);
+    if (st == UW_OK) st = run_route(r, static_cast<uint8_t*>(ws_dev) + mlp, need - mlp, s);
+    return st != UW_OK ? st : uw_expert_mlp(gate, up, down, tokens, topk, offsets_dev, rows_dev, slots_dev, weights_dev,
+                                            x_dev, out_dev, ws_dev, mlp, stream);
+  }
+  c.r = RaggedRows{nullptr, nullptr, tokens * topk, tokens};
+  c.x = x_dev;
+  c.y = ws_dev;
+  st = status_of(launch_layer_gated(c, r, s));
+  return st != UW_OK ? st : status_of(launch_layer_down(down->v, r, static_cast<const uint16_t*>(ws_dev), out_dev, s));
 }
 
 }  // extern "C"

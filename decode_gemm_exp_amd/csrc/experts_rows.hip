@@ -16,196 +16,30 @@
 //     nibble forms give lane group g a run of 32 (MXFP4: 64) consecutive k, so
 //     that a lane's weights lie in one UWF1 group or whole MXFP4 blocks;
 //   * the waves' sums meet in LDS and are added in a fixed order.
-#include "experts.h"
+#include "experts_rows.h"
+#include "fp8.h"
 
 namespace uw {
 namespace {
 
-__device__ __forceinline__ uint32_t word4(const uint4& v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-
-// Every load goes through a buffer resource (or, for a UWF1 expert's
-// exponents, a selected pointer): what must count as nothing -- weights and
-// x beyond K, rows beyond N, slots beyond the share, row indices outside x --
-// has an offset past the resource's end and reads zero, so the loop holds no
-// selects.  This is what a UWF1 expert's lane reads there:
-__device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
-
-// BF16 and UWF1: k of MFMA m's eight weights in lane group g, from the start of
-// a window of 128
-template <int FORM>
-__device__ __forceinline__ int k_off(int m, int g) {
-  return FORM == kFormBf16 ? 32 * m + 8 * g : 32 * g + 8 * m;
-}
-
-// A block's rows [n0, n0 + rows) of one expert's matrix.
-template <int FORM>
-struct Mat {
-  __amdgpu_buffer_rsrc_t w;   // BF16: from row n0
-  ExpertEntry t;              // UWF1
-  uint32_t el0, el_end;       // ... its elements [n0 K, (n0 + rows) K)
-};
-
-template <int FORM>
-__device__ __forceinline__ Mat<FORM> matrix_of(const ExpertsView& v, int e, int64_t n0, int span) {
-  Mat<FORM> m{};
-  const int64_t rows = v.n - n0 < span ? v.n - n0 : span;
-  if constexpr (form_is_pal(FORM)) {
-    m.t = v.table[e];
-    m.el0 = (uint32_t)(n0 * v.k);
-    m.el_end = (uint32_t)((n0 + rows) * v.k);
-    m.w = rsrc_of(m.t.sm + n0 * v.k, (uint64_t)(rows * v.k));
-  } else {
-    m.w = rsrc_of(v.w + (int64_t)e * v.w_stride + n0 * 2 * v.k, (uint64_t)(rows * 2 * v.k));
-  }
-  return m;
-}
-
-// A lane's weights of one window of one row, as loaded:
-//   BF16: d[m] = the eight of MFMA m;  UWF1: d[0], d[1] = 32 sign+mantissa
-//   bytes, d[2] = 32 index nibbles, or d[2], d[3] = 32 exponent bytes when f
-//   (verbatim group)
-struct Raw {
-  uint4 d[4];
-  uint32_t f;
-};
-
-// flag and rank words of the lane's group (UWF1), loaded a window ahead
-struct Flags {
-  uint32_t fw, rw;
-};
-
-// row: from n0
-template <int FORM>
-__device__ __forceinline__ void load_flags(const Mat<FORM>& m, int row, int K, int k, Flags& f) {
-  if constexpr (form_is_pal(FORM)) {
-    const uint32_t el = m.el0 + (uint32_t)row * (uint32_t)K + (uint32_t)k;
-    const uint32_t w = (k < K && el < m.el_end ? el : m.el0) >> 11;
-    f.fw = gload<uint32_t>(m.t.vflags + w);
-    f.rw = gload<uint32_t>(m.t.vrank + w);
-  }
-}
-
-// k0: the window's start (K or more: nothing)
-template <int FORM>
-__device__ __forceinline__ void load_raw(const Mat<FORM>& m, int row, int K, int k0, int g, const Flags& fl, Raw& r) {
-  if constexpr (FORM == kFormBf16) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = k0 + k_off<FORM>(i, g);
-      r.d[i] = bload16(m.w, k < K ? (uint32_t)(row * K + k) * 2u : kOutside);
-    }
-  } else {
-    const int k = k0 + k_off<FORM>(0, g);
-    const uint32_t at = (uint32_t)row * (uint32_t)K + (uint32_t)k, el = m.el0 + at;
-    const bool in = k < K && el < m.el_end;
-    r.d[0] = bload16(m.w, in ? at : kOutside);
-    r.d[1] = bload16(m.w, in ? at + 16u : kOutside);
-    const uint32_t grp = el >> 6;
-    const bool v = in && group_verbatim(fl.fw, grp);
-    const uint32_t vo = group_rank(fl.fw, fl.rw, grp) * 64u + (el & 63u);
-    // outside the matrix the exponents are zeros, as of a verbatim group
-    const uint8_t* p = v ? m.t.vexp + vo : in ? m.t.pidx + el / 2 : reinterpret_cast<const uint8_t*>(g_zero16);
-    r.d[2] = gload16(p);
-    r.d[3] = make_uint4(0u, 0u, 0u, 0u);
-    if (v) r.d[3] = gload16(p + 16);   // (rarely any lane: a fourth load for all would cost 10 %)
-    r.f = v || !in ? 1u : 0u;
-  }
-}
-
-// A operand of MFMA m
-template <int FORM>
-__device__ __forceinline__ bf16x8_t a_frag(const Mat<FORM>& mt, const Raw& r, int m) {
-  uint4 o;
-  if constexpr (FORM == kFormBf16) {
-    o = r.d[m];
-  } else {
-    const int wi = 2 * (m & 1);
-    uint32_t e0, e1;
-    pal8<FORM == kFormPalRun>(word4(r.d[2], m), mt.t.pal, e0, e1);
-    e0 = r.f ? word4(r.d[2 + (m >> 1)], wi) : e0;
-    e1 = r.f ? word4(r.d[2 + (m >> 1)], wi + 1) : e1;
-    rebuild4(word4(r.d[m >> 1], wi), e0, o.x, o.y);
-    rebuild4(word4(r.d[m >> 1], wi + 1), e1, o.z, o.w);
-  }
-  return __builtin_bit_cast(bf16x8_t, o);
-}
-
-// A block's tile of output rows and chunk of slots.  The chunks of one matrix
-// read the same weights, so a tile's chunks follow each other on one XCD and
-// share them in its L2 (MXFP4 5001x8224, 45 rows: 18.1 -> 15.2 us).  Experts'
-// chunks share little, and all XCDs walking through an expert together do
-// better (MXFP4 layer of 37 tokens over 32 experts: 109 us against 118).
-struct Place {
-  unsigned tile, chunk;
-};
-__device__ __forceinline__ Place place_of(const RaggedRows& rr, unsigned ntiles, unsigned chunks) {
-  if (rr.offsets) return {blockIdx.x % ntiles, blockIdx.x / ntiles};
-  const unsigned turn = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);   // (the grid is a multiple of 8)
-  return {turn / chunks, turn % chunks};
-}
-
-// The waves' sums, added in wave order and stored.  red: per wave and tile
-// the MFMA's D: lane l holds output features 4 (l / 16) .. +3 of slot l % 16.
-template <int R, int Q, bool GATED, int NW>
-__device__ __forceinline__ void finish(const f32x4_t* red, const Share& sh, int64_t n0, int64_t N, void* __restrict__ y) {
-  constexpr int RT = GATED ? R / 2 : R;
-  for (int i = threadIdx.x; i < RT * Q * 64; i += 64 * NW) {
-    const int ln = i & 63, q = (i >> 6) % Q, t = (i >> 6) / Q;
-    auto sum = [&](int tt) __attribute__((always_inline)) {
-      f32x4_t s = red[(tt * Q + q) * 64 + ln];
-#pragma unroll
-      for (int v = 1; v < NW; ++v) s += red[((v * R + tt) * Q + q) * 64 + ln];
-      return s;
-    };
-    f32x4_t s = sum(t);
-    const int b = 16 * q + (ln & 15);
-    const int64_t n = n0 + 16 * t + 4 * (ln >> 4);
-    if (b >= sh.count || n >= N) continue;
-    const int64_t at = (sh.first + b) * N + n;
-    if constexpr (GATED) {
-      const f32x4_t u = sum(t + RT);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) s[c] = silu(s[c]) * u[c];
-      uint16_t* o = static_cast<uint16_t*>(y) + at;
-      const uint32_t lo = bf16_pair(s[0], s[1]), hi = bf16_pair(s[2], s[3]);
-      if ((N & 3) == 0) {
-        *reinterpret_cast<uint2*>(o) = make_uint2(lo, hi);
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < N) o[c] = (uint16_t)((c < 2 ? lo : hi) >> (16 * (c & 1)));
-      }
-    } else {
-      float* o = static_cast<float*>(y) + at;
-      if ((N & 3) == 0) {
-        *reinterpret_cast<f32x4_t*>(o) = s;
-      } else {
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (n + c < N) o[c] = s[c];
-      }
-    }
-  }
-}
-
 // R weight tiles of 16 rows (gated: the first half from W, the second the
 // same rows of U), Q groups of 16 slots
-template <int FORM, int R, int Q, bool GATED>
-__global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsView vu, RaggedRows rr,
+template <int FORM, int R, int Q, bool GATED, typename RR>
+__global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsView vu, RR rr,
                                                       const uint16_t* __restrict__ x, void* __restrict__ y,
                                                       int ntiles, int chunks) {
   constexpr int W = 128;
   constexpr int RT = GATED ? R / 2 : R;   // distinct output tiles
   __shared__ f32x4_t red[4 * R * Q * 64];
-  const Place at = place_of(rr, (unsigned)ntiles, (unsigned)chunks);
-  if (at.tile >= (unsigned)ntiles || at.chunk >= (unsigned)chunks) return;
-  const Share sh = find_share(rr, vw.count, at.chunk, 16 * Q);
-  if (sh.count == 0) return;
+  __shared__ typename Finder<RR>::Lds found;
+  unsigned tile;
+  Share sh;
+  if (!Finder<RR>::find(rr, found, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i16 = lane & 15, g = lane >> 4;
   const int64_t N = vw.n;
   const int K = (int)vw.k;
-  const int64_t n0 = (int64_t)at.tile * (16 * RT);
+  const int64_t n0 = (int64_t)tile * (16 * RT);
   const Mat<FORM> mw = matrix_of<FORM>(vw, sh.expert, n0, 16 * RT);
   Mat<FORM> mu = mw;
   if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert, n0, 16 * RT);
@@ -215,13 +49,8 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   // x rows of this lane's slots
   const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
   uint32_t xrow[Q];
-  int32_t row[Q];   // (fewer than 2^31 slots)
-#pragma unroll
-  for (int q = 0; q < Q; ++q) row[q] = (int32_t)sh.first + (16 * q + i16 < sh.count ? 16 * q + i16 : 0);
-  if (rr.rows) {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) row[q] = rr.rows[row[q]];
-  }
+  int32_t row[Q];
+  Finder<RR>::rows(rr, found, sh, row, [&](int q) __attribute__((always_inline)) { return 16 * q + i16; });
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
     const bool in = (16 * q + i16 < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
@@ -308,8 +137,8 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
 // four / two waves: 5120x5120, 64 rows, 320 blocks 18.5 / 14.4; 14336x4096, 32 rows, 448
 // blocks 15.1 / 13.0; 14 rows, 224 blocks 9.5 / 11.5).  Without XL four waves it is (two /
 // four / eight: one row of 14336x4096 9.7 / 8.0 / 9.3, layer of 37 tokens 111 / 104 / 146).
-template <int Q, bool GATED, bool XL, int NW>
-__global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, ExpertsView vu, RaggedRows rr,
+template <int Q, bool GATED, bool XL, int NW, typename RR>
+__global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, ExpertsView vu, RR rr,
                                                      const uint16_t* __restrict__ x, void* __restrict__ y,
                                                      int ntiles, int chunks) {
   constexpr int R = 4, RT = GATED ? 2 : 4, kRows = 16 * RT;
@@ -317,15 +146,15 @@ __global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, Experts
   __shared__ __attribute__((aligned(128))) char w0[NW * kW], w1[NW * kW], s0[NW * kS], s1[NW * kS];
   constexpr int kX = XL ? 16 * 512 : 4;
   __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
-  const Place at = place_of(rr, (unsigned)ntiles, (unsigned)chunks);
-  if (at.tile >= (unsigned)ntiles || at.chunk >= (unsigned)chunks) return;
-  const Share sh = find_share(rr, vw.count, at.chunk, 16 * Q);
-  if (sh.count == 0) return;
+  __shared__ typename Finder<RR>::Lds found;
+  unsigned tile;
+  Share sh;
+  if (!Finder<RR>::find(rr, found, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int i16 = lane & 15, g = lane >> 4;
   const int64_t N = vw.n;
   const int K = (int)vw.k, st = (int)mx4_scale_stride(K);
-  const int64_t n0 = (int64_t)at.tile * kRows;
+  const int64_t n0 = (int64_t)tile * kRows;
   const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
   auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
     return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * (K / 2), (uint64_t)(rows * (K / 2)));
@@ -342,12 +171,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, Experts
   uint32_t xrow[XR];
   int32_t row[XR];
   auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 2 * q + (lane >> 5) : 16 * q + i16; };
-#pragma unroll
-  for (int q = 0; q < XR; ++q) row[q] = (int32_t)sh.first + (slot(q) < sh.count ? slot(q) : 0);   // (fewer than 2^31 slots)
-  if (rr.rows) {
-#pragma unroll
-    for (int q = 0; q < XR; ++q) row[q] = rr.rows[row[q]];
-  }
+  Finder<RR>::rows(rr, found, sh, row, slot);
 
   f32x4_t acc[R][Q];
 #pragma unroll
@@ -476,17 +300,17 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (!grid_fits(grid, 256)) return hipErrorNotSupported;
   if constexpr (FORM == kFormMx4) {
-    auto k = k_experts_mx4<Q, GATED, false, 4>;
+    auto k = k_experts_mx4<Q, GATED, false, 4, RaggedRows>;
     int waves = 4;
     if constexpr (Q == 1 && !GATED) {
       if (!c.r.offsets && c.r.slots > 7) {   // one matrix, slots mostly filled
         waves = grid > device_cus() ? 2 : 4;
-        k = waves == 2 ? k_experts_mx4<1, false, true, 2> : k_experts_mx4<1, false, true, 4>;
+        k = waves == 2 ? k_experts_mx4<1, false, true, 2, RaggedRows> : k_experts_mx4<1, false, true, 4, RaggedRows>;
       }
     }
     hipLaunchKernelGGL(k, dim3((unsigned)grid), dim3(64 * waves), 0, s, c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
   } else {
-    hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,
+    hipLaunchKernelGGL((k_experts_rows<FORM, R, Q, GATED, RaggedRows>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, c.r, c.x,
                        c.y, (int)ntiles, (int)chunks);
   }
   return hipGetLastError();
@@ -516,7 +340,34 @@ hipError_t launch_gated(const ExpertsCall& c, int64_t avg, hipStream_t s) {
   return c.gated ? launch_form<FORM, true>(c, avg, s) : launch_form<FORM, false>(c, avg, s);
 }
 
+template <int FORM>
+hipError_t launch_routed(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
+  const int64_t rows = FORM == kFormMx4 ? 32 : 16, ntiles = (c.w.n + rows - 1) / rows, grid = routed_grid(r, ntiles);
+  if (!grid_fits(grid, 256)) return hipErrorNotSupported;
+  return with_routed(r, [&](auto rr) {
+    using RR = decltype(rr);
+    if constexpr (FORM == kFormMx4) {
+      hipLaunchKernelGGL((k_experts_mx4<1, true, false, 4, RR>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, rr,
+                         c.x, c.y, (int)ntiles, 0);
+    } else {
+      hipLaunchKernelGGL((k_experts_rows<FORM, 2, 1, true, RR>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u, rr,
+                         c.x, c.y, (int)ntiles, 0);
+    }
+    return hipGetLastError();
+  });
+}
+
 }  // namespace
+
+hipError_t launch_layer_gated(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
+  switch (c.w.form) {
+    case kFormBf16: return launch_routed<kFormBf16>(c, r, s);
+    case kFormPal: return launch_routed<kFormPal>(c, r, s);
+    case kFormPalRun: return launch_routed<kFormPalRun>(c, r, s);
+    case kFormFp8: return launch_layer_gated_fp8(c, r, s);
+    default: return launch_routed<kFormMx4>(c, r, s);
+  }
+}
 
 hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
   const int64_t e = c.r.offsets ? c.w.count : 1, avg = (c.r.slots + e - 1) / e;
@@ -547,6 +398,7 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
 //   MXFP4 14336x4096: 64 rows 25 / 52 / 59, 128 rows 45 / 55 / 60, 256 rows 74 / 58 / 61
 //   MXFP4, few tiles: 5001x8224, 200 rows 58 / 109 / 125; 4096x4096, 256 rows 25 / 52 / 63
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
+  if (c.w.form == kFormFp8) return launch_fp8(c, s);
   const int64_t e = c.r.offsets ? c.w.count : 1;
   const int64_t avg = (c.r.slots + e - 1) / e;
   if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_experts_tile(c, 256, false, s);   // x past 2 GiB: by pointers

@@ -1,0 +1,387 @@
+// fp8_tile.hip -- products with E4M3 weights (an FP32 scale per 128 x 128 block) for
+// many rows: LDS-tiled v_mfma_f32_32x32x16_bf16, plain (fp32 out) and gated
+// (silu(x G^T) * (x U^T), BF16 out), one matrix or grouped by expert, x in BF16 or
+// E4M3 values held as BF16 with a scale per 1 x 128 (ACT8).
+//
+// Elements go through the BF16 instruction, where they and their products are exact
+// and sums are FP32.  (v_mfma_f32_32x32x64_f8f6f4 would take the bytes as they are at
+// twice the rate, but it adds products in groups of eight aligned to the largest and
+// drops what lies below 2^-13 of it: 2.2e-5 of the result's norm at 5001x8224, 13 rows,
+// against 9e-8 here.)
+//
+// A block computes BM slots times 256 weight rows (gated: 128 gate rows and the same
+// 128 up rows, 32 by 32 interleaved so that a wave holds both factors of its
+// outputs); eight waves, two along the slots and four along the columns.  K advances
+// by 128, one block of scales: the sum over a block is gathered in registers of its
+// own and added, scaled, to the running sum while the next block's first MFMAs run.
+// Weights are the MFMA's A and x its B, so that a lane's sixteen outputs of a tile lie
+// in one slot and share its scale.
+//
+// LDS holds x as BF16, rows of 256 bytes, 16-byte piece c of row r at c ^ (r % 16), and
+// the weights as they are, rows of 128 bytes (piece_at); both travel straight from
+// memory.  A lane's piece of weights, 16 of a row's k, is two slices' worth; it becomes
+// BF16 in registers.  The order of k inside a slice is free as long as both operands
+// agree: half h of the lanes takes k 32 (t / 2) + 16 h + 8 (t % 2) .. +7 of slice t.
+// The one barrier of a step stands before its last slice's MFMAs, and the buffer the
+// step leaves is refilled right behind it.
+#include <type_traits>
+
+#include "fp8.h"
+
+namespace uw {
+namespace {
+
+typedef __attribute__((ext_vector_type(16))) float f32x16_t;
+
+constexpr int kBN = 256, kNT = 512, kStep = kFp8Block;
+
+// what a K tail or a row index outside x reads where x goes by pointers
+__device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
+
+struct ActScales {
+  const float* s;   // [rows][blocks of k] (ACT8)
+};
+
+template <int BM, bool GATED, bool ACT8, bool BIG>
+__global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu, RaggedRows rr,
+                                                  const uint16_t* __restrict__ x, ActScales act, void* __restrict__ y,
+                                                  int ntiles, int spread) {
+  constexpr int TM = BM / 64;                 // 32-slot tiles of a wave; two column tiles
+  constexpr int OUT = GATED ? 128 : 256;      // output columns of a block
+  constexpr int XP = BM / 32, WP = 4, P = XP + WP;   // pieces a thread moves per step
+  constexpr int S = BM == 64 ? 3 : 2;         // buffers: as many as fit
+  constexpr int kX = BM * 256, kW = kBN * 128;
+  // objects of their own rather than parts of one, so that the compiler sees that
+  // what is read from one does not wait for what travels into another
+  __shared__ __attribute__((aligned(256))) char x0[kX], x1[kX], w0[kW], w1[kW];
+  __shared__ __attribute__((aligned(256))) char x2[S > 2 ? kX : 16], w2[S > 2 ? kW : 16];
+  char* const xbufs[3] = {x0, x1, x2};
+  char* const wbufs[3] = {w0, w1, w2};
+
+  Share sh;
+  const int nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, ntiles, BM, sh);
+  if (nt < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3, col = lane & 31, half = lane >> 5;
+  const int K = (int)vw.k, steps = (int)fp8_blocks(K);
+  const int64_t n0 = (int64_t)nt * OUT;
+
+  // x: thread t's pieces are those at its place, piece t % 16 ^ t / 16 % 16 of rows t / 16 + 32 i
+  const int xcol = 8 * ((tid ^ (tid >> 4)) & 15);
+  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, BIG ? 0 : (uint64_t)rr.x_rows * 2 * K);
+  uint32_t xo[XP];
+  const uint16_t* xp[XP];
+  int32_t rows[XP];   // (fewer than 2^31 slots); all indices loaded before one is used
+#pragma unroll
+  for (int i = 0; i < XP; ++i) rows[i] = (int32_t)sh.first + (tid / 16 + 32 * i < sh.count ? tid / 16 + 32 * i : 0);
+  if (rr.rows) {
+#pragma unroll
+    for (int i = 0; i < XP; ++i) rows[i] = rr.rows[rows[i]];
+  }
+#pragma unroll
+  for (int i = 0; i < XP; ++i) {
+    const int64_t row = rows[i];
+    const bool in = (row >= 0) & (row < rr.x_rows);
+    xo[i] = in ? (uint32_t)(2 * (row * K + xcol)) : kOutside;
+    xp[i] = in ? x + row * K + xcol : nullptr;
+  }
+  auto direct_x = [&](int k0, char* buf, int i) __attribute__((always_inline)) {
+    lds_char* to = (lds_char*)(buf + wave * 1024 + 8192 * i);
+    if constexpr (BIG) {
+      const void* p = xp[i] && k0 + xcol < K ? (const void*)(xp[i] + k0) : (const void*)g_zero16;
+      __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, to, 16, 0, 0);
+    } else {
+      const uint32_t ko = k0 + xcol < K ? 2u * (uint32_t)k0 : kOutside;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, to, 16, (int)(xo[i] + ko), 0, 0, 0);
+    }
+  };
+  // weights: piece t % 8 ^ t / 16 % 8 of LDS rows t / 8 + 64 i; LDS row c is weight row c, gated 32 by 32 of gate
+  // and up (a wave's eight rows, and all four i, are of one of the two)
+  const int wcol = 16 * ((tid ^ (tid >> 4)) & 7);
+  const bool up = GATED && (tid / 8 & 32);
+  const ExpertsView& mine = __builtin_amdgcn_readfirstlane((int)up) ? vu : vw;
+  const int64_t rows_w = vw.n - n0 < OUT ? vw.n - n0 : OUT;
+  const __amdgpu_buffer_rsrc_t rw =
+      rsrc_of(mine.w + (int64_t)sh.expert * mine.w_stride + n0 * K, (uint64_t)rows_w * (uint64_t)K);
+  const uint32_t wo = (uint32_t)(GATED ? tid / 8 & 31 : tid / 8) * (uint32_t)K + (uint32_t)wcol;
+  const uint32_t rows64 = (GATED ? 32u : 64u) * (uint32_t)K;
+  auto direct_w = [&](int k0, char* buf, int i) __attribute__((always_inline)) {
+    const uint32_t ko = k0 + wcol < K ? (uint32_t)k0 : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (lds_char*)(buf + wave * 1024) + 8192 * i, 16,
+                                             (int)(wo + ko + (uint32_t)i * rows64), 0, 0, 0);
+  };
+
+  // Scales of a step: the wave's columns lie in one row of blocks (gated: one of gate's
+  // and one of up's), its slots are one a lane.
+  const int64_t block_row = (GATED ? n0 : n0 + wn * 64) >> 7;
+  auto scales_of = [&](const ExpertsView& v) __attribute__((always_inline)) {
+    return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + block_row * steps * 4,
+                   block_row < fp8_blocks(v.n) ? (uint64_t)steps * 4 : 0);
+  };
+  const __amdgpu_buffer_rsrc_t rs0 = scales_of(vw), rs1 = GATED ? scales_of(vu) : rs0;
+  const __amdgpu_buffer_rsrc_t ra = rsrc_of(ACT8 ? act.s + sh.first * steps : nullptr,
+                                            ACT8 ? (uint64_t)sh.count * (uint64_t)steps * 4 : 0);
+  auto slot_of = [&](int i) __attribute__((always_inline)) { return 64 * i + 32 * wm; };
+  struct Scales {
+    float w[2], x[TM];
+  };
+  // spread: each block starts its walk along K elsewhere (see experts_tile.hip)
+  const int rot = spread ? (int)((blockIdx.x * 5u) % (unsigned)steps) : 0;
+  auto block_of = [&](int s) __attribute__((always_inline)) {   // past the last: a block past K
+    const int ss = s + rot;
+    return s >= steps ? steps : ss >= steps ? ss - steps : ss;
+  };
+  auto load_scales = [&](int s, Scales& c) __attribute__((always_inline)) {
+    const int b = block_of(s), at = b < steps ? 4 * b : (int)kOutside;
+    c.w[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs0, at, 0, 0));
+    c.w[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs1, at, 0, 0)) : c.w[0];
+    if constexpr (ACT8) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+        c.x[i] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(ra, at + 4 * steps * (slot_of(i) + col), 0, 0));
+    }
+  };
+
+  f32x16_t acc[TM][2], part[TM][2];
+  bf16x8_t fx[2][TM];
+  uint4 fw[2][2];   // two slices' weights, current and next
+  Scales sc[2];
+  // Addresses: one base each, the slice flipping some of its bits (the empty asm keeps
+  // the compiler from holding every slice's address in a register).
+  const uint32_t base_x = (uint32_t)((32 * wm + col) * 256 + ((2 * half ^ (col & 15)) << 4));
+  const uint32_t base_w = piece_at(wn * 64 + col, half);
+  auto read_x = [&](const char* buf, int t, int p, auto TA) __attribute__((always_inline)) {
+    uint32_t a = base_x;
+    asm volatile("" : "+v"(a));
+    a ^= (uint32_t)(64 * (t >> 1) + 16 * (t & 1));   // piece 4 (t / 2) + 2 half + t % 2
+#pragma unroll
+    for (int i = 0; i < decltype(TA)::value; ++i) fx[p][i] = *reinterpret_cast<const bf16x8_t*>(buf + a + i * 64 * 256);
+  };
+  auto read_w = [&](const char* buf, int t2, int p) __attribute__((always_inline)) {
+    uint32_t b = base_w;
+    asm volatile("" : "+v"(b));
+    b ^= 32u * (uint32_t)t2;   // piece 2 t2 + half
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fw[p][j] = *reinterpret_cast<const uint4*>(buf + b + j * 4096);
+  };
+  auto a_of = [&](int t, int j) __attribute__((always_inline)) {
+    const uint4& q = fw[t >> 1 & 1][j];
+    return __builtin_bit_cast(bf16x8_t, t & 1 ? fp8_unpack8(q.z, q.w) : fp8_unpack8(q.x, q.y));
+  };
+  auto fold = [&](const Scales& c, int i, int j) __attribute__((always_inline)) {
+    const float s = ACT8 ? c.x[i] * c.w[j] : c.w[j];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[i][j][r], s, acc[i][j][r]);
+  };
+
+  // Step s finds its data in buffers J % S; the sums of the step before, scaled by
+  // sc[(J + 1) % 2], are added on the way.  TA: the wave's slot tiles that hold slots
+  // (0: it moves data for the others).
+  auto step = [&](int s, auto J, auto TA) __attribute__((always_inline)) {
+    constexpr int j = decltype(J)::value, ta = decltype(TA)::value;
+    char* const xcur = xbufs[j % S];
+    char* const wcur = wbufs[j % S];
+    if constexpr (ta > 0) {
+#pragma unroll
+      for (int t = 0; t < 7; ++t) {
+        // (the scheduling barriers keep each slice's reads ahead of the MFMAs of the
+        // slice before, which cover their latency)
+        read_x(xcur, t + 1, (t + 1) & 1, TA);
+        if (t & 1) read_w(wcur, (t + 1) >> 1, (t + 1) >> 1 & 1);
+        __builtin_amdgcn_sched_barrier(0);
+        bf16x8_t a[2];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) a[c] = a_of(t, c);
+#pragma unroll
+        for (int i = 0; i < ta; ++i)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            if (t == 0) {
+              fold(sc[(j + 1) % 2], i, c);
+              part[i][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c], fx[0][i], f32x16_t{}, 0, 0, 0);
+            } else {
+              part[i][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c], fx[t & 1][i], part[i][c], 0, 0, 0);
+            }
+          }
+        if (t == 0) load_scales(s + 1, sc[(j + 1) % 2]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    bf16x8_t a[2];
+    if constexpr (ta > 0) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c) a[c] = a_of(7, c);
+    }
+    // This thread's part of step s + 1 has landed, and this wave has read all
+    // of step s: after the barrier both hold for the block.  What may still
+    // travel, all issued after s + 1's pieces: those of the S - 2 later steps
+    // (the scale loads among them only make the wait stricter).
+    __builtin_amdgcn_s_waitcnt(0x70 | (P * (S - 2)));   // vmcnt, lgkmcnt 0
+    bare_barrier();
+    bf16x8_t fl[TM];
+    if constexpr (ta > 0) {
+#pragma unroll
+      for (int i = 0; i < ta; ++i) fl[i] = fx[1][i];
+      read_x(xbufs[(j + 1) % S], 0, 0, TA);
+      read_w(wbufs[(j + 1) % S], 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    // the pieces that refill this step's buffers, some behind each MFMA
+    constexpr int kMma = 2 * ta, kPer = kMma ? (P + kMma - 1) / kMma : P;
+    const int k0 = kStep * block_of(s + S);
+#pragma unroll
+    for (int m = 0; m < (kMma ? kMma : 1); ++m) {
+      if constexpr (ta > 0)
+        part[m / 2][m % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m % 2], fl[m / 2], part[m / 2][m % 2], 0, 0, 0);
+#pragma unroll
+      for (int i = m * kPer; i < (m + 1) * kPer; ++i) {
+        if (i < XP) direct_x(k0, xcur, i);
+        else if (i < P) direct_w(k0, wcur, i - XP);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // D of the MFMA: lane l, register r: weight row 8 (r / 4) + 4 (l / 32) + r % 4, slot l % 32.
+  // The tile's rows of y are one buffer resource: rows behind the last slot are
+  // dropped by its bound, as are columns past N, by an offset outside.
+  auto write = [&](auto TA) __attribute__((always_inline)) {
+    constexpr int kSize = GATED ? 2 : 4, kCols = GATED ? 1 : 2;
+    const __amdgpu_buffer_rsrc_t ry =
+        rsrc_of(static_cast<char*>(y) + sh.first * vw.n * kSize, (uint64_t)sh.count * (uint64_t)vw.n * kSize);
+    const int N = (int)vw.n;
+    const bool whole = N % 4 == 0;
+#pragma unroll
+    for (int i = 0; i < decltype(TA)::value; ++i)
+#pragma unroll
+      for (int j = 0; j < kCols; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int n = (int)n0 + (GATED ? wn * 32 : wn * 64 + 32 * j) + 8 * q + 4 * half;
+          const uint32_t at = (uint32_t)((slot_of(i) + col) * N + n) * kSize;
+          float v[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            v[c] = acc[i][j][4 * q + c];
+            if constexpr (GATED) v[c] = silu(v[c]) * acc[i][1][4 * q + c];
+          }
+          if constexpr (GATED) {
+            const uint32_t lo = bf16_pair(v[0], v[1]), hi = bf16_pair(v[2], v[3]);
+            if (whole) {
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{lo, hi}, ry, (int)(n < N ? at : kOutside), 0, 0);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                __builtin_amdgcn_raw_buffer_store_b16((short)((c < 2 ? lo : hi) >> (16 * (c & 1))), ry,
+                                                      (int)(n + c < N ? at + 2 * c : kOutside), 0, 0);
+            }
+          } else if (whole) {
+            const u32x4_t o = {__builtin_bit_cast(unsigned int, v[0]), __builtin_bit_cast(unsigned int, v[1]),
+                               __builtin_bit_cast(unsigned int, v[2]), __builtin_bit_cast(unsigned int, v[3])};
+            __builtin_amdgcn_raw_buffer_store_b128(o, ry, (int)(n < N ? at : kOutside), 0, 0);
+          } else {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(unsigned int, v[c]), ry,
+                                                    (int)(n + c < N ? at + 4 * c : kOutside), 0, 0);
+          }
+        }
+  };
+  auto run = [&](auto TA) __attribute__((always_inline)) {
+    constexpr int ta = decltype(TA)::value;
+#pragma unroll
+    for (int i = 0; i < ta; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = part[i][j] = f32x16_t{};
+    if constexpr (ta > 0) {
+      read_x(x0, 0, 0, TA);
+      read_w(w0, 0, 0);
+    }
+    // whole rounds of buffers and register sets, then what is left; what the last
+    // steps fetch lies past K: zeros
+    constexpr int kRound = S == 2 ? 2 : 6;
+    auto steps_from = [&](int s, auto J, auto self) __attribute__((always_inline)) {
+      step(s, J, TA);
+      constexpr int j = decltype(J)::value + 1;
+      if constexpr (j < kRound) self(s + 1, std::integral_constant<int, j>{}, self);
+    };
+    auto rest_from = [&](int s, auto J, auto self) __attribute__((always_inline)) {
+      if (s >= steps) return;
+      step(s, J, TA);
+      constexpr int j = decltype(J)::value + 1;
+      if constexpr (j + 1 < kRound) self(s + 1, std::integral_constant<int, j>{}, self);
+    };
+    int s = 0;
+    for (; s + kRound <= steps; s += kRound) steps_from(s, std::integral_constant<int, 0>{}, steps_from);
+    rest_from(s, std::integral_constant<int, 0>{}, rest_from);
+    if constexpr (ta > 0) {
+      // the last step's sums: its scales are in the set of its parity
+      const bool odd = (steps & 1) == 0;
+      Scales last;
+      last.w[0] = odd ? sc[1].w[0] : sc[0].w[0];
+      last.w[1] = odd ? sc[1].w[1] : sc[0].w[1];
+#pragma unroll
+      for (int i = 0; i < ta; ++i) last.x[i] = odd ? sc[1].x[i] : sc[0].x[i];
+#pragma unroll
+      for (int i = 0; i < ta; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) fold(last, i, j);
+      write(TA);
+    }
+  };
+
+#pragma unroll
+  for (int b = 0; b < S; ++b) {
+    const int k0 = kStep * block_of(b);
+#pragma unroll
+    for (int i = 0; i < XP; ++i) direct_x(k0, xbufs[b], i);
+#pragma unroll
+    for (int i = 0; i < WP; ++i) direct_w(k0, wbufs[b], i);
+  }
+  // before the first step there are no sums to add
+  sc[1].w[0] = sc[1].w[1] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) sc[0].x[i] = sc[1].x[i] = 0.0f;
+  load_scales(0, sc[0]);
+  asm volatile("" : : "s"(y));   // its scalar load ends here: pending, it would make the loop's first LDS wait a full one
+  __builtin_amdgcn_s_waitcnt(0x70 | (P * (S - 1) < 16 ? P * (S - 1) : 15));   // step 0 has landed
+  bare_barrier();
+  // (a wave takes one of the loops as a whole; all pass the same barriers)
+  if (sh.count > (TM > 1 ? 64 + 32 * wm : 32 * wm)) {
+    run(std::integral_constant<int, TM>{});
+  } else if (TM > 1 && sh.count > 32 * wm) {
+    run(std::integral_constant<int, TM == 1 ? 1 : TM / 2>{});
+  } else {
+    run(std::integral_constant<int, 0>{});
+  }
+  __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more when the block gives it back
+}
+
+template <int BM, bool GATED, bool ACT8, bool BIG = false>
+hipError_t launch_one(const ExpertsCall& c, const float* act, bool spread, hipStream_t s) {
+  const int64_t out = GATED ? 128 : 256, ntiles = (c.w.n + out - 1) / out;
+  // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
+  const int64_t tiles = max_chunks(c.r.slots, c.w.count, BM, c.r.offsets != nullptr) * ntiles;
+  const int64_t grid = (tiles + 7) / 8 * 8;
+  if (!grid_fits(grid, kNT)) return hipErrorNotSupported;
+  hipLaunchKernelGGL((k_fp8_tile<BM, GATED, ACT8, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x,
+                     ActScales{act}, c.y, (int)ntiles, (int)spread);
+  return hipGetLastError();
+}
+
+template <bool GATED, bool ACT8>
+hipError_t launch_rows(const ExpertsCall& c, const float* act, int rows, bool spread, hipStream_t s) {
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_one<128, GATED, ACT8, true>(c, act, spread, s);
+  if (rows <= 64) return launch_one<64, GATED, ACT8>(c, act, spread, s);
+  return launch_one<128, GATED, ACT8>(c, act, spread, s);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_tile(const ExpertsCall& c, const float* act, int rows, bool spread, hipStream_t s) {
+  if (act) return launch_rows<false, true>(c, act, rows, spread, s);
+  return c.gated ? launch_rows<true, false>(c, nullptr, rows, spread, s)
+                 : launch_rows<false, false>(c, nullptr, rows, spread, s);
+}
+
+}  // namespace uw

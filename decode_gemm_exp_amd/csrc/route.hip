@@ -21,133 +21,13 @@
 // its pairs behind the counts of all blocks before it.  No atomics decide an
 // order: the rank of a pair among its wave's equals comes from ballots, the
 // waves' counts are added in wave order.
-#include "experts.h"
+#include "route.h"
 
 namespace uw {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kOneBlockPairs = 1024, kOneWavePairs = 64;
-
-// larger floats have larger keys; 0 = not selectable
-__device__ __forceinline__ uint32_t order_key(float v) {
-  v += 0.0f;   // -0 ties with 0
-  const uint32_t u = __builtin_bit_cast(uint32_t, v);
-  const uint32_t k = u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-  return (v != v || v == -__builtin_inff()) ? 0u : k;
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-
-// butterflies over the L lanes of a token: after each step a lane and its
-// partner agree
-template <int L, typename F>
-__device__ __forceinline__ void butterfly(F&& f) {
-  f([](uint32_t v) { return dpp<0xB1>(v); });    // quad: 1 0 3 2
-  f([](uint32_t v) { return dpp<0x4E>(v); });    // quad: 2 3 0 1
-  f([](uint32_t v) { return dpp<0x141>(v); });   // half row mirrored
-  f([](uint32_t v) { return dpp<0x140>(v); });   // row mirrored
-  if constexpr (L == 64) {
-    f([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 16); });
-    f([](uint32_t v) { return (uint32_t)__shfl_xor((int)v, 32); });
-  }
-}
-
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-  butterfly<L>([&](auto from) { v = fmaxf(v, __builtin_bit_cast(float, from(__builtin_bit_cast(uint32_t, v)))); });
-  return v;
-}
-
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-  butterfly<L>([&](auto from) { v += __builtin_bit_cast(float, from(__builtin_bit_cast(uint32_t, v))); });
-  return v;
-}
-
-// exp(v - top) with equals giving 1, infinities included
-__device__ __forceinline__ float exp_from(float v, float top) { return v == top ? 1.0f : expf(v - top); }
-
-__device__ __forceinline__ float logit_at(const RouteCall& c, int64_t at) {
-  return c.bf16 ? __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t*>(c.logits)[at] << 16)
-                : static_cast<const float*>(c.logits)[at];
-}
-
-// One token on L lanes (l: this lane's place): lane j < topk returns choice j
-// (-1: none) and its weight.  live: the token exists.
-template <int L, int NV>
-__device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live, int l, int& id, float& weight) {
-  float v[NV];
-  uint32_t key[NV];
-  // all loads first, absent keys' from the row's first place (a load under a
-  // condition waits for itself: twelve in a row took most of the kernel's time)
-  const int64_t row = (live ? t : 0) * c.ld;
-  if (c.bf16) {
-    uint16_t u[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) u[i] = static_cast<const uint16_t*>(c.logits)[row + (i * L + l < c.experts ? i * L + l : 0)];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = __builtin_bit_cast(float, (uint32_t)u[i] << 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = static_cast<const float*>(c.logits)[row + (i * L + l < c.experts ? i * L + l : 0)];
-  }
-  float bias[NV] = {};
-  if (c.bias) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) bias[i] = c.bias[i * L + l < c.experts ? i * L + l : 0];
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = live && i * L + l < c.experts;
-    key[i] = in ? order_key(v[i] + bias[i]) : 0u;
-  }
-  if (c.on_score) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool in = live && i * L + l < c.experts && order_key(v[i]);
-      key[i] = in ? order_key(1.0f / (1.0f + expf(-v[i])) + bias[i]) : 0u;
-    }
-  }
-  float top = -__builtin_inff(), sum = 0.0f;
-  if (c.scoring == 0) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) top = fmaxf(top, key[i] ? v[i] : -__builtin_inff());
-    top = group_max<L>(top);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) sum += key[i] ? exp_from(v[i], top) : 0.0f;
-  }
-  id = -1;
-  for (int j = 0; j < c.topk; ++j) {
-    uint32_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-    butterfly<L>([&](auto from) { best = max(best, from(best)); });
-    if (best == 0) best = 0xFFFFFFFFu;   // nothing left: no key equals this (a positive NaN's, and NaN has key 0)
-    // the lowest index that has it
-    uint32_t at = 0xFFFFFFFFu;
-#pragma unroll
-    for (int i = NV - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(i * L + l) : at;
-    uint32_t e = at;
-    butterfly<L>([&](auto from) { e = min(e, from(e)); });
-    id = l == j ? (int)e : id;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) key[i] = e == (uint32_t)(i * L + l) ? 0u : key[i];
-  }
-  float mine = -__builtin_inff();   // lane j: the logit of choice j
-  if (id >= 0) mine = logit_at(c, t * c.ld + id);
-  const bool chosen = id >= 0;
-  if (c.scoring == 2) mine = fminf(mine, 0.0f) - log1pf(expf(-__builtin_fabsf(mine)));   // log sigmoid
-  if (c.scoring != 0) {
-    top = group_max<L>(chosen ? mine : -__builtin_inff());
-    sum = chosen ? exp_from(mine, top) : 0.0f;
-  }
-  sum = group_sum<L>(sum);
-  weight = chosen ? exp_from(mine, top) / sum : 0.0f;
-}
 
 // The block's tokens [t0, t1): ids and weights to memory, and expert(pair)
 // for each of their pairs through `each` (pair counted from t0's first).
@@ -237,15 +117,6 @@ __device__ __forceinline__ int place_chunk(PlanLds& s, int experts, int e) {
   }
   __syncthreads();
   return slot;
-}
-
-// What the wave's lanes wrote to LDS before, its lanes read after.  LDS serves a
-// wave in order, so nothing is waited for, but the compiler has to keep the order: a
-// wave barrier alone holds back no memory access.
-__device__ __forceinline__ void wave_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Everything in one wave (tokens * topk <= 64).

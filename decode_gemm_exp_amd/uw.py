@@ -147,6 +147,11 @@ _SIGS = {
     "uw_dequantize_mx4": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp]),
     "uw_workspace_size_mx4": (ctypes.c_int, [_i64, _i64, _i64, ctypes.c_int, ctypes.POINTER(_sz)]),
     "uw_matmul_mx4": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, ctypes.c_int, _vp, _sz, _vp]),
+    "uw_quantize_fp8": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, _i64, ctypes.c_int32, _vp, _vp, _vp]),
+    "uw_dequantize_fp8": (ctypes.c_int, [_vp, _vp, _i64, _i64, ctypes.c_int32, _vp, _i64, _vp]),
+    "uw_workspace_size_fp8": (ctypes.c_int, [_i64, _i64, _i64, ctypes.c_int, ctypes.POINTER(_sz)]),
+    "uw_matmul_fp8": (ctypes.c_int, [_vp, _vp, _i64, _i64, _vp, _i64, _vp, ctypes.c_int, _vp, _sz, _vp]),
+    "uw_experts_fp8": (ctypes.c_int, [_vp, _vp, ctypes.c_int32, _i64, _i64, _i64, _i64, ctypes.POINTER(_vp)]),
     "uw_workspace_size_route": (ctypes.c_int, [_i64, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(_sz)]),
     "uw_route_experts": (ctypes.c_int, [_vp, ctypes.c_int, _i64, ctypes.c_int32, _i64, _vp, ctypes.c_int32,
                                         ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
@@ -160,6 +165,9 @@ _SIGS = {
     "uw_workspace_size_expert_mlp": (ctypes.c_int, [_vp, _vp, _i64, ctypes.c_int32, ctypes.POINTER(_sz)]),
     "uw_expert_mlp": (ctypes.c_int, [_vp, _vp, _vp, _i64, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
                                      _vp]),
+    "uw_workspace_size_expert_layer": (ctypes.c_int, [_vp, _vp, _i64, ctypes.c_int32, ctypes.POINTER(_sz)]),
+    "uw_expert_layer": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _vp, ctypes.c_int32, ctypes.c_int,
+                                       _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _f = getattr(_lib, _name)
@@ -554,7 +562,7 @@ class TorchAllocator:
 # The calls below check what a pointer cannot carry -- element type, shape,
 # contiguity, device -- and raise ValueError before the library sees them.
 
-ACT_BF16, ACT_MX4 = 0, 1
+ACT_BF16, ACT_MX4, ACT_FP8 = 0, 1, 2
 SCORE = {"softmax": 0, "softmax_topk": 1, "sigmoid": 2, "sigmoid_biased": 4}
 _TYPES = {torch.float32: 0, torch.bfloat16: 1}
 
@@ -658,6 +666,77 @@ def uw_matmul_mx4(elem: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: t
     _check(_lib.uw_matmul_mx4(pe, ps, n, k, px, batch, py, act, pw, nb, _stream(stream)), "uw_matmul_mx4")
 
 
+# ---- FP8 -----------------------------------------------------------------------
+
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)   # elements: as E4M3, or as bytes
+
+
+def fp8_scale_shape(rows: int, cols: int, block_rows: int = 1) -> tuple[int, int]:
+    """Shape of the scales of a [rows][cols] array in blocks of block_rows x 128."""
+    return (rows + block_rows - 1) // block_rows, (cols + 127) // 128
+
+
+def _want_fp8(t: torch.Tensor, what: str, shape, dev: int) -> int:
+    return _want(t, what, torch.uint8 if t.dtype is torch.uint8 else torch.float8_e4m3fn, shape, dev)
+
+
+def _block_rows(block_rows: int) -> None:
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows: 1 or 128 expected, got {block_rows}")
+
+
+def uw_quantize_fp8(src: torch.Tensor, elem: torch.Tensor, scale: torch.Tensor, block_rows: int = 1,
+                    stream=None) -> None:
+    """src [rows][cols] BF16 or FP32 (rows may be strided) -> elem [rows][cols] float8_e4m3fn (or uint8), scale
+    [fp8_scale_shape(rows, cols, block_rows)] FP32."""
+    if src.dtype not in _TYPES:
+        raise ValueError(f"src: float32 or bfloat16 expected, got {src.dtype}")
+    _block_rows(block_rows)
+    dev = _current()
+    ld = _rows2d(src, "src", dev)
+    rows, cols = src.shape
+    pe = _want_fp8(elem, "elem", (rows, cols), dev)
+    ps = _want(scale, "scale", torch.float32, fp8_scale_shape(rows, cols, block_rows), dev)
+    _check(_lib.uw_quantize_fp8(src.data_ptr(), _TYPES[src.dtype], rows, cols, ld, block_rows, pe, ps,
+                                _stream(stream)), "uw_quantize_fp8")
+
+
+def uw_dequantize_fp8(elem: torch.Tensor, scale: torch.Tensor, out: torch.Tensor, block_rows: int = 1,
+                      stream=None) -> None:
+    """The values of uw_quantize_fp8's arrays into out [rows][cols] BF16 (rows may be strided)."""
+    if out.dtype is not torch.bfloat16:
+        raise ValueError(f"out: bfloat16 expected, got {out.dtype}")
+    _block_rows(block_rows)
+    dev = _current()
+    ld = _rows2d(out, "out", dev)
+    rows, cols = out.shape
+    pe = _want_fp8(elem, "elem", (rows, cols), dev)
+    ps = _want(scale, "scale", torch.float32, fp8_scale_shape(rows, cols, block_rows), dev)
+    _check(_lib.uw_dequantize_fp8(pe, ps, rows, cols, block_rows, out.data_ptr(), ld, _stream(stream)),
+           "uw_dequantize_fp8")
+
+
+def uw_workspace_size_fp8(n: int, k: int, batch: int, act: int = ACT_BF16) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.uw_workspace_size_fp8(n, k, batch, act, ctypes.byref(b)), "uw_workspace_size_fp8")
+    return b.value
+
+
+def uw_matmul_fp8(elem: torch.Tensor, scale: torch.Tensor, x: torch.Tensor, y: torch.Tensor,
+                  ws: torch.Tensor | None = None, act: int = ACT_BF16, stream=None) -> None:
+    """y [batch][n] FP32 = x [batch][k] BF16 times the FP8 matrix (elem [n][k], scale [fp8_scale_shape(n, k, 128)])."""
+    if x.dim() != 2 or elem.dim() != 2:
+        raise ValueError("x and elem: two dimensions expected")
+    dev = _current()
+    (batch, k), n = x.shape, elem.shape[0]
+    pe = _want_fp8(elem, "elem", (n, k), dev)
+    ps = _want(scale, "scale", torch.float32, fp8_scale_shape(n, k, 128), dev)
+    px = _want(x, "x", torch.bfloat16, None, dev)
+    py = _want(y, "y", torch.float32, (batch, n), dev)
+    pw, nb = _ws(ws, dev)
+    _check(_lib.uw_matmul_fp8(pe, ps, n, k, px, batch, py, act, pw, nb, _stream(stream)), "uw_matmul_fp8")
+
+
 # ---- mixture of experts ------------------------------------------------------
 
 class Routing:
@@ -694,6 +773,20 @@ class Routing:
             raise ValueError(f"routing: must be on the current device, is on {self._t[2].device}")
 
 
+def _router(logits: torch.Tensor, bias: torch.Tensor | None, scoring: str, tokens: int, experts: int, dev: int):
+    """Type, scoring, row stride and bias pointer of a router's scores."""
+    kind = _TYPES.get(logits.dtype)
+    if kind is None:
+        raise ValueError(f"logits: float32 or bfloat16 expected, got {logits.dtype}")
+    score = SCORE.get(scoring)
+    if score is None:
+        raise ValueError(f"scoring: one of {sorted(SCORE)} expected, got {scoring!r}")
+    ld = _rows2d(logits, "logits", dev)
+    if logits.shape != (tokens, experts):
+        raise ValueError(f"logits: shape {(tokens, experts)} expected, got {tuple(logits.shape)}")
+    return kind, score, ld, _want(bias, "bias", torch.float32, (experts,), dev) if bias is not None else None
+
+
 def uw_route_experts(logits: torch.Tensor, routing: Routing, scoring: str = "softmax_topk",
                      bias: torch.Tensor | None = None, stream=None) -> None:
     """logits [tokens][experts] FP32 or BF16 (rows may be strided) -> routing's ids, weights and plan.
@@ -702,17 +795,8 @@ def uw_route_experts(logits: torch.Tensor, routing: Routing, scoring: str = "sof
     weights are without it.
     """
     tokens, experts, topk = routing._shape
-    kind = _TYPES.get(logits.dtype)
-    if kind is None:
-        raise ValueError(f"logits: float32 or bfloat16 expected, got {logits.dtype}")
-    score = SCORE.get(scoring)
-    if score is None:
-        raise ValueError(f"scoring: one of {sorted(SCORE)} expected, got {scoring!r}")
     dev = _current()
-    ld = _rows2d(logits, "logits", dev)
-    if logits.shape != (tokens, experts):
-        raise ValueError(f"logits: shape {(tokens, experts)} expected, got {tuple(logits.shape)}")
-    pb = _want(bias, "bias", torch.float32, (experts,), dev) if bias is not None else None
+    kind, score, ld, pb = _router(logits, bias, scoring, tokens, experts, dev)
     routing._check_device(dev)
     _check(_lib.uw_route_experts(logits.data_ptr(), kind, tokens, experts, ld, pb, topk, score, *routing._ptrs,
                                  *routing._ws_args, _stream(stream)), "uw_route_experts")
@@ -820,6 +904,31 @@ def uw_experts_mx4(elem: torch.Tensor, scale: torch.Tensor, count: int, n: int, 
     return Experts(h.value, count, n, k, (elem, scale))
 
 
+def uw_experts_fp8(elem: torch.Tensor, scale: torch.Tensor, count: int, n: int, k: int, elem_stride: int = 0,
+                   scale_stride: int = 0) -> Experts:
+    """elem: float8_e4m3fn (or uint8), expert e's [n][k] at element e * elem_stride; scale: FP32, expert e's
+    [fp8_scale_shape(n, k, 128)] at element e * scale_stride (0: contiguous); views as for uw_experts_bf16."""
+    if elem.dtype not in _E4M3:
+        raise ValueError(f"elem: {_E4M3[0]} or {_E4M3[1]} expected, got {elem.dtype}")
+    if scale.dtype is not torch.float32:
+        raise ValueError(f"scale: {torch.float32} expected, got {scale.dtype}")
+    for t, what in ((elem, "elem"), (scale, "scale")):
+        _on_device(t, what, _current())
+    h = ctypes.c_void_p()
+    _check(_lib.uw_experts_fp8(elem.data_ptr(), scale.data_ptr(), count, n, k, elem_stride, scale_stride,
+                               ctypes.byref(h)), "uw_experts_fp8")
+    sr, sc = fp8_scale_shape(n, k, 128)
+    try:
+        _stack(elem, "elem", count, n, k, elem_stride)
+        _stack(scale, "scale", count, sr, sc, scale_stride)
+        _holds(elem, (elem_stride or n * k) * (count - 1) + n * k, "elem")
+        _holds(scale, 4 * ((scale_stride or sr * sc) * (count - 1) + sr * sc), "scale")
+    except ValueError:
+        _lib.uw_free_experts(h)
+        raise
+    return Experts(h.value, count, n, k, (elem, scale))
+
+
 def uw_experts_uwf1(ms, stream=None) -> Experts:
     """ms: compressed matrices of one shape with resident palette indices, one per expert."""
     arr = (ctypes.c_void_p * len(ms))(*[m.handle.value for m in ms])
@@ -878,3 +987,26 @@ def uw_expert_mlp(gate: Experts, up: Experts, down: Experts, routing: Routing, x
     _, weights, offsets, rows, slots = routing._ptrs
     _check(_lib.uw_expert_mlp(gate.handle, up.handle, down.handle, tokens, topk, offsets, rows, slots, weights, px, po,
                               *_ws(ws, dev), _stream(stream)), "uw_expert_mlp")
+
+
+def uw_workspace_size_expert_layer(gate: Experts, down: Experts, tokens: int, topk: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_lib.uw_workspace_size_expert_layer(gate.handle, down.handle, tokens, topk, ctypes.byref(b)),
+           "uw_workspace_size_expert_layer")
+    return b.value
+
+
+def uw_expert_layer(gate: Experts, up: Experts, down: Experts, logits: torch.Tensor, routing: Routing, x: torch.Tensor,
+                    out: torch.Tensor, ws: torch.Tensor, scoring: str = "softmax_topk",
+                    bias: torch.Tensor | None = None, stream=None) -> None:
+    """uw_route_experts into routing and uw_expert_mlp on it: out [tokens][k] BF16, logits [tokens][experts]."""
+    tokens, experts, topk = routing._shape
+    if experts != gate.count:
+        raise ValueError(f"routing: {gate.count} experts expected, got {experts}")
+    dev = _current()
+    kind, score, ld, pb = _router(logits, bias, scoring, tokens, experts, dev)
+    px = _want(x, "x", torch.bfloat16, (tokens, gate.k), dev)
+    po = _want(out, "out", torch.bfloat16, (tokens, gate.k), dev)
+    routing._check_device(dev)
+    _check(_lib.uw_expert_layer(gate.handle, up.handle, down.handle, logits.data_ptr(), kind, tokens, ld, pb, topk, score,
+                                *routing._ptrs, px, po, *_ws(ws, dev), _stream(stream)), "uw_expert_layer")

@@ -532,11 +532,50 @@ uw_status uw_dequantize_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, i
  * UW_ACT_MX4 up to 8 rows; beyond, UW_ACT_MX4 multiplies it as it is.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
  * 16-byte aligned.  The workspace (uw_workspace_size_mx4 bytes, 16-byte
  * aligned) serves one call at a time. */
-typedef enum { UW_ACT_BF16 = 0, UW_ACT_MX4 = 1 } uw_activation;
+typedef enum { UW_ACT_BF16 = 0, UW_ACT_MX4 = 1, UW_ACT_FP8 = 2 /* uw_matmul_fp8 */ } uw_activation;
 uw_status uw_workspace_size_mx4(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes);
 uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64_t n, int64_t k,
                         const uint16_t* x_dev, int64_t batch, float* y_dev, uw_activation act, void* ws_dev,
                         size_t ws_bytes, void* stream);
+
+/* ---- FP8 weights and activations ----------------------------------------------
+ * OCP OFP8 E4M3 elements (largest value 448, bytes 0x7F and 0xFF are NaN), one FP32
+ * scale per block of 128 columns and `block_rows` rows: 1 as activations have them,
+ * 128 as a weight matrix has them.  Blocks at the right and lower edge are cut off.
+ * Elements are [rows][cols] bytes, scales [ceil(rows / block_rows)][ceil(cols / 128)]
+ * floats; an element stands for its E4M3 value times its block's scale.  cols must
+ * be a multiple of 32; rows and cols are at most 2^20 (UW_ERR_UNSUPPORTED).
+ * (saidapartage.blog, section "Un complément, pas un remplaçant": quantised weights
+ * are the other half of what is served; uw_compress_fp8 stores the same elements
+ * without loss, these calls make them and multiply with them.) */
+
+/* Convert a [rows][cols] array whose rows start `ld` elements apart (ld >= cols, a
+ * multiple of 8).  m being a block's largest magnitude, at least 2^-110, its scale is
+ * m / 448 and its elements are v * (448 / m) rounded to nearest, ties to even; both
+ * quotients and the product are FP32 numbers, each rounded to nearest.  A block with
+ * an infinity or a NaN gets scale NaN and zero elements.  block_rows: 1 or 128
+ * (UW_ERR_INVALID).  src_dev, elem_dev 16-byte, scale_dev 4-byte aligned. */
+uw_status uw_quantize_fp8(const void* src_dev, uw_type src_type, int64_t rows, int64_t cols, int64_t ld,
+                          int32_t block_rows, uint8_t* elem_dev, float* scale_dev, void* stream);
+
+/* The values the elements stand for, as BF16, rows `ld` apart (>= cols, a multiple of
+ * 8); what lies between rows is left as it was.  The product of element and scale is
+ * rounded to FP32, then to BF16. */
+uw_status uw_dequantize_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t rows, int64_t cols,
+                            int32_t block_rows, uint16_t* out_dev, int64_t ld, void* stream);
+
+/* y[b][n] = sum_k x[b][k] W[n][k] for b < batch, W in E4M3 ([n][k]) with scales per 128 x
+ * 128 block ([ceil(n / 128)][ceil(k / 128)]).  act: UW_ACT_BF16 takes x as it is,
+ * UW_ACT_FP8 its elements and scales per 1 x 128 (uw_quantize_fp8's, made inside the
+ * call).  Elements are multiplied and added up over a block of 128 k in FP32; the
+ * block's sum is multiplied by its scales (with UW_ACT_FP8 their product in FP32) and
+ * added to y's, in FP32, rounded once where it is a fused multiply-add.  Results
+ * repeat bit for bit.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
+ * 16-byte aligned.  The workspace (uw_workspace_size_fp8 bytes, 16-byte aligned, may
+ * be 0) serves one call at a time. */
+uw_status uw_workspace_size_fp8(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes);
+uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t n, int64_t k, const uint16_t* x_dev,
+                        int64_t batch, float* y_dev, uw_activation act, void* ws_dev, size_t ws_bytes, void* stream);
 
 /* ---- mixture of experts --------------------------------------------------------
  * The MLP of a mixture-of-experts layer: a router picks topk of the experts for
@@ -588,7 +627,7 @@ uw_status uw_plan_experts(const int32_t* ids_dev, int64_t tokens, int32_t expert
                           void* stream);
 
 /* The experts' weights of one projection, W_e[n][k] for e < count, in one of
- * three forms.  The set keeps the pointers; the weights stay the caller's and
+ * four forms.  The set keeps the pointers; the weights stay the caller's and
  * must outlive it.  k must be a multiple of 32, n and k at most 2^20, count
  * <= 1024 (UW_ERR_UNSUPPORTED).
  *   uw_experts_bf16   BF16, expert e at w_dev + e * stride elements (0: n * k;
@@ -596,6 +635,10 @@ uw_status uw_plan_experts(const int32_t* ids_dev, int64_t tokens, int32_t expert
  *   uw_experts_mx4    MXFP4, expert e's elements and scales e * their stride
  *                     in bytes on (0: contiguous; multiples of 16 and 4); a
  *                     weight whose value overflows BF16 counts as infinite
+ *   uw_experts_fp8    E4M3 with scales per 128 x 128 block of each expert's matrix,
+ *                     expert e's elements e * elem_stride bytes (0: n * k; a
+ *                     multiple of 16) and its scales e * scale_stride floats (0:
+ *                     contiguous) on; summed and scaled as by uw_matmul_fp8
  *   uw_experts_uwf1   `count` compressed matrices of one shape, stored [N][K]
  *                     (UW_ERR_UNSUPPORTED otherwise), with resident palette
  *                     indices (uw_transcode_palette(m, NULL);
@@ -608,6 +651,8 @@ typedef struct uw_experts uw_experts;
 uw_status uw_experts_bf16(const uint16_t* w_dev, int32_t count, int64_t n, int64_t k, int64_t stride,
                           uw_experts** out);
 uw_status uw_experts_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int32_t count, int64_t n, int64_t k,
+                         int64_t elem_stride, int64_t scale_stride, uw_experts** out);
+uw_status uw_experts_fp8(const uint8_t* elem_dev, const float* scale_dev, int32_t count, int64_t n, int64_t k,
                          int64_t elem_stride, int64_t scale_stride, uw_experts** out);
 uw_status uw_experts_uwf1(const uw_matrix* const* ms, int32_t count, void* stream, uw_experts** out);
 void uw_free_experts(uw_experts* w);
@@ -643,6 +688,24 @@ uw_status uw_expert_mlp(const uw_experts* gate, const uw_experts* up, const uw_e
                         int32_t topk, const int32_t* offsets_dev, const int32_t* rows_dev, const int32_t* slots_dev,
                         const float* weights_dev, const uint16_t* x_dev, uint16_t* out_dev, void* ws_dev,
                         size_t ws_bytes, void* stream);
+
+/* A whole layer from the router's scores: uw_route_experts' choice and plan, written as
+ * that call writes them, and uw_expert_mlp's result on them.  Up to
+ * UW_LAYER_TOKENS tokens it is two kernels, the first of which routes, and out[t]'s
+ * sum over its experts is in FP32 in an order that depends on the call's shapes and on
+ * which experts the tokens chose, not in that of j; beyond, it is what the two calls
+ * do.  Results repeat bit for bit.  Arguments as of those calls; ids_dev and weights_dev
+ * are [tokens][topk], experts is gate's count.  Without tokens only the offsets are
+ * written.  The workspace (uw_workspace_size_expert_layer bytes, 16-byte aligned)
+ * serves one call at a time. */
+#define UW_LAYER_TOKENS 16
+uw_status uw_workspace_size_expert_layer(const uw_experts* gate, const uw_experts* down, int64_t tokens, int32_t topk,
+                                         size_t* bytes);
+uw_status uw_expert_layer(const uw_experts* gate, const uw_experts* up, const uw_experts* down, const void* logits_dev,
+                          uw_type type, int64_t tokens, int64_t ld, const float* bias_dev, int32_t topk,
+                          uw_scoring scoring, int32_t* ids_dev, float* weights_dev, int32_t* offsets_dev,
+                          int32_t* rows_dev, int32_t* slots_dev, const uint16_t* x_dev, uint16_t* out_dev, void* ws_dev,
+                          size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
