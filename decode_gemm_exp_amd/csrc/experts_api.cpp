@@ -281,10 +281,8 @@ uw_status uw_workspace_size_fp8(int64_t n, int64_t k, int64_t batch, uw_activati
   if (st != UW_OK) return st;
   // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
   if (batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512)) return UW_ERR_UNSUPPORTED;
-  const uint64_t b = (uint64_t)batch;
-  *bytes = act != UW_ACT_FP8 || batch <= kFp8RowsMax
-               ? 0
-               : pad256(2 * b * (uint64_t)k) + pad256(4 * b * (uint64_t)fp8_blocks(k));
+  const Fp8Plan p = plan_fp8(n, k, batch, act == UW_ACT_FP8);
+  *bytes = p.x_bytes + p.scale_bytes + p.part_bytes;
   return UW_OK;
 }
 
@@ -311,12 +309,7 @@ uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t
   c.r = RaggedRows{nullptr, nullptr, batch, batch};
   c.x = x_dev;
   c.y = y_dev;
-  if (act == UW_ACT_FP8) {
-    uint8_t* xe = static_cast<uint8_t*>(ws_dev);
-    return status_of(launch_fp8_act(c, reinterpret_cast<uint16_t*>(xe),
-                                    reinterpret_cast<float*>(xe + pad256(2 * (uint64_t)batch * (uint64_t)k)), s));
-  }
-  return status_of(launch_experts(c, s));
+  return status_of(launch_fp8_product(c, act == UW_ACT_FP8, ws_dev, s));
 }
 
 uw_status uw_experts_fp8(const uint8_t* elem_dev, const float* scale_dev, int32_t count, int64_t n, int64_t k,

@@ -398,7 +398,7 @@ hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s) {
 //   MXFP4 14336x4096: 64 rows 25 / 52 / 59, 128 rows 45 / 55 / 60, 256 rows 74 / 58 / 61
 //   MXFP4, few tiles: 5001x8224, 200 rows 58 / 109 / 125; 4096x4096, 256 rows 25 / 52 / 63
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s) {
-  if (c.w.form == kFormFp8) return launch_fp8(c, s);
+  if (c.w.form == kFormFp8) return launch_fp8_experts(c, s);
   const int64_t e = c.r.offsets ? c.w.count : 1;
   const int64_t avg = (c.r.slots + e - 1) / e;
   if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_experts_tile(c, 256, false, s);   // x past 2 GiB: by pointers

@@ -77,13 +77,26 @@ hipError_t launch_dequantize_fp8(const uint8_t* elem, const float* scale, int64_
 // rows of x -> their elements per 1 x 128 as BF16 numbers, unscaled, and scales
 hipError_t launch_round_fp8(const uint16_t* x, int64_t rows, int64_t cols, uint16_t* out, float* scale, hipStream_t s);
 
-// products with an FP8 matrix (see ExpertsView): few rows, or tiles; act: NULL, or the scales of the E4M3 values that c.x holds as BF16
-hipError_t launch_fp8_tile(const ExpertsCall& c, const float* act, int rows, bool spread, hipStream_t s);
-// rows of x in BF16, or converted on the way
-// (a call on more rows than this converts x into memory first: elements and scales)
-constexpr int64_t kFp8RowsMax = 32;
-hipError_t launch_fp8_act(const ExpertsCall& c, uint16_t* xe, float* xs, hipStream_t s);
-hipError_t launch_fp8(const ExpertsCall& c, hipStream_t s);
+// Products with E4M3 weights.  How the tiles run one:
+struct Fp8Tile {
+  int rows;           // of a tile: 64 or 128
+  bool spread;
+  int splits;         // slices of K, summed by a second kernel (one matrix, plain)
+  float* part;        // [splits][slots][n], when there are several
+  const float* act;   // x's scales when c.x holds E4M3 values as BF16
+};
+hipError_t launch_fp8_tile(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s);
 hipError_t launch_fp8_rows(const ExpertsCall& c, bool act8, hipStream_t s);
+// experts' rows
+hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s);
+
+// One matrix: which kernel serves it, and the workspace that takes.
+struct Fp8Plan {
+  bool few;           // launch_fp8_rows
+  Fp8Tile tile;       // (pointers not set)
+  uint64_t x_bytes, scale_bytes, part_bytes;
+};
+Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8);
+hipError_t launch_fp8_product(const ExpertsCall& c, bool act8, void* ws, hipStream_t s);
 
 }  // namespace uw

@@ -20,13 +20,15 @@
 namespace uw {
 namespace {
 
-template <int Q, bool GATED, bool ACT8, int NW, typename RR>
+template <int R, int Q, bool GATED, bool ACT8, bool XL, int NW, typename RR>
 __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, ExpertsView vu, RR rr,
                                                          const uint16_t* __restrict__ x, void* __restrict__ y,
                                                          int ntiles, int chunks) {
-  constexpr int R = 4, RT = GATED ? 2 : 4, kRows = 16 * RT;
-  constexpr int kW = 64 * 128;   // a wave's weights of a window
+  constexpr int RT = GATED ? R / 2 : R, kRows = 16 * RT;
+  constexpr int kW = 16 * R * 128;   // a wave's weights of a window
+  constexpr int kX = XL ? 16 * 256 : 4;
   __shared__ __attribute__((aligned(128))) char w0[NW * kW], w1[NW * kW];
+  __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
   __shared__ typename Finder<RR>::Lds found;
   unsigned tile;
   Share sh;
@@ -48,9 +50,10 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
 
   // x rows of this lane's slots
   const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
-  uint32_t xrow[Q];
-  int32_t row[Q];
-  auto slot = [&](int q) __attribute__((always_inline)) { return 16 * q + i16; };
+  constexpr int XR = XL ? 4 : Q;
+  uint32_t xrow[XR];
+  int32_t row[XR];
+  auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 4 * q + g : 16 * q + i16; };
   Finder<RR>::rows(rr, found, sh, row, slot);
 
   f32x4_t acc[R][Q];
@@ -59,16 +62,16 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
 #pragma unroll
     for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // Load i of eight takes rows 8 i .. 8 i + 7, eight lanes a row; of the 64 rows
+  // Load i takes rows 8 i .. 8 i + 7, eight lanes a row; of the 16 R rows
   // the gated form has W's first, then U's.
   const int pr = lane >> 3;
   auto load_w = [&](int j, char* wbuf) __attribute__((always_inline)) {
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
     const int k0 = 128 * j;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool u = GATED && i >= 4;
-      const int r = 8 * (u ? i - 4 : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
+    for (int i = 0; i < 2 * R; ++i) {
+      const bool u = GATED && i >= R;
+      const int r = 8 * (u ? i - R : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
       const uint32_t off = k0 + 16 * piece < K ? (uint32_t)(r * K + (k0 + 16 * piece)) : kOutside;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(u ? uw : ww, (lds_char*)(wbuf + wave * kW + 1024 * i), 16, (int)off, 0,
                                                0, 0);
@@ -78,20 +81,34 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
     uint4 xv[Q][4];
     float s[2];   // the blocks' scales, 0 past the last window
   };
-  auto load_x = [&](int j, Win& w) __attribute__((always_inline)) {
+  auto load_x = [&](int j, char* xbuf, Win& w) __attribute__((always_inline)) {
     const int k0 = 128 * j;
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
+    if constexpr (XL) {   // rows 4 i .. 4 i + 3, sixteen lanes a row; piece p of row r at 16 (p ^ r)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int k = k0 + 32 * g + 8 * i;
-        w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+        const int k = k0 + 8 * (i16 ^ (4 * i + g));
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char*)(xbuf + wave * kX + 1024 * i), 16,
+                                                 (int)(k < K ? xrow[i] + 2u * (uint32_t)k : kOutside), 0, 0, 0);
       }
+    } else {
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + 32 * g + 8 * i;
+          w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+        }
+    }
     const int at = j < nwin ? 4 * j : (int)kOutside;
     w.s[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ws, at, 0, 0));
     w.s[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(us, at, 0, 0)) : w.s[0];
   };
-  auto compute = [&](const char* wbuf, const Win& w) __attribute__((always_inline)) {
+  auto compute = [&](const char* wbuf, const char* xbuf, Win& w) __attribute__((always_inline)) {
+    if constexpr (XL) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w.xv[0][i] = *reinterpret_cast<const uint4*>(xbuf + wave * kX + i16 * 256 + (((4 * g + i) ^ i16) << 4));
+    }
     uint4 d[R][2];
 #pragma unroll
     for (int t = 0; t < R; ++t) {
@@ -152,18 +169,18 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
   Win wa, wb;
   load_w(wave, w0);   // on its way while the row indices arrive
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
+  for (int q = 0; q < XR; ++q) {
     const bool in = (slot(q) < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
     xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
   }
-  load_x(wave, wa);
+  load_x(wave, x0, wa);
   for (int j = wave; j < nwin; j += 2 * NW) {
     load_w(j + NW, w1);
-    load_x(j + NW, wb);
-    compute(w0, wa);
+    load_x(j + NW, x1, wb);
+    compute(w0, x0, wa);
     load_w(j + 2 * NW, w0);
-    load_x(j + 2 * NW, wa);
-    compute(w1, wb);
+    load_x(j + 2 * NW, x0, wa);
+    compute(w1, x1, wb);
   }
 
   __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
@@ -178,24 +195,42 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
   finish<R, Q, GATED, NW>(red, sh, n0, N, y);
 }
 
-template <int Q, bool GATED, bool ACT8>
+template <int R, int Q, bool GATED, bool ACT8, bool XL, int NW>
 hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
-  const int64_t rows = GATED ? 32 : 64, ntiles = (c.w.n + rows - 1) / rows;
+  const int64_t rows = GATED ? 8 * R : 16 * R, ntiles = (c.w.n + rows - 1) / rows;
   const int64_t chunks = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr);
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
-  if (!grid_fits(grid, 256)) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_experts_fp8<Q, GATED, ACT8, 4, RaggedRows>), dim3((unsigned)grid), dim3(256), 0, s, c.w, c.u,
-                     c.r, c.x, c.y, (int)ntiles, (int)chunks);
+  if (!grid_fits(grid, 64 * NW)) return hipErrorNotSupported;
+  hipLaunchKernelGGL((k_experts_fp8<R, Q, GATED, ACT8, XL, NW, RaggedRows>), dim3((unsigned)grid), dim3(64 * NW), 0, s,
+                     c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
   return hipGetLastError();
 }
+// One matrix: 64 rows of it a wave, or 32 and eight waves a block where that makes too
+// few blocks; x through LDS, like the weights, once its loads are many, or two groups of
+// sixteen rows where the blocks still fill the chip.  Measured (us; 64 rows, 64 with x in LDS, 32
+// with eight waves, the same with x in LDS, two groups; x in BF16):
+//   14336x4096   1 row 14.4 / 15.6 / 14.2 / 15.8, 16 rows 15.3 / 16.0 / 17.5 / 17.5, 32 rows 21.5 / 22.2 / 26.8 / 26.7 / 19.2
+//   5001x8224    1 row 21.7 / 24.1 / 15.0 / 15.6, 16 rows 28.2 / 25.4 / 18.9 / 17.9, 32 rows 26.6 / 24.1 / 29.5 / 27.3 / 39.8
+//   4096x4096    1 row  7.9 /  8.6 /  5.8 /  6.1, 16 rows  9.2 /  8.9 /  8.2 /  6.7, 32 rows  9.3 /  8.7 /  8.4 /  7.0 / 13.0
+//   28672x8192  16 rows 47.8 / 47.2 / 55.5 / 52.9, in 8 bits 51.3 / 45.9 / 67.1 / 57.3
+template <bool ACT8>
+hipError_t launch_matrix(const ExpertsCall& c, hipStream_t s) {
+  const int64_t cus = device_cus(), rows = c.r.slots, tiles = (c.w.n + 63) / 64;
+  if (rows > 16 && tiles * ((rows + 31) / 32) >= cus) return launch_one<4, 2, false, ACT8, false, 4>(c, s);
+  const int64_t blocks = tiles * ((rows + 15) / 16);
+  if (blocks >= cus * 3 / 4)
+    return rows > (ACT8 ? 8 : 15) ? launch_one<4, 1, false, ACT8, true, 4>(c, s)
+                                  : launch_one<4, 1, false, ACT8, false, 4>(c, s);
+  return rows > 8 ? launch_one<2, 1, false, ACT8, true, 8>(c, s) : launch_one<2, 1, false, ACT8, false, 8>(c, s);
+}
 
-template <bool GATED, bool ACT8>
-hipError_t launch_q(const ExpertsCall& c, hipStream_t s) {
-  const int64_t e = c.r.offsets ? c.w.count : 1, avg = (c.r.slots + e - 1) / e;
-  const int64_t rows = GATED ? 32 : 64;
-  const int64_t blocks = (c.w.n + rows - 1) / rows * max_chunks(c.r.slots, c.w.count, 32, c.r.offsets != nullptr);
-  if (avg <= (c.r.offsets ? 12 : 16) || blocks < device_cus()) return launch_one<1, GATED, ACT8>(c, s);
-  return launch_one<2, GATED, ACT8>(c, s);
+// Grouped by expert: two groups of sixteen slots where experts have more as a rule.
+template <bool GATED>
+hipError_t launch_grouped(const ExpertsCall& c, hipStream_t s) {
+  const int64_t avg = (c.r.slots + c.w.count - 1) / c.w.count, rows = GATED ? 32 : 64;
+  const int64_t blocks = (c.w.n + rows - 1) / rows * max_chunks(c.r.slots, c.w.count, 32, true);
+  if (avg <= 12 || blocks < device_cus()) return launch_one<4, 1, GATED, false, false, 4>(c, s);
+  return launch_one<4, 2, GATED, false, false, 4>(c, s);
 }
 
 }  // namespace
@@ -204,33 +239,106 @@ hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipS
   const int64_t ntiles = (c.w.n + 31) / 32, grid = routed_grid(r, ntiles);
   if (!grid_fits(grid, 256)) return hipErrorNotSupported;
   return with_routed(r, [&](auto rr) {
-    hipLaunchKernelGGL((k_experts_fp8<1, true, false, 4, decltype(rr)>), dim3((unsigned)grid), dim3(256), 0, s, c.w,
+    hipLaunchKernelGGL((k_experts_fp8<4, 1, true, false, false, 4, decltype(rr)>), dim3((unsigned)grid), dim3(256), 0, s, c.w,
                        c.u, rr, c.x, c.y, (int)ntiles, 0);
     return hipGetLastError();
   });
 }
 
 hipError_t launch_fp8_rows(const ExpertsCall& c, bool act8, hipStream_t s) {
-  if (act8) return launch_q<false, true>(c, s);
-  return c.gated ? launch_q<true, false>(c, s) : launch_q<false, false>(c, s);
+  if (!c.r.offsets) return act8 ? launch_matrix<true>(c, s) : launch_matrix<false>(c, s);
+  return c.gated ? launch_grouped<true>(c, s) : launch_grouped<false>(c, s);
 }
 
-// Which kernel, by the rows an expert has on average if every slot is used.
-hipError_t launch_fp8(const ExpertsCall& c, hipStream_t s) {
-  const int64_t e = c.r.offsets ? c.w.count : 1, avg = (c.r.slots + e - 1) / e;
-  const bool big = c.r.x_rows * 2 * c.w.k > kOutside;   // x past 2 GiB: by pointers
+namespace {
+
+// Estimates in us, fitted to measured times (some 650 of one matrix, 1 to 1024 rows, 300 x 9600 to
+// 28672 x 8192, the tiles' within 16 % rms; 350 of 8 to 64 experts, 4 to 256 rows each):
+//   tiles  rounds of one block a CU, each its steps of 128 k and three more, at 1.15 (64 rows) or
+//          1.55 (128 rows);
+//   rows   3 and the weights once per group of rows.
+double tile_us(int64_t blocks, int64_t steps, int rows) {
+  const int64_t cus = device_cus();
+  return (double)((blocks + cus - 1) / cus * (steps + 3)) * (rows == 64 ? 1.15 : 1.55);
+}
+
+}  // namespace
+
+// Grouped by expert.  The chunks of rows that the plan will make are not known here: one an
+// expert at least, and half a chunk an expert more than whole ones.  Weights pass the rows kernel
+// at 5 TB/s, in groups of 16 rows or, with more than 12 an expert, 32, and the tiles at 4.7 TB/s at
+// most.  (us, measured rows / 64 / 128: 32 experts 2048x2048 of 4 rows 31 / 29 / 31, of 32 rows 43 / 31 / 32, of
+// 64 rows 65 / 50 / 37; 8 of 2048x4096, 64 rows 32 / 38 / 46, 256 rows - / 81 / 59.)
+hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
+  const int64_t e = c.w.count, slots = c.r.slots, avg = (slots + e - 1) / e, with_rows = slots < e ? slots : e;
+  const int64_t ntiles = (c.w.n + (c.gated ? 127 : 255)) / (c.gated ? 128 : 256);
+  auto chunks = [&](int64_t rows) {
+    const int64_t n = slots / rows + with_rows / 2;
+    return n > with_rows ? n : with_rows;
+  };
   const bool spread = avg <= 96;
-  if (avg <= 32 && !big) return launch_fp8_rows(c, false, s);
-  return launch_fp8_tile(c, nullptr, avg <= 64 ? 64 : 128, spread, s);
+  // x past 2 GiB goes by pointers, in 128-row tiles
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_fp8_tile(c, Fp8Tile{128, spread, 1, nullptr, nullptr}, s);
+  const double weights = (c.gated ? 2.0 : 1.0) * (double)c.w.n * (double)c.w.k * 1e-6;
+  const int64_t steps = fp8_blocks(c.w.k);
+  const double t64 = tile_us(ntiles * chunks(64), steps, 64), t128 = tile_us(ntiles * chunks(128), steps, 128);
+  const double least = (double)with_rows * weights / 4.7, best = t64 < t128 ? t64 : t128;
+  if (3 + (double)chunks(avg > 12 ? 32 : 16) * weights / 5 < (best > least ? best : least))
+    return launch_fp8_rows(c, false, s);
+  return launch_fp8_tile(c, Fp8Tile{t64 < t128 ? 64 : 128, spread, 1, nullptr, nullptr}, s);
 }
 
-hipError_t launch_fp8_act(const ExpertsCall& c, uint16_t* xe, float* xs, hipStream_t s) {
-  if (c.r.slots <= kFp8RowsMax) return launch_fp8_rows(c, true, s);
-  const hipError_t e = launch_round_fp8(c.x, c.r.slots, c.w.k, xe, xs, s);
-  if (e != hipSuccess) return e;
-  ExpertsCall t = c;
-  t.x = xe;
-  return launch_fp8_tile(t, xs, c.r.slots <= 64 ? 64 : 128, c.r.slots <= 96, s);
+// One matrix.  The weights pass the tiles at 2.5 TB/s at most; K in slices costs 6.5 and the slices'
+// sums at 5.3 TB/s; the rows kernel takes the weights once per 16 rows at 7 TB/s, or per 32 at 6.2
+// where that fills the chip.
+Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
+  auto pad = [](uint64_t b) { return (b + 255) / 256 * 256; };
+  Fp8Plan p{};
+  const bool big = batch * 2 * k > kOutside;
+  const int64_t cus = device_cus(), steps = fp8_blocks(k);
+  const double weights = (double)n * (double)k * 1e-6;
+  double best = 0;
+  for (int rows = big ? 128 : 64; rows <= 128; rows *= 2)
+    for (int splits = 1; splits <= 16 && (splits == 1 || steps >= 2 * splits); ++splits) {
+      const int64_t blocks = (batch + rows - 1) / rows * ((n + 255) / 256) * splits;
+      double us = tile_us(blocks, (steps + splits - 1) / splits, rows);
+      if (us < weights / 2.5) us = weights / 2.5;
+      if (splits > 1) us += 6.5 + (double)splits * (double)batch * (double)n * 8e-6 / 5.3;
+      if (best == 0 || us < best) {
+        best = us;
+        p.tile = Fp8Tile{rows, batch <= 96, splits, nullptr, nullptr};
+      }
+    }
+  if (batch <= 256 && !big) {   // (beyond, x's share of the traffic would count)
+    const double sixteens = (double)((batch + 15) / 16) * weights / 7, twos = (double)((batch + 31) / 32) * weights / 6.2;
+    const bool fills = (n + 63) / 64 * ((batch + 31) / 32) >= cus;
+    p.few = 3 + (fills && twos < sixteens ? twos : sixteens) < best;
+    if (p.few) return p;
+  }
+  if (act8) {
+    p.x_bytes = pad(2 * (uint64_t)batch * (uint64_t)k);
+    p.scale_bytes = pad(4 * (uint64_t)batch * (uint64_t)steps);
+  }
+  if (p.tile.splits > 1) p.part_bytes = pad(4 * (uint64_t)p.tile.splits * (uint64_t)batch * (uint64_t)n);
+  return p;
+}
+
+hipError_t launch_fp8_product(const ExpertsCall& c, bool act8, void* ws, hipStream_t s) {
+  const Fp8Plan p = plan_fp8(c.w.n, c.w.k, c.r.slots, act8);
+  if (p.few) return launch_fp8_rows(c, act8, s);
+  char* const at = static_cast<char*>(ws);
+  ExpertsCall call = c;
+  Fp8Tile t = p.tile;
+  t.part = reinterpret_cast<float*>(at + p.x_bytes + p.scale_bytes);
+  if (act8) {
+    uint16_t* const xe = reinterpret_cast<uint16_t*>(at);
+    float* const xs = reinterpret_cast<float*>(at + p.x_bytes);
+    const hipError_t e = launch_round_fp8(c.x, c.r.slots, c.w.k, xe, xs, s);
+    if (e != hipSuccess) return e;
+    call.x = xe;
+    t.act = xs;
+  }
+  return launch_fp8_tile(call, t, s);
 }
 
 }  // namespace uw

@@ -38,14 +38,16 @@ constexpr int kBN = 256, kNT = 512, kStep = kFp8Block;
 // what a K tail or a row index outside x reads where x goes by pointers
 __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0};
 
-struct ActScales {
-  const float* s;   // [rows][blocks of k] (ACT8)
+struct TileArgs {
+  const float* act;   // x's scales, [rows][blocks of k] (ACT8)
+  int ntiles;
+  int spread;         // blocks start along K at different places (see experts_tile.hip)
+  int splits;         // slices of K; slice i's sums go to y + i * slots * n (one matrix, plain)
 };
 
 template <int BM, bool GATED, bool ACT8, bool BIG>
 __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu, RaggedRows rr,
-                                                  const uint16_t* __restrict__ x, ActScales act, void* __restrict__ y,
-                                                  int ntiles, int spread) {
+                                                  const uint16_t* __restrict__ x, TileArgs args, void* __restrict__ y) {
   constexpr int TM = BM / 64;                 // 32-slot tiles of a wave; two column tiles
   constexpr int OUT = GATED ? 128 : 256;      // output columns of a block
   constexpr int XP = BM / 32, WP = 4, P = XP + WP;   // pieces a thread moves per step
@@ -59,11 +61,14 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   char* const wbufs[3] = {w0, w1, w2};
 
   Share sh;
-  const int nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, ntiles, BM, sh);
+  const int nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, args.ntiles, BM, sh);
   if (nt < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3, col = lane & 31, half = lane >> 5;
-  const int K = (int)vw.k, steps = (int)fp8_blocks(K);
+  // the slice's blocks of k: `steps` from `first` on
+  const int K = (int)vw.k, nk = (int)fp8_blocks(K), slice = (int)blockIdx.y;
+  const int first = (int)((int64_t)nk * slice / args.splits);
+  const int steps = (int)((int64_t)nk * (slice + 1) / args.splits) - first;
   const int64_t n0 = (int64_t)nt * OUT;
 
   // x: thread t's pieces are those at its place, piece t % 16 ^ t / 16 % 16 of rows t / 16 + 32 i
@@ -115,31 +120,30 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   // and one of up's), its slots are one a lane.
   const int64_t block_row = (GATED ? n0 : n0 + wn * 64) >> 7;
   auto scales_of = [&](const ExpertsView& v) __attribute__((always_inline)) {
-    return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + block_row * steps * 4,
-                   block_row < fp8_blocks(v.n) ? (uint64_t)steps * 4 : 0);
+    return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + block_row * nk * 4,
+                   block_row < fp8_blocks(v.n) ? (uint64_t)nk * 4 : 0);
   };
   const __amdgpu_buffer_rsrc_t rs0 = scales_of(vw), rs1 = GATED ? scales_of(vu) : rs0;
-  const __amdgpu_buffer_rsrc_t ra = rsrc_of(ACT8 ? act.s + sh.first * steps : nullptr,
-                                            ACT8 ? (uint64_t)sh.count * (uint64_t)steps * 4 : 0);
+  const __amdgpu_buffer_rsrc_t ra = rsrc_of(ACT8 ? args.act + sh.first * nk : nullptr,
+                                            ACT8 ? (uint64_t)sh.count * (uint64_t)nk * 4 : 0);
   auto slot_of = [&](int i) __attribute__((always_inline)) { return 64 * i + 32 * wm; };
   struct Scales {
     float w[2], x[TM];
   };
-  // spread: each block starts its walk along K elsewhere (see experts_tile.hip)
-  const int rot = spread ? (int)((blockIdx.x * 5u) % (unsigned)steps) : 0;
+  const int rot = args.spread ? (int)((blockIdx.x * 5u) % (unsigned)steps) : 0;
   auto block_of = [&](int s) __attribute__((always_inline)) {   // past the last: a block past K
     const int ss = s + rot;
-    return s >= steps ? steps : ss >= steps ? ss - steps : ss;
+    return s >= steps ? nk : first + (ss >= steps ? ss - steps : ss);
   };
   auto load_scales = [&](int s, Scales& c) __attribute__((always_inline)) {
-    const int b = block_of(s), at = b < steps ? 4 * b : (int)kOutside;
+    const int b = block_of(s), at = b < nk ? 4 * b : (int)kOutside;
     c.w[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs0, at, 0, 0));
     c.w[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs1, at, 0, 0)) : c.w[0];
     if constexpr (ACT8) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
         c.x[i] = __builtin_bit_cast(
-            float, __builtin_amdgcn_raw_buffer_load_b32(ra, at + 4 * steps * (slot_of(i) + col), 0, 0));
+            float, __builtin_amdgcn_raw_buffer_load_b32(ra, at + 4 * nk * (slot_of(i) + col), 0, 0));
     }
   };
 
@@ -248,7 +252,7 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   auto write = [&](auto TA) __attribute__((always_inline)) {
     constexpr int kSize = GATED ? 2 : 4, kCols = GATED ? 1 : 2;
     const __amdgpu_buffer_rsrc_t ry =
-        rsrc_of(static_cast<char*>(y) + sh.first * vw.n * kSize, (uint64_t)sh.count * (uint64_t)vw.n * kSize);
+        rsrc_of(static_cast<char*>(y) + (slice * rr.slots + sh.first) * vw.n * kSize, (uint64_t)sh.count * (uint64_t)vw.n * kSize);
     const int N = (int)vw.n;
     const bool whole = N % 4 == 0;
 #pragma unroll
@@ -357,31 +361,54 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more when the block gives it back
 }
 
+// y[i] = the slices' sums in their order
+__global__ __launch_bounds__(256) void k_sum_slices(const float* __restrict__ part, int splits, int64_t count,
+                                                    float* __restrict__ y) {
+  const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (i >= count) return;
+  if (i + 4 <= count && count % 4 == 0) {
+    f32x4_t s = *reinterpret_cast<const f32x4_t*>(part + i);
+    for (int v = 1; v < splits; ++v) s += *reinterpret_cast<const f32x4_t*>(part + v * count + i);
+    *reinterpret_cast<f32x4_t*>(y + i) = s;
+    return;
+  }
+  for (int64_t c = i; c < count && c < i + 4; ++c) {
+    float s = part[c];
+    for (int v = 1; v < splits; ++v) s += part[v * count + c];
+    y[c] = s;
+  }
+}
+
 template <int BM, bool GATED, bool ACT8, bool BIG = false>
-hipError_t launch_one(const ExpertsCall& c, const float* act, bool spread, hipStream_t s) {
+hipError_t launch_one(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s) {
   const int64_t out = GATED ? 128 : 256, ntiles = (c.w.n + out - 1) / out;
   // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
   const int64_t tiles = max_chunks(c.r.slots, c.w.count, BM, c.r.offsets != nullptr) * ntiles;
   const int64_t grid = (tiles + 7) / 8 * 8;
-  if (!grid_fits(grid, kNT)) return hipErrorNotSupported;
-  hipLaunchKernelGGL((k_fp8_tile<BM, GATED, ACT8, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x,
-                     ActScales{act}, c.y, (int)ntiles, (int)spread);
+  if (!grid_fits(grid * t.splits, kNT)) return hipErrorNotSupported;
+  const TileArgs a{t.act, (int)ntiles, (int)t.spread, t.splits};
+  hipLaunchKernelGGL((k_fp8_tile<BM, GATED, ACT8, BIG>), dim3((unsigned)grid, (unsigned)t.splits), dim3(kNT), 0, s, c.w,
+                     c.u, c.r, c.x, a, t.splits > 1 ? t.part : c.y);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || t.splits == 1) return e;
+  const int64_t count = c.r.slots * c.w.n;
+  hipLaunchKernelGGL(k_sum_slices, dim3((unsigned)((count + 1023) / 1024)), dim3(256), 0, s, t.part, t.splits, count,
+                     static_cast<float*>(c.y));
   return hipGetLastError();
 }
 
 template <bool GATED, bool ACT8>
-hipError_t launch_rows(const ExpertsCall& c, const float* act, int rows, bool spread, hipStream_t s) {
-  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_one<128, GATED, ACT8, true>(c, act, spread, s);
-  if (rows <= 64) return launch_one<64, GATED, ACT8>(c, act, spread, s);
-  return launch_one<128, GATED, ACT8>(c, act, spread, s);
+hipError_t launch_rows(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s) {
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_one<128, GATED, ACT8, true>(c, t, s);
+  if (t.rows <= 64) return launch_one<64, GATED, ACT8>(c, t, s);
+  return launch_one<128, GATED, ACT8>(c, t, s);
 }
 
 }  // namespace
 
-hipError_t launch_fp8_tile(const ExpertsCall& c, const float* act, int rows, bool spread, hipStream_t s) {
-  if (act) return launch_rows<false, true>(c, act, rows, spread, s);
-  return c.gated ? launch_rows<true, false>(c, nullptr, rows, spread, s)
-                 : launch_rows<false, false>(c, nullptr, rows, spread, s);
+hipError_t launch_fp8_tile(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s) {
+  if (t.act) return launch_rows<false, true>(c, t, s);
+  return c.gated ? launch_rows<true, false>(c, t, s) : launch_rows<false, false>(c, t, s);
 }
 
 }  // namespace uw

@@ -62,7 +62,7 @@ def test_product_refusals(uw):
     assert size(1 << 20, 64, 1 << 30, 2, ctypes.byref(n)) == UNSUPPORTED   # more GPU threads than a launch has
     assert size((1 << 20) + 1, 64, 4, 0, ctypes.byref(n)) == UNSUPPORTED
     assert size(64, (1 << 20) + 32, 4, 0, ctypes.byref(n)) == UNSUPPORTED
-    assert size(64, 64, 4, 0, ctypes.byref(n)) == 0
+    assert size(64, 64, 4, 0, ctypes.byref(n)) == 0 and n.value == 0
     m = uw._lib.uw_matmul_fp8
     assert m(None, P, 64, 64, P, 4, P, 0, None, 0, None) == INVALID
     assert m(P, None, 64, 64, P, 4, P, 0, None, 0, None) == INVALID
