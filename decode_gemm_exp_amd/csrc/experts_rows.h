@@ -131,17 +131,21 @@ __device__ __forceinline__ Place place_of(const RaggedRows& rr, unsigned ntiles,
   return {turn / chunks, turn % chunks};
 }
 
-// A block's tile and expert, and the rows of x its slots multiply.  RaggedRows: by
-// the plan in memory.  RoutedRows: by its own choice, block 0 writing the plan.
+// A block's tiles and experts, and the rows of x its slots multiply.  RaggedRows: one
+// tile, by the plan in memory.  RoutedRows: by its own choice, block 0 writing the plan
+// and the others walking through the tiles of every expert that has pairs, so that a block
+// routes once however many tiles there are.
 template <typename RR>
 struct Finder;
 
 template <>
 struct Finder<RaggedRows> {
+  static constexpr bool kWalks = false;
   struct Lds {};
-  // false: the block is done
-  __device__ __forceinline__ static bool find(const RaggedRows& rr, Lds&, unsigned ntiles, unsigned chunks, int experts,
-                                              int most, unsigned& tile, Share& sh) {
+  // false: the block has nothing (more) to do
+  __device__ __forceinline__ bool begin(const RaggedRows&, Lds&) { return true; }
+  __device__ __forceinline__ bool find(const RaggedRows& rr, Lds&, int, unsigned ntiles, unsigned chunks, int experts,
+                                       int most, unsigned& tile, Share& sh) const {
     const Place at = place_of(rr, ntiles, chunks);
     if (at.tile >= ntiles || at.chunk >= chunks) return false;
     tile = at.tile;
@@ -150,7 +154,7 @@ struct Finder<RaggedRows> {
   }
   // row[q]: of slot slot(q), those behind the share's last as its first
   template <int N, typename F>
-  __device__ __forceinline__ static void rows(const RaggedRows& rr, const Lds&, const Share& sh, int32_t (&row)[N], F&& slot) {
+  __device__ __forceinline__ void rows(const RaggedRows& rr, const Lds&, const Share& sh, int32_t (&row)[N], F&& slot) const {
 #pragma unroll
     for (int q = 0; q < N; ++q) row[q] = (int32_t)sh.first + (slot(q) < sh.count ? slot(q) : 0);   // (fewer than 2^31 slots)
     if (rr.rows) {
@@ -162,23 +166,32 @@ struct Finder<RaggedRows> {
 
 template <int L, int NV>
 struct Finder<RoutedRows<L, NV>> {
+  static constexpr bool kWalks = true;
   using Lds = RoutedLds;
-  __device__ __forceinline__ static bool find(const RoutedRows<L, NV>& rr, Lds& lds, unsigned ntiles, unsigned, int, int,
-                                              unsigned& tile, Share& sh) {
+  int items;
+  __device__ __forceinline__ bool begin(const RoutedRows<L, NV>& rr, Lds& lds) {
     if (blockIdx.x == 0) {
       route_few<L, NV, true>(rr.c, lds);
-      plan_few(rr.c, lds);
       return false;
     }
-    route_few<L, NV, false>(rr.c, lds);
-    tile = (blockIdx.x - 1) % ntiles;
-    sh = share_few(rr.c, lds, (int)((blockIdx.x - 1) / ntiles));
-    return sh.count != 0;
+    items = __builtin_amdgcn_readfirstlane(route_few<L, NV, false>(rr.c, lds));
+    return true;
+  }
+  // the block's turn-th tile
+  __device__ __forceinline__ bool find(const RoutedRows<L, NV>&, Lds& lds, int turn, unsigned ntiles, unsigned, int, int,
+                                       unsigned& tile, Share& sh) const {
+    const unsigned at = blockIdx.x - 1 + (unsigned)turn * (gridDim.x - 1), item = at / ntiles;
+    if (item >= (unsigned)items) return false;
+    tile = at - item * ntiles;
+    sh.expert = __builtin_amdgcn_readfirstlane(lds.p.item_expert[item]);
+    sh.first = __builtin_amdgcn_readfirstlane(lds.p.item_first[item]);
+    sh.count = __builtin_amdgcn_readfirstlane(lds.p.item_first[item + 1]) - (int)sh.first;
+    return true;
   }
   template <int N, typename F>
-  __device__ __forceinline__ static void rows(const RoutedRows<L, NV>&, const Lds& lds, const Share& sh, int32_t (&row)[N], F&& slot) {
+  __device__ __forceinline__ void rows(const RoutedRows<L, NV>&, const Lds& lds, const Share& sh, int32_t (&row)[N], F&& slot) const {
 #pragma unroll
-    for (int q = 0; q < N; ++q) row[q] = lds.tok[threadIdx.x >> 6][slot(q) < sh.count ? slot(q) : 0];
+    for (int q = 0; q < N; ++q) row[q] = lds.p.token[sh.first + (slot(q) < sh.count ? slot(q) : 0)];
   }
 };
 

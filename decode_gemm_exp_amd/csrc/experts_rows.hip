@@ -32,92 +32,98 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   constexpr int RT = GATED ? R / 2 : R;   // distinct output tiles
   __shared__ f32x4_t red[4 * R * Q * 64];
   __shared__ typename Finder<RR>::Lds found;
-  unsigned tile;
-  Share sh;
-  if (!Finder<RR>::find(rr, found, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, g = lane >> 4;
-  const int64_t N = vw.n;
-  const int K = (int)vw.k;
-  const int64_t n0 = (int64_t)tile * (16 * RT);
-  const Mat<FORM> mw = matrix_of<FORM>(vw, sh.expert, n0, 16 * RT);
-  Mat<FORM> mu = mw;
-  if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert, n0, 16 * RT);
-  auto mat = [&](int t) __attribute__((always_inline)) -> const Mat<FORM>& { return GATED && t >= RT ? mu : mw; };
-  auto row_of = [&](int t) __attribute__((always_inline)) { return 16 * (t % RT) + i16; };
+  Finder<RR> finder;
+  if (!finder.begin(rr, found)) return;
+  for (int turn = 0;; ++turn) {
+    unsigned tile;
+    Share sh;
+    if (!finder.find(rr, found, turn, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int i16 = lane & 15, g = lane >> 4;
+    const int64_t N = vw.n;
+    const int K = (int)vw.k;
+    const int64_t n0 = (int64_t)tile * (16 * RT);
+    const Mat<FORM> mw = matrix_of<FORM>(vw, sh.expert, n0, 16 * RT);
+    Mat<FORM> mu = mw;
+    if constexpr (GATED) mu = matrix_of<FORM>(vu, sh.expert, n0, 16 * RT);
+    auto mat = [&](int t) __attribute__((always_inline)) -> const Mat<FORM>& { return GATED && t >= RT ? mu : mw; };
+    auto row_of = [&](int t) __attribute__((always_inline)) { return 16 * (t % RT) + i16; };
 
-  // x rows of this lane's slots
-  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
-  uint32_t xrow[Q];
-  int32_t row[Q];
-  Finder<RR>::rows(rr, found, sh, row, [&](int q) __attribute__((always_inline)) { return 16 * q + i16; });
+    // x rows of this lane's slots
+    const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
+    uint32_t xrow[Q];
+    int32_t row[Q];
+    finder.rows(rr, found, sh, row, [&](int q) __attribute__((always_inline)) { return 16 * q + i16; });
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    const bool in = (16 * q + i16 < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
-    xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
+    for (int q = 0; q < Q; ++q) {
+      const bool in = (16 * q + i16 < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
+      xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
+    }
+
+    const int nwin = (K + W - 1) / W;
+    f32x4_t acc[R][Q];
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    struct Win {
+      Raw r[R];
+      uint4 xv[Q][4];
+    };
+    auto flags = [&](int j, Flags (&f)[R]) __attribute__((always_inline)) {
+#pragma unroll
+      for (int t = 0; t < R; ++t) load_flags<FORM>(mat(t), row_of(t), K, W * j + k_off<FORM>(0, g), f[t]);
+    };
+    // windows past the last (whole rounds of four) lie past K and load zeros
+    auto load = [&](int j, const Flags (&f)[R], Win& w) __attribute__((always_inline)) {
+      const int k0 = W * j;
+#pragma unroll
+      for (int t = 0; t < R; ++t) load_raw<FORM>(mat(t), row_of(t), K, k0, g, f[t], w.r[t]);
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = k0 + k_off<FORM>(i, g);
+          w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+        }
+    };
+    auto compute = [&](const Win& w) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const bf16x8_t a = a_frag<FORM>(mat(t), w.r[t], i);
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, w.xv[q][i]), acc[t][q],
+                                                                0, 0, 0);
+        }
+    };
+
+    Win wa, wb;
+    Flags fa[R], fb[R];
+    flags(wave, fa);
+    flags(wave + 4, fb);
+    load(wave, fa, wa);
+    flags(wave + 8, fa);
+    for (int j = wave; j < nwin; j += 8) {
+      load(j + 4, fb, wb);
+      flags(j + 12, fb);
+      compute(wa);
+      load(j + 8, fa, wa);
+      flags(j + 16, fa);
+      compute(wb);
+    }
+#pragma unroll
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
+    __syncthreads();
+    finish<R, Q, GATED, 4>(red, sh, n0, N, y);
+    if constexpr (!Finder<RR>::kWalks) return;
+    __syncthreads();   // the sums have been read
   }
-
-  const int nwin = (K + W - 1) / W;
-  f32x4_t acc[R][Q];
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  struct Win {
-    Raw r[R];
-    uint4 xv[Q][4];
-  };
-  auto flags = [&](int j, Flags (&f)[R]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < R; ++t) load_flags<FORM>(mat(t), row_of(t), K, W * j + k_off<FORM>(0, g), f[t]);
-  };
-  // windows past the last (whole rounds of four) lie past K and load zeros
-  auto load = [&](int j, const Flags (&f)[R], Win& w) __attribute__((always_inline)) {
-    const int k0 = W * j;
-#pragma unroll
-    for (int t = 0; t < R; ++t) load_raw<FORM>(mat(t), row_of(t), K, k0, g, f[t], w.r[t]);
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = k0 + k_off<FORM>(i, g);
-        w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
-      }
-  };
-  auto compute = [&](const Win& w) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const bf16x8_t a = a_frag<FORM>(mat(t), w.r[t], i);
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-          acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, w.xv[q][i]), acc[t][q],
-                                                              0, 0, 0);
-      }
-  };
-
-  Win wa, wb;
-  Flags fa[R], fb[R];
-  flags(wave, fa);
-  flags(wave + 4, fb);
-  load(wave, fa, wa);
-  flags(wave + 8, fa);
-  for (int j = wave; j < nwin; j += 8) {
-    load(j + 4, fb, wb);
-    flags(j + 12, fb);
-    compute(wa);
-    load(j + 8, fa, wa);
-    flags(j + 16, fa);
-    compute(wb);
-  }
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
-  __syncthreads();
-  finish<R, Q, GATED, 4>(red, sh, n0, N, y);
 }
 
 // MXFP4.  Its weights are few bytes a lane, and a wave that loads operands
@@ -147,150 +153,156 @@ __global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, Experts
   constexpr int kX = XL ? 16 * 512 : 4;
   __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
   __shared__ typename Finder<RR>::Lds found;
-  unsigned tile;
-  Share sh;
-  if (!Finder<RR>::find(rr, found, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int i16 = lane & 15, g = lane >> 4;
-  const int64_t N = vw.n;
-  const int K = (int)vw.k, st = (int)mx4_scale_stride(K);
-  const int64_t n0 = (int64_t)tile * kRows;
-  const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
-  auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
-    return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * (K / 2), (uint64_t)(rows * (K / 2)));
-  };
-  auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {
-    return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + n0 * st, (uint64_t)(rows * st));
-  };
-  const __amdgpu_buffer_rsrc_t ww = weights(vw), ws = scales(vw);
-  const __amdgpu_buffer_rsrc_t uw = GATED ? weights(vu) : ww, us = GATED ? scales(vu) : ws;
+  Finder<RR> finder;
+  if (!finder.begin(rr, found)) return;
+  for (int turn = 0;; ++turn) {
+    unsigned tile;
+    Share sh;
+    if (!finder.find(rr, found, turn, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int i16 = lane & 15, g = lane >> 4;
+    const int64_t N = vw.n;
+    const int K = (int)vw.k, st = (int)mx4_scale_stride(K);
+    const int64_t n0 = (int64_t)tile * kRows;
+    const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
+    auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
+      return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * (K / 2), (uint64_t)(rows * (K / 2)));
+    };
+    auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {
+      return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + n0 * st, (uint64_t)(rows * st));
+    };
+    const __amdgpu_buffer_rsrc_t ww = weights(vw), ws = scales(vw);
+    const __amdgpu_buffer_rsrc_t uw = GATED ? weights(vu) : ww, us = GATED ? scales(vu) : ws;
 
-  // x rows of this lane's slots
-  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
-  constexpr int XR = XL ? 8 : Q;
-  uint32_t xrow[XR];
-  int32_t row[XR];
-  auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 2 * q + (lane >> 5) : 16 * q + i16; };
-  Finder<RR>::rows(rr, found, sh, row, slot);
+    // x rows of this lane's slots
+    const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
+    constexpr int XR = XL ? 8 : Q;
+    uint32_t xrow[XR];
+    int32_t row[XR];
+    auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 2 * q + (lane >> 5) : 16 * q + i16; };
+    finder.rows(rr, found, sh, row, slot);
 
-  f32x4_t acc[R][Q];
+    f32x4_t acc[R][Q];
 #pragma unroll
-  for (int t = 0; t < R; ++t)
+    for (int t = 0; t < R; ++t)
 #pragma unroll
-    for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  uint32_t top[R] = {};   // the largest scale byte of the lane's rows
+      for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    uint32_t top[R] = {};   // the largest scale byte of the lane's rows
 
-  // Load i of eight takes rows 8 i .. 8 i + 7, eight lanes a row; of the 64 rows
-  // the gated form has W's first, then U's.
-  const int pr = lane >> 3;                                   // row of the eight
-  auto load_w = [&](int j, char* wbuf, char* sbuf) __attribute__((always_inline)) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
-    const int k0 = 256 * j;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool u = GATED && i >= 4;
-      const int r = 8 * (u ? i - 4 : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
-      const uint32_t off = k0 + 32 * piece < K ? (uint32_t)(r * (K / 2) + (k0 / 2 + 16 * piece)) : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(u ? uw : ww, (lds_char*)(wbuf + wave * kW + 1024 * i), 16, (int)off, 0,
-                                               0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {   // scales, two lanes a row
-      const int r = GATED ? lane >> 1 : 32 * i + (lane >> 1);
-      const uint32_t off = k0 + 128 * (lane & 1) < K ? (uint32_t)(r * st + 8 * j + 4 * (lane & 1)) : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(GATED && i ? us : ws, (lds_char*)(sbuf + wave * kS + 256 * i), 4,
-                                               (int)off, 0, 0, 0);
-    }
-  };
-  auto load_x = [&](int j, char* xbuf, uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
-    const int k0 = 256 * j;
-    if constexpr (XL) {
+    // Load i of eight takes rows 8 i .. 8 i + 7, eight lanes a row; of the 64 rows
+    // the gated form has W's first, then U's.
+    const int pr = lane >> 3;                                   // row of the eight
+    auto load_w = [&](int j, char* wbuf, char* sbuf) __attribute__((always_inline)) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
+      const int k0 = 256 * j;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int k = k0 + 8 * ((lane & 31) ^ (2 * i + (lane >> 5)));
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char*)(xbuf + wave * kX + 1024 * i), 16,
-                                                 (int)(k < K ? xrow[i] + 2u * (uint32_t)k : kOutside), 0, 0, 0);
+        const bool u = GATED && i >= 4;
+        const int r = 8 * (u ? i - 4 : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
+        const uint32_t off = k0 + 32 * piece < K ? (uint32_t)(r * (K / 2) + (k0 / 2 + 16 * piece)) : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(u ? uw : ww, (lds_char*)(wbuf + wave * kW + 1024 * i), 16, (int)off, 0,
+                                                 0, 0);
       }
-    } else {
 #pragma unroll
-      for (int q = 0; q < Q; ++q)
+      for (int i = 0; i < 2; ++i) {   // scales, two lanes a row
+        const int r = GATED ? lane >> 1 : 32 * i + (lane >> 1);
+        const uint32_t off = k0 + 128 * (lane & 1) < K ? (uint32_t)(r * st + 8 * j + 4 * (lane & 1)) : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(GATED && i ? us : ws, (lds_char*)(sbuf + wave * kS + 256 * i), 4,
+                                                 (int)off, 0, 0, 0);
+      }
+    };
+    auto load_x = [&](int j, char* xbuf, uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
+      const int k0 = 256 * j;
+      if constexpr (XL) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const int k = k0 + 64 * g + 8 * i;
-          xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+          const int k = k0 + 8 * ((lane & 31) ^ (2 * i + (lane >> 5)));
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char*)(xbuf + wave * kX + 1024 * i), 16,
+                                                   (int)(k < K ? xrow[i] + 2u * (uint32_t)k : kOutside), 0, 0, 0);
         }
-    }
-  };
-  auto compute = [&](int j, const char* wbuf, const char* sbuf, const char* xbuf, const uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
-    const bool in0 = 256 * j + 64 * g < K, in1 = 256 * j + 64 * g + 32 < K;
-    float scale[R][2];
-    uint4 d[R][2];
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      const int r = 16 * t + i16;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        d[t][u] = *reinterpret_cast<const uint4*>(wbuf + wave * kW + r * 128 + (((2 * g + u) ^ (r >> 1 & 7)) << 4));
-      const uint32_t f = *reinterpret_cast<const uint16_t*>(sbuf + wave * kS + r * 8 + 2 * g);
-      const uint32_t lo = in0 ? f & 255u : 0u, hi = in1 ? f >> 8 : 0u;
-      scale[t][0] = e8m0_float(lo);
-      scale[t][1] = e8m0_float(hi);
-      top[t] = max(top[t], max(lo, hi));
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      uint4 xl;
-      if constexpr (XL) xl = *reinterpret_cast<const uint4*>(xbuf + wave * kX + i16 * 512 + (((8 * g + i) ^ i16) << 4));
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, mx4_unpack8(word4(d[t][i / 4], i % 4), scale[t][i / 4]));
+      } else {
 #pragma unroll
         for (int q = 0; q < Q; ++q)
-          acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, XL ? xl : xv[q][i]), acc[t][q],
-                                                              0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int k = k0 + 64 * g + 8 * i;
+            xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+          }
       }
+    };
+    auto compute = [&](int j, const char* wbuf, const char* sbuf, const char* xbuf, const uint4 (&xv)[Q][8]) __attribute__((always_inline)) {
+      const bool in0 = 256 * j + 64 * g < K, in1 = 256 * j + 64 * g + 32 < K;
+      float scale[R][2];
+      uint4 d[R][2];
+#pragma unroll
+      for (int t = 0; t < R; ++t) {
+        const int r = 16 * t + i16;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          d[t][u] = *reinterpret_cast<const uint4*>(wbuf + wave * kW + r * 128 + (((2 * g + u) ^ (r >> 1 & 7)) << 4));
+        const uint32_t f = *reinterpret_cast<const uint16_t*>(sbuf + wave * kS + r * 8 + 2 * g);
+        const uint32_t lo = in0 ? f & 255u : 0u, hi = in1 ? f >> 8 : 0u;
+        scale[t][0] = e8m0_float(lo);
+        scale[t][1] = e8m0_float(hi);
+        top[t] = max(top[t], max(lo, hi));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint4 xl;
+        if constexpr (XL) xl = *reinterpret_cast<const uint4*>(xbuf + wave * kX + i16 * 512 + (((8 * g + i) ^ i16) << 4));
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const bf16x8_t a = __builtin_bit_cast(bf16x8_t, mx4_unpack8(word4(d[t][i / 4], i % 4), scale[t][i / 4]));
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, XL ? xl : xv[q][i]), acc[t][q],
+                                                                0, 0, 0);
+        }
+      }
+    };
+
+    // windows past the last (whole rounds of the waves) lie past K and load zeros
+    const int nwin = (K + 255) / 256;
+    uint4 xa[Q][8], xb[Q][8];
+    load_w(wave, w0, s0);   // on its way while the row indices arrive
+#pragma unroll
+    for (int q = 0; q < XR; ++q) {
+      const bool in = (slot(q) < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
+      xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
     }
-  };
+    load_x(wave, x0, xa);
+    for (int j = wave; j < nwin; j += 2 * NW) {
+      load_w(j + NW, w1, s1);
+      load_x(j + NW, x1, xb);
+      compute(j, w0, s0, x0, xa);
+      load_w(j + 2 * NW, w0, s0);
+      load_x(j + 2 * NW, x0, xa);
+      compute(j + NW, w1, s1, x1, xb);
+    }
+    // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+    for (int t = 0; t < R; ++t) {
+      const uint32_t n = top[t] == 255u ? 0x7FC07FC0u : 0u;
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+        acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(n, n, n, n)),
+                                                            __builtin_bit_cast(bf16x8_t, zero), acc[t][q], 0, 0, 0);
+    }
 
-  // windows past the last (whole rounds of the waves) lie past K and load zeros
-  const int nwin = (K + 255) / 256;
-  uint4 xa[Q][8], xb[Q][8];
-  load_w(wave, w0, s0);   // on its way while the row indices arrive
+    __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
+    __syncthreads();
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(w0);
+    static_assert(R * Q * 64 * 16 <= kW, "the sums fit one ring buffer");
 #pragma unroll
-  for (int q = 0; q < XR; ++q) {
-    const bool in = (slot(q) < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
-    xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
+    for (int t = 0; t < R; ++t)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
+    __syncthreads();
+    finish<R, Q, GATED, NW>(red, sh, n0, N, y);
+    if constexpr (!Finder<RR>::kWalks) return;
+    __syncthreads();   // the sums have been read
   }
-  load_x(wave, x0, xa);
-  for (int j = wave; j < nwin; j += 2 * NW) {
-    load_w(j + NW, w1, s1);
-    load_x(j + NW, x1, xb);
-    compute(j, w0, s0, x0, xa);
-    load_w(j + 2 * NW, w0, s0);
-    load_x(j + 2 * NW, x0, xa);
-    compute(j + NW, w1, s1, x1, xb);
-  }
-  // a NaN scale makes its row's outputs NaN: one more MFMA, NaN times zero
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-  for (int t = 0; t < R; ++t) {
-    const uint32_t n = top[t] == 255u ? 0x7FC07FC0u : 0u;
-#pragma unroll
-    for (int q = 0; q < Q; ++q)
-      acc[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, make_uint4(n, n, n, n)),
-                                                          __builtin_bit_cast(bf16x8_t, zero), acc[t][q], 0, 0, 0);
-  }
-
-  __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
-  __syncthreads();
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(w0);
-  static_assert(R * Q * 64 * 16 <= kW, "the sums fit one ring buffer");
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
-  __syncthreads();
-  finish<R, Q, GATED, NW>(red, sh, n0, N, y);
 }
 
 template <int FORM, int R, int Q, bool GATED>
@@ -342,7 +354,7 @@ hipError_t launch_gated(const ExpertsCall& c, int64_t avg, hipStream_t s) {
 
 template <int FORM>
 hipError_t launch_routed(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
-  const int64_t rows = FORM == kFormMx4 ? 32 : 16, ntiles = (c.w.n + rows - 1) / rows, grid = routed_grid(r, ntiles);
+  const int64_t rows = FORM == kFormMx4 ? 32 : 16, ntiles = (c.w.n + rows - 1) / rows, grid = routed_grid(r, ntiles, FORM == kFormMx4 ? 2 : 4);
   if (!grid_fits(grid, 256)) return hipErrorNotSupported;
   return with_routed(r, [&](auto rr) {
     using RR = decltype(rr);

@@ -30,169 +30,175 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
   __shared__ __attribute__((aligned(128))) char w0[NW * kW], w1[NW * kW];
   __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
   __shared__ typename Finder<RR>::Lds found;
-  unsigned tile;
-  Share sh;
-  if (!Finder<RR>::find(rr, found, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int i16 = lane & 15, g = lane >> 4;
-  const int64_t N = vw.n;
-  const int K = (int)vw.k, nwin = (int)fp8_blocks(K);
-  const int64_t n0 = (int64_t)tile * kRows;
-  const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
-  auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
-    return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * K, (uint64_t)(rows * K));
-  };
-  auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {   // the row of blocks that holds n0
-    return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + (n0 >> 7) * nwin * 4, (uint64_t)nwin * 4);
-  };
-  const __amdgpu_buffer_rsrc_t ww = weights(vw), ws = scales(vw);
-  const __amdgpu_buffer_rsrc_t uw = GATED ? weights(vu) : ww, us = GATED ? scales(vu) : ws;
+  Finder<RR> finder;
+  if (!finder.begin(rr, found)) return;
+  for (int turn = 0;; ++turn) {
+    unsigned tile;
+    Share sh;
+    if (!finder.find(rr, found, turn, (unsigned)ntiles, (unsigned)chunks, vw.count, 16 * Q, tile, sh)) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int i16 = lane & 15, g = lane >> 4;
+    const int64_t N = vw.n;
+    const int K = (int)vw.k, nwin = (int)fp8_blocks(K);
+    const int64_t n0 = (int64_t)tile * kRows;
+    const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
+    auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
+      return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * K, (uint64_t)(rows * K));
+    };
+    auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {   // the row of blocks that holds n0
+      return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + (n0 >> 7) * nwin * 4, (uint64_t)nwin * 4);
+    };
+    const __amdgpu_buffer_rsrc_t ww = weights(vw), ws = scales(vw);
+    const __amdgpu_buffer_rsrc_t uw = GATED ? weights(vu) : ww, us = GATED ? scales(vu) : ws;
 
-  // x rows of this lane's slots
-  const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
-  constexpr int XR = XL ? 4 : Q;
-  uint32_t xrow[XR];
-  int32_t row[XR];
-  auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 4 * q + g : 16 * q + i16; };
-  Finder<RR>::rows(rr, found, sh, row, slot);
+    // x rows of this lane's slots
+    const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
+    constexpr int XR = XL ? 4 : Q;
+    uint32_t xrow[XR];
+    int32_t row[XR];
+    auto slot = [&](int q) __attribute__((always_inline)) { return XL ? 4 * q + g : 16 * q + i16; };
+    finder.rows(rr, found, sh, row, slot);
 
-  f32x4_t acc[R][Q];
-#pragma unroll
-  for (int t = 0; t < R; ++t)
-#pragma unroll
-    for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-
-  // Load i takes rows 8 i .. 8 i + 7, eight lanes a row; of the 16 R rows
-  // the gated form has W's first, then U's.
-  const int pr = lane >> 3;
-  auto load_w = [&](int j, char* wbuf) __attribute__((always_inline)) {
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
-    const int k0 = 128 * j;
-#pragma unroll
-    for (int i = 0; i < 2 * R; ++i) {
-      const bool u = GATED && i >= R;
-      const int r = 8 * (u ? i - R : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
-      const uint32_t off = k0 + 16 * piece < K ? (uint32_t)(r * K + (k0 + 16 * piece)) : kOutside;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(u ? uw : ww, (lds_char*)(wbuf + wave * kW + 1024 * i), 16, (int)off, 0,
-                                               0, 0);
-    }
-  };
-  struct Win {
-    uint4 xv[Q][4];
-    float s[2];   // the blocks' scales, 0 past the last window
-  };
-  auto load_x = [&](int j, char* xbuf, Win& w) __attribute__((always_inline)) {
-    const int k0 = 128 * j;
-    if constexpr (XL) {   // rows 4 i .. 4 i + 3, sixteen lanes a row; piece p of row r at 16 (p ^ r)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = k0 + 8 * (i16 ^ (4 * i + g));
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char*)(xbuf + wave * kX + 1024 * i), 16,
-                                                 (int)(k < K ? xrow[i] + 2u * (uint32_t)k : kOutside), 0, 0, 0);
-      }
-    } else {
-#pragma unroll
-      for (int q = 0; q < Q; ++q)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = k0 + 32 * g + 8 * i;
-          w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
-        }
-    }
-    const int at = j < nwin ? 4 * j : (int)kOutside;
-    w.s[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ws, at, 0, 0));
-    w.s[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(us, at, 0, 0)) : w.s[0];
-  };
-  auto compute = [&](const char* wbuf, const char* xbuf, Win& w) __attribute__((always_inline)) {
-    if constexpr (XL) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        w.xv[0][i] = *reinterpret_cast<const uint4*>(xbuf + wave * kX + i16 * 256 + (((4 * g + i) ^ i16) << 4));
-    }
-    uint4 d[R][2];
-#pragma unroll
-    for (int t = 0; t < R; ++t) {
-      const int r = 16 * t + i16;
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        d[t][u] = *reinterpret_cast<const uint4*>(wbuf + wave * kW + r * 128 + (((2 * g + u) ^ (r >> 1 & 7)) << 4));
-    }
-    f32x4_t part[R][Q];
+    f32x4_t acc[R][Q];
 #pragma unroll
     for (int t = 0; t < R; ++t)
 #pragma unroll
-      for (int q = 0; q < Q; ++q) part[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    float sx[Q];
-    uint4 xv[Q][4];
+      for (int q = 0; q < Q; ++q) acc[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+    // Load i takes rows 8 i .. 8 i + 7, eight lanes a row; of the 16 R rows
+    // the gated form has W's first, then U's.
+    const int pr = lane >> 3;
+    auto load_w = [&](int j, char* wbuf) __attribute__((always_inline)) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // what was read from the buffer has been
+      const int k0 = 128 * j;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      sx[q] = 1.0f;
-      if constexpr (ACT8) {   // the block's maximum is over the four lane groups
-        uint32_t m = max_halves(max_halves(bf16_top8(w.xv[q][0]), bf16_top8(w.xv[q][1])),
-                                max_halves(bf16_top8(w.xv[q][2]), bf16_top8(w.xv[q][3])));
-        m = max_halves(m, (uint32_t)__shfl_xor((int)m, 16));
-        m = max_halves(m, (uint32_t)__shfl_xor((int)m, 32));
-        const Fp8Scale f = fp8_scale(top_bits(m));
-        sx[q] = f.scale;
+      for (int i = 0; i < 2 * R; ++i) {
+        const bool u = GATED && i >= R;
+        const int r = 8 * (u ? i - R : i) + pr, piece = (lane & 7) ^ ((8 * i + pr) >> 1 & 7);
+        const uint32_t off = k0 + 16 * piece < K ? (uint32_t)(r * K + (k0 + 16 * piece)) : kOutside;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(u ? uw : ww, (lds_char*)(wbuf + wave * kW + 1024 * i), 16, (int)off, 0,
+                                                 0, 0);
+      }
+    };
+    struct Win {
+      uint4 xv[Q][4];
+      float s[2];   // the blocks' scales, 0 past the last window
+    };
+    auto load_x = [&](int j, char* xbuf, Win& w) __attribute__((always_inline)) {
+      const int k0 = 128 * j;
+      if constexpr (XL) {   // rows 4 i .. 4 i + 3, sixteen lanes a row; piece p of row r at 16 (p ^ r)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint2 e = fp8_pack8(w.xv[q][i], f.inv);
-          xv[q][i] = fp8_unpack8(e.x, e.y);
+          const int k = k0 + 8 * (i16 ^ (4 * i + g));
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_char*)(xbuf + wave * kX + 1024 * i), 16,
+                                                   (int)(k < K ? xrow[i] + 2u * (uint32_t)k : kOutside), 0, 0, 0);
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) xv[q][i] = w.xv[q][i];
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int t = 0; t < R; ++t) {
-        const uint4& h = d[t][i >> 1];
-        const bf16x8_t a = __builtin_bit_cast(bf16x8_t, i & 1 ? fp8_unpack8(h.z, h.w) : fp8_unpack8(h.x, h.y));
-#pragma unroll
         for (int q = 0; q < Q; ++q)
-          part[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, xv[q][i]), part[t][q],
-                                                               0, 0, 0);
-      }
 #pragma unroll
-    for (int q = 0; q < Q; ++q)
+          for (int i = 0; i < 4; ++i) {
+            const int k = k0 + 32 * g + 8 * i;
+            w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
+          }
+      }
+      const int at = j < nwin ? 4 * j : (int)kOutside;
+      w.s[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ws, at, 0, 0));
+      w.s[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(us, at, 0, 0)) : w.s[0];
+    };
+    auto compute = [&](const char* wbuf, const char* xbuf, Win& w) __attribute__((always_inline)) {
+      if constexpr (XL) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          w.xv[0][i] = *reinterpret_cast<const uint4*>(xbuf + wave * kX + i16 * 256 + (((4 * g + i) ^ i16) << 4));
+      }
+      uint4 d[R][2];
 #pragma unroll
       for (int t = 0; t < R; ++t) {
-        const float sw = w.s[t >= RT ? 1 : 0], s = ACT8 ? sx[q] * sw : sw;
+        const int r = 16 * t + i16;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[t][q][c] = __builtin_fmaf(part[t][q][c], s, acc[t][q][c]);
+        for (int u = 0; u < 2; ++u)
+          d[t][u] = *reinterpret_cast<const uint4*>(wbuf + wave * kW + r * 128 + (((2 * g + u) ^ (r >> 1 & 7)) << 4));
       }
-  };
+      f32x4_t part[R][Q];
+#pragma unroll
+      for (int t = 0; t < R; ++t)
+#pragma unroll
+        for (int q = 0; q < Q; ++q) part[t][q] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      float sx[Q];
+      uint4 xv[Q][4];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        sx[q] = 1.0f;
+        if constexpr (ACT8) {   // the block's maximum is over the four lane groups
+          uint32_t m = max_halves(max_halves(bf16_top8(w.xv[q][0]), bf16_top8(w.xv[q][1])),
+                                  max_halves(bf16_top8(w.xv[q][2]), bf16_top8(w.xv[q][3])));
+          m = max_halves(m, (uint32_t)__shfl_xor((int)m, 16));
+          m = max_halves(m, (uint32_t)__shfl_xor((int)m, 32));
+          const Fp8Scale f = fp8_scale(top_bits(m));
+          sx[q] = f.scale;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint2 e = fp8_pack8(w.xv[q][i], f.inv);
+            xv[q][i] = fp8_unpack8(e.x, e.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) xv[q][i] = w.xv[q][i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const uint4& h = d[t][i >> 1];
+          const bf16x8_t a = __builtin_bit_cast(bf16x8_t, i & 1 ? fp8_unpack8(h.z, h.w) : fp8_unpack8(h.x, h.y));
+#pragma unroll
+          for (int q = 0; q < Q; ++q)
+            part[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, xv[q][i]), part[t][q],
+                                                                 0, 0, 0);
+        }
+#pragma unroll
+      for (int q = 0; q < Q; ++q)
+#pragma unroll
+        for (int t = 0; t < R; ++t) {
+          const float sw = w.s[t >= RT ? 1 : 0], s = ACT8 ? sx[q] * sw : sw;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[t][q][c] = __builtin_fmaf(part[t][q][c], s, acc[t][q][c]);
+        }
+    };
 
-  // windows past the last (whole rounds of the waves) lie past K: zeros, scaled by 0
-  Win wa, wb;
-  load_w(wave, w0);   // on its way while the row indices arrive
+    // windows past the last (whole rounds of the waves) lie past K: zeros, scaled by 0
+    Win wa, wb;
+    load_w(wave, w0);   // on its way while the row indices arrive
 #pragma unroll
-  for (int q = 0; q < XR; ++q) {
-    const bool in = (slot(q) < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
-    xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
-  }
-  load_x(wave, x0, wa);
-  for (int j = wave; j < nwin; j += 2 * NW) {
-    load_w(j + NW, w1);
-    load_x(j + NW, x1, wb);
-    compute(w0, x0, wa);
-    load_w(j + 2 * NW, w0);
-    load_x(j + 2 * NW, x0, wa);
-    compute(w1, x1, wb);
-  }
+    for (int q = 0; q < XR; ++q) {
+      const bool in = (slot(q) < sh.count) & (row[q] >= 0) & (row[q] < rr.x_rows);
+      xrow[q] = in ? (uint32_t)((int64_t)row[q] * K) * 2u : kOutside;
+    }
+    load_x(wave, x0, wa);
+    for (int j = wave; j < nwin; j += 2 * NW) {
+      load_w(j + NW, w1);
+      load_x(j + NW, x1, wb);
+      compute(w0, x0, wa);
+      load_w(j + 2 * NW, w0);
+      load_x(j + 2 * NW, x0, wa);
+      compute(w1, x1, wb);
+    }
 
-  __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
-  __syncthreads();
-  f32x4_t* red = reinterpret_cast<f32x4_t*>(w0);
-  static_assert(R * Q * 64 * 16 <= kW, "the sums fit one ring buffer");
+    __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more
+    __syncthreads();
+    f32x4_t* red = reinterpret_cast<f32x4_t*>(w0);
+    static_assert(R * Q * 64 * 16 <= kW, "the sums fit one ring buffer");
 #pragma unroll
-  for (int t = 0; t < R; ++t)
+    for (int t = 0; t < R; ++t)
 #pragma unroll
-    for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
-  __syncthreads();
-  finish<R, Q, GATED, NW>(red, sh, n0, N, y);
+      for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
+    __syncthreads();
+    finish<R, Q, GATED, NW>(red, sh, n0, N, y);
+    if constexpr (!Finder<RR>::kWalks) return;
+    __syncthreads();   // the sums have been read
+  }
 }
 
 template <int R, int Q, bool GATED, bool ACT8, bool XL, int NW>
@@ -236,7 +242,7 @@ hipError_t launch_grouped(const ExpertsCall& c, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
-  const int64_t ntiles = (c.w.n + 31) / 32, grid = routed_grid(r, ntiles);
+  const int64_t ntiles = (c.w.n + 31) / 32, grid = routed_grid(r, ntiles, 2);
   if (!grid_fits(grid, 256)) return hipErrorNotSupported;
   return with_routed(r, [&](auto rr) {
     hipLaunchKernelGGL((k_experts_fp8<4, 1, true, false, false, 4, decltype(rr)>), dim3((unsigned)grid), dim3(256), 0, s, c.w,

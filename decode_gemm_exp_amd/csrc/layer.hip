@@ -5,17 +5,22 @@
 //
 // A stream over the rows of D of every expert that has tokens.  A block owns 16 / P
 // output features and walks all those experts, so the weighted sum ends in one
-// block and needs neither partial sums in memory nor a third launch.  Its waves cut
-// the list of (expert, window of k) into contiguous runs; a window is a few MFMAs
-// with the weights as A (16 features) and h as B (16 tokens), whose sum is
-// weighted per token and added to the wave's.  A token without the expert keeps its
-// sum: its column could hold an infinity's product with zero.  The waves' sums meet
-// in LDS and are added in a fixed order.
+// block and needs neither partial sums in memory nor a third launch.  An item is an
+// expert and up to C of its tokens; the waves cut the list of (item, window of k)
+// into contiguous runs.  A window is a few MFMAs with the weights as A and h as B; at
+// the end of an item (or of a run) a wave adds its tokens' sums, weighted, to sums of
+// its own in LDS, and the waves' are added in a fixed order at last.
 //
-// P > 1, few tokens and few features: the sixteen rows of an MFMA are 16 / P
-// features at P places of k, the columns 16 / P tokens at the same P places.  Where
-// the two places agree D holds a product, elsewhere nothing that is used.  Blocks
-// are then P times as many, each with P times as much of k in a window.
+// Rows and columns of an MFMA are used to the full:
+//   P > 1: its sixteen rows are 16 / P features at P places of k, its columns 16 / P
+//     at the same P places.  Where the two places agree D holds a product, elsewhere
+//     nothing that is used.  Blocks are P times as many: 2048 features are 128 tiles
+//     of sixteen, half the CUs (16 tokens over 64 experts 1408x2048, P = 1 / 2: BF16 93 / 55 us, FP8
+//     60 / 38; MXFP4 over 160 experts 66 / 38).
+//   C < 16 / P: few tokens have an expert in common, and the columns behind the C-th of a
+//     place would hold nothing.  A load of h then fetches the pieces of 16 / (P C)
+//     MFMAs at once, one in each run of C columns, and each MFMA but the first moves
+//     its pieces to the first run.
 #include "experts_rows.h"
 #include "fp8.h"
 
@@ -23,6 +28,7 @@ namespace uw {
 namespace {
 
 constexpr int kNW = 8, kNT = 64 * kNW;
+
 
 struct LayerDown {
   ExpertsView d;
@@ -33,17 +39,10 @@ struct LayerDown {
   int tokens, topk;
 };
 
-// The pairs by expert: number of experts with pairs, which, and per expert and
-// token its slot (-1: none) and weight.
-struct PairsLds {
-  int32_t by_slot[kLayerPairs], index[kLayerPairs];
-  int32_t expert[kLayerPairs];
-  int16_t slot[kLayerPairs][kLayerTokens];
-  float weight[kLayerPairs][kLayerTokens];
-};
-
+// returns the number of items
+template <int C>
 __device__ __forceinline__ int sort_pairs(const LayerDown& c, PairsLds& s) {
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pairs = c.tokens * c.topk;
+  const int tid = threadIdx.x, pairs = c.tokens * c.topk;
   int id = -1, slot = -1;
   float w = 0.0f;
   if (tid < pairs) {
@@ -51,38 +50,22 @@ __device__ __forceinline__ int sort_pairs(const LayerDown& c, PairsLds& s) {
     slot = c.slots[tid];
     w = c.weights[tid];
   }
-  if (tid < kLayerPairs) s.by_slot[tid] = -1;
-  static_assert(sizeof(s.slot) == 16 * kNT, "one store a thread");
-  reinterpret_cast<uint4*>(s.slot)[tid] = make_uint4(~0u, ~0u, ~0u, ~0u);
-  __syncthreads();
-  if (slot >= 0) s.by_slot[slot] = id;
-  __syncthreads();
-  int experts = 0;   // with pairs; every wave counts them all, the first four write
-#pragma unroll
-  for (int i = 0; i < kLayerPairs / 64; ++i) {
-    const int at = 64 * i + lane, e = s.by_slot[at];
-    const bool first = e >= 0 && (at == 0 || s.by_slot[at == 0 ? 0 : at - 1] != e);
-    const uint64_t mask = __ballot(first);
-    const int mine = experts + __popcll(mask & ((2ull << lane) - 1ull)) - 1;
-    if (wave == i) {
-      s.index[at] = mine;
-      if (first) s.expert[mine] = e;
-    }
-    experts += __popcll(mask);
-  }
+  if (tid < kLayerPairs) s.expert[tid] = -1;
   __syncthreads();
   if (slot >= 0) {
-    const int i = s.index[slot], t = tid / c.topk;
-    s.slot[i][t] = (int16_t)slot;
-    s.weight[i][t] = w;
+    s.expert[slot] = id;
+    s.token[slot] = tid / c.topk;
+    s.weight[slot] = w;
   }
   __syncthreads();
-  return experts;
+  return list_items<C>(s);
 }
 
 // k of a window, and the eight k of an MFMA in lane group g from the window's start
 template <int FORM> constexpr int kWindow = FORM == kFormMx4 ? 256 : 128;
 template <int FORM> constexpr int kMfmas = kWindow<FORM> / 32;
+// windows a wave has on their way
+template <int FORM> constexpr int kDepth = FORM == kFormMx4 ? 4 : 3;
 template <int FORM>
 __device__ __forceinline__ int down_k(int m, int g) {
   if constexpr (FORM == kFormMx4) return 128 * (m >> 2) + 32 * g + 8 * (m & 3);
@@ -90,25 +73,37 @@ __device__ __forceinline__ int down_k(int m, int g) {
   else return k_off<FORM>(m, g);
 }
 
-template <int FORM, int P>
+// lane i takes lane i + N's (within sixteen)
+template <int N>
+__device__ __forceinline__ uint4 from_right(const uint4& v) {
+  auto move = [](uint32_t x) __attribute__((always_inline)) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x100 + N, 0xF, 0xF, true);
+  };
+  return make_uint4(move(v.x), move(v.y), move(v.z), move(v.w));
+}
+
+template <int FORM, int P, int C>
 __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
-  constexpr int kRows = 16 / P, kTokens = 16 / P, W = kWindow<FORM>, M = kMfmas<FORM>;
+  constexpr int kRows = 16 / P, X = kRows / C;   // X: MFMAs whose pieces of h one load fetches
+  constexpr int W = kWindow<FORM>, M = kMfmas<FORM>;
+  static_assert(M % X == 0, "loads of h are whole");
   __shared__ PairsLds pairs;
-  __shared__ f32x4_t red[kNW * 64];
-  const int experts = sort_pairs(c, pairs);
+  __shared__ float sums[kNW][P][kLayerTokens][kRows];
+  const int items = sort_pairs<C>(c, pairs);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int i16 = lane & 15, g = lane >> 4;
-  const int place = i16 / kRows, row = i16 % kRows, token = i16 % kTokens;
+  const int place = i16 / kRows, row = i16 % kRows, piece = row / C, token = row % C;
   const int64_t n0 = (int64_t)blockIdx.x * kRows, N = c.d.n;
   const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
   const int K = (int)c.d.k, nwin = (K + P * W - 1) / (P * W);
   const __amdgpu_buffer_rsrc_t rh = rsrc_of(c.h, (uint64_t)c.tokens * c.topk * 2 * (uint64_t)K);
+  for (int i = lane; i < P * kLayerTokens * kRows; i += 64) (&sums[wave][0][0][0])[i] = 0.0f;
 
-  const int total = __builtin_amdgcn_readfirstlane(experts) * nwin;
+  const int total = __builtin_amdgcn_readfirstlane(items) * nwin;
   const int begin = (int)((int64_t)total * wave / kNW), end = (int)((int64_t)total * (wave + 1) / kNW);
 
-  // The walk: expert `at` of the list, window `j`.  It runs ahead of the sums, past
-  // the end as well, where everything reads zeros.
+  // The walk: item `at`, window `j`.  It runs ahead of the sums, past the end as well,
+  // where everything reads zeros.
   struct Walk {
     int at, j, left;
   };
@@ -123,62 +118,118 @@ __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
     Raw r;
     PalView pal;
     uint32_t sc[2];    // MXFP4: two blocks' scale bytes; FP8: the block's scale
-    uint4 xv[M];
-    float weight;
-    bool has;
+    uint4 xv[M / X];
+    float weight;      // of the item's token in this lane's column
+    int to;            // that token, -1: none
+    bool ends;         // the item's last window, or the run's
   };
   Walk wl{begin / nwin, begin % nwin, end - begin}, wf = wl;
-  Flags fa[3];
+  constexpr int D = kDepth<FORM>;
+  Flags fl[D];
 
   // UWF1: the flag and rank words, a window ahead of its data
   auto flags = [&](Flags& f) __attribute__((always_inline)) {
     if constexpr (form_is_pal(FORM)) {
-      const int e = __builtin_amdgcn_readfirstlane(pairs.expert[wf.left > 0 ? wf.at : 0]);
+      const int e = __builtin_amdgcn_readfirstlane(pairs.item_expert[wf.left > 0 ? wf.at : 0]);
       const Mat<FORM> m = matrix_of<FORM>(c.d, e, n0, kRows);
       load_flags(m, row, K, wf.left > 0 ? P * W * wf.j + W * place + k_off<FORM>(0, g) : K, f);
       next(wf);
     }
   };
+  // A lane's offsets in its matrix, scales and row of h for window 0; the window goes by
+  // the loads' scalar offset.  The last window may pass K and has offsets of its own.
+  constexpr int NW_ = FORM == kFormBf16 ? 4 : 2, NX = M / X;
+  uint32_t wo[2][NW_], so[2][2], xo[2][NX];
+  const int last = P * W * (nwin - 1);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int end_k = t ? K - last : W * P;   // from the window's start
+    auto at = [&](int k, uint32_t off) __attribute__((always_inline)) { return k < end_k ? off : kOutside; };
+    const int kp = W * place, st = (int)mx4_scale_stride(K);
+#pragma unroll
+    for (int i = 0; i < NW_; ++i) {
+      const int k = kp + (FORM == kFormBf16 ? 32 * i + 8 * g : FORM == kFormFp8 ? 64 * i + 16 * g : 128 * i + 32 * g);
+      wo[t][i] = at(k, FORM == kFormBf16 ? (uint32_t)(row * K + k) * 2u
+                                         : FORM == kFormFp8 ? (uint32_t)(row * K + k) : (uint32_t)(row * (K / 2) + k / 2));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      so[t][i] = FORM == kFormFp8 ? at(kp, 4u * place) : at(kp + 128 * i + 32 * g, (uint32_t)(row * st + (kp + 128 * i + 32 * g) / 32));
+#pragma unroll
+    for (int l = 0; l < NX; ++l) {
+      int k = kp + down_k<FORM>(X * l, g);
+#pragma unroll
+      for (int x = 1; x < X; ++x) k = piece == x ? kp + down_k<FORM>(X * l + x, g) : k;
+      xo[t][l] = at(k, 2u * (uint32_t)k);
+    }
+  }
+  // the item that is being loaded
+  __amdgpu_buffer_rsrc_t rw = rh, rs = rh;
+  uint32_t hrow = kOutside;
+  float weight = 0.0f;
+  int to = -1, loaded = -1;      // the token of this lane's column, -1: none
+  // what LDS says of the next one, read an item ahead
+  int next_e = 0, next_slot = 0, next_end = 0;
+  auto look = [&](int item) __attribute__((always_inline)) {
+    next_e = pairs.item_expert[item];
+    next_slot = pairs.item_first[item] + token;
+    next_end = pairs.item_first[item + 1];
+  };
   auto load = [&](const Flags& f, Win& w) __attribute__((always_inline)) {
     const bool in = wl.left > 0;
-    const int at = in ? wl.at : 0, e = __builtin_amdgcn_readfirstlane(pairs.expert[at]);
-    const int slot = token < c.tokens ? pairs.slot[at][token] : -1;
-    w.weight = pairs.weight[at][token];
-    w.has = in && slot >= 0;
-    const int k0 = in ? P * W * wl.j + W * place : K;
-    if constexpr (FORM == kFormBf16 || form_is_pal(FORM)) {
-      const Mat<FORM> m = matrix_of<FORM>(c.d, e, n0, kRows);
-      load_raw(m, row, K, k0, g, f, w.r);
-      if constexpr (form_is_pal(FORM)) w.pal = m.t.pal;
-    } else if constexpr (FORM == kFormFp8) {
-      const __amdgpu_buffer_rsrc_t rw = rsrc_of(c.d.w + (int64_t)e * c.d.w_stride + n0 * K, (uint64_t)(rows * K));
-      const int nb = (int)fp8_blocks(K);
-      const __amdgpu_buffer_rsrc_t rs =
-          rsrc_of(c.d.scale + (int64_t)e * c.d.scale_stride + (n0 >> 7) * nb * 4, (uint64_t)nb * 4);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = k0 + 64 * i + 16 * g;
-        w.r.d[i] = bload16(rw, k < K ? (uint32_t)(row * K + k) : kOutside);
-      }
-      w.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, k0 < K ? (k0 >> 7) * 4 : (int)kOutside, 0, 0);
-    } else {
-      const int st = (int)mx4_scale_stride(K);
-      const __amdgpu_buffer_rsrc_t rw =
-          rsrc_of(c.d.w + (int64_t)e * c.d.w_stride + n0 * (K / 2), (uint64_t)(rows * (K / 2)));
-      const __amdgpu_buffer_rsrc_t rs =
-          rsrc_of(c.d.scale + (int64_t)e * c.d.scale_stride + n0 * st, (uint64_t)(rows * st));
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int k = k0 + 128 * i + 32 * g;
-        w.r.d[i] = bload16(rw, k < K ? (uint32_t)(row * (K / 2) + k / 2) : kOutside);
-        w.sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, k < K ? (int)(row * st + k / 32) : (int)kOutside, 0, 0);
+    if (in && wl.at != loaded) {
+      loaded = wl.at;
+      const int e = __builtin_amdgcn_readfirstlane(next_e);
+      const bool has = next_slot < next_end;   // (slots up to the next item's first are the item's)
+      hrow = has ? (uint32_t)next_slot * 2u * (uint32_t)K : kOutside;
+      weight = pairs.weight[has ? next_slot : 0];
+      to = has ? pairs.token[next_slot] : -1;
+      look(loaded + 1);
+      const uint8_t* base = c.d.w + (int64_t)e * c.d.w_stride;
+      if constexpr (FORM == kFormBf16) {
+        rw = rsrc_of(base + n0 * 2 * K, (uint64_t)(rows * 2 * K));
+      } else if constexpr (FORM == kFormFp8) {
+        const int nb = (int)fp8_blocks(K);
+        rw = rsrc_of(base + n0 * K, (uint64_t)(rows * K));
+        rs = rsrc_of(c.d.scale + (int64_t)e * c.d.scale_stride + (n0 >> 7) * nb * 4, (uint64_t)nb * 4);
+      } else if constexpr (FORM == kFormMx4) {
+        const int st = (int)mx4_scale_stride(K);
+        rw = rsrc_of(base + n0 * (K / 2), (uint64_t)(rows * (K / 2)));
+        rs = rsrc_of(c.d.scale + (int64_t)e * c.d.scale_stride + n0 * st, (uint64_t)(rows * st));
       }
     }
-    const uint32_t hrow = slot >= 0 ? (uint32_t)slot * 2u * (uint32_t)K : kOutside;
+    w.weight = weight;
+    w.to = to;
+    w.ends = in && (wl.j == nwin - 1 || wl.left == 1);
+    const bool tail = wl.j == nwin - 1;
+    const int k0 = P * W * wl.j;
+    auto pick = [&](uint32_t most, uint32_t end) __attribute__((always_inline)) {
+      return (int)(in ? tail ? end : most : kOutside);
+    };
+    if constexpr (form_is_pal(FORM)) {
+      const int e = __builtin_amdgcn_readfirstlane(pairs.item_expert[loaded]);
+      const Mat<FORM> m = matrix_of<FORM>(c.d, e, n0, kRows);
+      load_raw(m, row, K, in ? k0 + W * place : K, g, f, w.r);
+      w.pal = m.t.pal;
+    } else {
 #pragma unroll
-    for (int m = 0; m < M; ++m) {
-      const int k = k0 + down_k<FORM>(m, g);
-      w.xv[m] = bload16(rh, k < K ? hrow + 2u * (uint32_t)k : kOutside);
+      for (int i = 0; i < NW_; ++i) {
+        const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(
+            rw, pick(wo[0][i], wo[1][i]), FORM == kFormBf16 ? 2 * k0 : FORM == kFormFp8 ? k0 : k0 / 2, 0);
+        w.r.d[i] = make_uint4(v.x, v.y, v.z, v.w);
+      }
+      if constexpr (FORM == kFormFp8)
+        w.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, pick(so[0][0], so[1][0]), k0 / 32, 0);
+      if constexpr (FORM == kFormMx4) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          w.sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, pick(so[0][i], so[1][i]), k0 / 32, 0);
+      }
+    }
+#pragma unroll
+    for (int l = 0; l < NX; ++l) {
+      const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)hrow + pick(xo[0][l], xo[1][l]), 2 * k0, 0);
+      w.xv[l] = make_uint4(v.x, v.y, v.z, v.w);
     }
     next(wl);
   };
@@ -186,6 +237,7 @@ __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   auto compute = [&](const Win& w) __attribute__((always_inline)) {
     f32x4_t part = {0.f, 0.f, 0.f, 0.f};
+    if constexpr (FORM != kFormFp8) part = acc;
 #pragma unroll
     for (int m = 0; m < M; ++m) {
       bf16x8_t a;
@@ -199,14 +251,15 @@ __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
         mt.t.pal = w.pal;
         a = a_frag(mt, w.r, m);
       }
-      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, w.xv[m]), part, 0, 0, 0);
-    }
-    float scale = w.weight;
-    if constexpr (FORM == kFormFp8) {
-      scale = __builtin_bit_cast(float, w.sc[0]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) part[i] *= scale;
-      scale = w.weight;
+      uint4 b = w.xv[m / X];
+      if constexpr (X > 1) {
+        if (m % X == 1) b = from_right<C>(b);
+        if constexpr (X > 2) {
+          if (m % X == 2) b = from_right<2 * C>(b);
+          if (m % X == 3) b = from_right<3 * C>(b);
+        }
+      }
+      part = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, b), part, 0, 0, 0);
     }
     if constexpr (FORM == kFormMx4) {   // a NaN scale makes its row NaN: one more MFMA, NaN times zero
       const bool nan = (w.sc[0] & 255u) == 255u || (w.sc[1] & 255u) == 255u;
@@ -216,61 +269,81 @@ __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
                                                        __builtin_bit_cast(bf16x8_t, make_uint4(0u, 0u, 0u, 0u)), part, 0, 0, 0);
       }
     }
+    if constexpr (FORM == kFormFp8) {
+      const float scale = __builtin_bit_cast(float, w.sc[0]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = w.has ? __builtin_fmaf(part[i], scale, acc[i]) : acc[i];
+      for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(part[i], scale, acc[i]);
+    } else {
+      acc = part;
+    }
+    if (w.ends) {
+      // D: lane l holds rows 4 (l / 16) .. +3 of column l % 16
+      if (piece == 0 && 4 * g / kRows == place && w.to >= 0) {
+        f32x4_t* to = reinterpret_cast<f32x4_t*>(&sums[wave][place][w.to][4 * g % kRows]);
+        f32x4_t s = *to;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[i] = __builtin_fmaf(acc[i], w.weight, s[i]);
+        *to = s;
+      }
+      acc = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
   };
 
   if (end > begin) {
-    Win wa, wb, wc;
-    flags(fa[0]);
-    flags(fa[1]);
-    load(fa[0], wa);
-    flags(fa[2]);
-    load(fa[1], wb);
-    flags(fa[0]);
-    for (int i = begin; i < end; i += 3) {
-      load(fa[2], wc);
-      flags(fa[1]);
-      compute(wa);
-      load(fa[0], wa);
-      flags(fa[2]);
-      compute(wb);
-      load(fa[1], wb);
-      flags(fa[0]);
-      compute(wc);
+    look(wl.at);
+    // D sets of registers in turn: a set's load is D - 1 windows ahead of its sums, its
+    // flags a window ahead of its load
+    Win w[D];
+    flags(fl[0]);
+#pragma unroll
+    for (int d = 0; d < D - 1; ++d) {
+      flags(fl[d + 1]);
+      load(fl[d], w[d]);
+    }
+    for (int i = begin; i < end; i += D) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) {
+        flags(fl[d]);
+        load(fl[(d + D - 1) % D], w[(d + D - 1) % D]);
+        __builtin_amdgcn_sched_barrier(0);   // (before the wait for the oldest)
+        compute(w[d]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
   }
-  red[wave * 64 + lane] = acc;
   __syncthreads();
-  // D: lane l holds rows 4 (l / 16) .. +3 of column l % 16
-  const float* r = reinterpret_cast<const float*>(red);
   for (int i = threadIdx.x; i < kRows * c.tokens; i += kNT) {
     const int t = i / kRows, f = i % kRows;
     if (f >= rows) continue;
     float s = 0.0f;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const int dr = p * kRows + f, at = ((dr >> 2) * 16 + p * kTokens + t) * 4 + (dr & 3);
+    for (int v = 0; v < kNW; ++v)
 #pragma unroll
-      for (int v = 0; v < kNW; ++v) s += r[v * 256 + at];
-    }
+      for (int p = 0; p < P; ++p) s += sums[v][p][t][f];
     c.out[(int64_t)t * N + n0 + f] = (uint16_t)bf16_pair(s, s);
   }
 }
 
-template <int FORM, int P>
-hipError_t launch_p(const LayerDown& c, hipStream_t s) {
+template <int FORM, int P, int C>
+hipError_t launch_one(const LayerDown& c, hipStream_t s) {
   const int64_t grid = (c.d.n + 16 / P - 1) / (16 / P);   // (n is at most 2^20)
-  hipLaunchKernelGGL((k_layer_down<FORM, P>), dim3((unsigned)grid), dim3(kNT), 0, s, c);
+  hipLaunchKernelGGL((k_layer_down<FORM, P, C>), dim3((unsigned)grid), dim3(kNT), 0, s, c);
   return hipGetLastError();
 }
 
+// Places until every CU has a block; columns for the tokens that an expert has, about twice their
+// average so that hardly any expert is two items.
 template <int FORM>
 hipError_t launch_form(const LayerDown& c, hipStream_t s) {
   const int64_t cus = device_cus();
-  if (c.d.n / 16 >= cus || c.tokens > 8) return launch_p<FORM, 1>(c, s);
-  if (c.d.n / 8 >= cus || c.tokens > 4) return launch_p<FORM, 2>(c, s);
-  return launch_p<FORM, 4>(c, s);
+  const int pairs = c.tokens * c.topk, most = c.tokens < (2 * pairs + c.d.count - 1) / c.d.count + 1
+                                                  ? c.tokens
+                                                  : (2 * pairs + c.d.count - 1) / c.d.count + 1;
+  if (c.d.n / 16 >= cus || most > 8)
+    return most > 4 ? launch_one<FORM, 1, 16>(c, s) : launch_one<FORM, 1, 4>(c, s);
+  if (c.d.n / 8 >= cus || most > 4)
+    return most > 4 ? launch_one<FORM, 2, 8>(c, s) : most > 2 ? launch_one<FORM, 2, 4>(c, s) : launch_one<FORM, 2, 2>(c, s);
+  return launch_one<FORM, 4, 4>(c, s);
 }
 
 }  // namespace

@@ -2,6 +2,8 @@
 // layer kernels that route for themselves (see route.hip for what it computes).
 #pragma once
 
+#include <type_traits>
+
 #include "experts.h"
 
 namespace uw {
@@ -54,12 +56,11 @@ __device__ __forceinline__ float logit_at(const RouteCall& c, int64_t at) {
                 : static_cast<const float*>(c.logits)[at];
 }
 
-// One token on L lanes (l: this lane's place): lane j < topk returns choice j
-// (-1: none) and, with WEIGHTS, its weight.  live: the token exists.
-template <int L, int NV, bool WEIGHTS = true>
-__device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live, int l, int& id, float& weight) {
-  float v[NV];
-  uint32_t key[NV];
+// A token's logits v and keys on L lanes (l: this lane's place), expert i L + l in
+// place i; live: the token exists.
+template <int L, int NV>
+__device__ __forceinline__ void load_keys(const RouteCall& c, int64_t t, bool live, int l, float (&v)[NV],
+                                          uint32_t (&key)[NV]) {
   // all loads first, absent keys' from the row's first place (a load under a
   // condition waits for itself: twelve in a row took most of the kernel's time)
   const int64_t row = (live ? t : 0) * c.ld;
@@ -90,8 +91,16 @@ __device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live,
       key[i] = in ? order_key(1.0f / (1.0f + expf(-v[i])) + bias[i]) : 0u;
     }
   }
+}
+
+// One token on L lanes: lane j < topk returns choice j (-1: none) and its weight.
+template <int L, int NV>
+__device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live, int l, int& id, float& weight) {
+  float v[NV];
+  uint32_t key[NV];
+  load_keys<L, NV>(c, t, live, l, v, key);
   float top = -__builtin_inff(), sum = 0.0f;
-  if (WEIGHTS && c.scoring == 0) {
+  if (c.scoring == 0) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) top = fmaxf(top, key[i] ? v[i] : -__builtin_inff());
     top = group_max<L>(top);
@@ -115,7 +124,6 @@ __device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live,
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = e == (uint32_t)(i * L + l) ? 0u : key[i];
   }
-  if constexpr (!WEIGHTS) return;
   float mine = -__builtin_inff();   // lane j: the logit of choice j
   if (id >= 0) mine = logit_at(c, t * c.ld + id);
   const bool chosen = id >= 0;
@@ -137,6 +145,46 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
+// The same choice on a whole wave, without weights, of Q tokens t, t + 4, .. at once: the
+// largest key goes through scalar registers, and ballots find the lowest index that
+// has it, so a round is one chain of row maxima instead of two butterflies, and
+// the tokens' chains run beside each other.
+template <int NV, int Q>
+__device__ __forceinline__ void choose_wave(const RouteCall& c, int t, int (&id)[Q]) {
+  const int lane = threadIdx.x & 63;
+  float v[Q][NV];
+  uint32_t key[Q][NV];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    load_keys<64, NV>(c, t + 4 * q, t + 4 * q < c.tokens, lane, v[q], key[q]);
+    id[q] = -1;
+  }
+  for (int j = 0; j < c.topk; ++j) {
+    uint32_t best[Q];
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      best[q] = key[q][0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) best[q] = max(best[q], key[q][i]);
+      butterfly<16>([&](auto from) { best[q] = max(best[q], from(best[q])); });
+    }
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      auto row = [&](int r) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_readlane((int)best[q], 16 * r); };
+      const uint32_t most = max(max(row(0), row(1)), max(row(2), row(3)));
+      int e = -1;   // stays so when nothing is left
+#pragma unroll
+      for (int i = NV - 1; i >= 0; --i) {
+        const uint64_t has = __ballot(key[q][i] == most);
+        e = has && most ? 64 * i + __ffsll((unsigned long long)has) - 1 : e;
+      }
+      id[q] = lane == j ? e : id[q];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[q][i] = e == 64 * i + lane ? 0u : key[q][i];
+    }
+  }
+}
+
 // ---- a few tokens, routed by every block for itself ----------------------------
 // kLayerTokens tokens at most.  Each block makes the choice anew (a microsecond, while a launch
 // of its own and the wait for it cost several) and finds its expert's rows in it;
@@ -148,103 +196,138 @@ struct RoutedRows {
   int64_t slots, x_rows;
 };
 
-struct RoutedLds {
-  int32_t pair[kLayerPairs];          // a pair's expert, -1: none
-  uint32_t has[kMaxExperts / 32];     // experts that have pairs, a bit each
-  int32_t tok[4][kLayerTokens];       // per wave: tokens of its block's expert
+// The pairs by expert, and the items they make: an expert and up to C of its tokens.
+struct PairsLds {
+  int32_t expert[kLayerPairs];                       // by slot, -1 behind the last
+  int32_t token[kLayerPairs];
+  float weight[kLayerPairs];                         // (where they are needed)
+  int32_t item_expert[kLayerPairs + 1];              // (one more, and of the first slots, for reading ahead)
+  int32_t item_first[kLayerPairs + 2];               // its first slot; behind the last item the number of slots
 };
 
-// The choice of every token, into s; WRITE: ids and weights to memory as well.
-template <int L, int NV, bool WRITE>
-__device__ __forceinline__ void route_few(const RouteCall& c, RoutedLds& s) {
-  const int l = threadIdx.x % L, group = threadIdx.x / L, tokens = (int)c.tokens;
-  if (threadIdx.x < kMaxExperts / 32) s.has[threadIdx.x] = 0u;
-  s.pair[threadIdx.x] = -1;
+// The items of the slots in s, which the block's threads have written; returns their
+// number.  Every wave counts them all, the first four write.
+template <int C>
+__device__ __forceinline__ int list_items(PairsLds& s) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int e[kLayerPairs / 64], prev[kLayerPairs / 64];
+#pragma unroll
+  for (int i = 0; i < kLayerPairs / 64; ++i) {
+    const int at = 64 * i + lane;
+    e[i] = s.expert[at];
+    prev[i] = s.expert[at ? at - 1 : 0];
+  }
+  const uint64_t upto = (2ull << lane) - 1ull;   // lanes up to this one
+  int items = 0, slots = 0, start = 0;           // start: the first slot of the expert before
+#pragma unroll
+  for (int i = 0; i < kLayerPairs / 64; ++i) {
+    const int at = 64 * i + lane;
+    const uint64_t starts = __ballot(e[i] >= 0 && (at == 0 || e[i] != prev[i]));
+    const int from = (starts & upto) ? 64 * i + 63 - __builtin_clzll(starts & upto) : start;
+    const bool first = e[i] >= 0 && (at - from) % C == 0;
+    const uint64_t mask = __ballot(first);
+    if (wave == i && first) {
+      const int mine = items + __popcll(mask & upto) - 1;
+      s.item_expert[mine] = e[i];
+      s.item_first[mine] = at;
+    }
+    items += __popcll(mask);
+    slots += __popcll(__ballot(e[i] >= 0));
+    start = starts ? 64 * i + 63 - __builtin_clzll(starts) : start;
+  }
+  if (threadIdx.x == 0) s.item_first[items] = slots;
   __syncthreads();
-  for (int t = group; t - group < tokens; t += 256 / L) {
-    const bool live = t < tokens;
-    if (__ballot(live) == 0) break;
-    int id;
-    float w = 0.0f;
-    choose<L, NV, WRITE>(c, t, live, l, id, w);
-    if (live && l < c.topk) {
-      s.pair[t * c.topk + l] = id;
-      if (id >= 0) atomicOr(&s.has[id >> 5], 1u << (id & 31));   // (bits: the order does not matter)
-      if constexpr (WRITE) {
+  return items;
+}
+
+struct RoutedLds {
+  __attribute__((aligned(16))) int32_t pair[kLayerPairs];   // a pair's expert, -1: none
+  PairsLds p;
+};
+
+// The choice of every token, sorted by expert, into s; returns the number of experts
+// with pairs.  A pair's slot is the number of pairs before it, by expert, then by pair.
+// WRITE: ids, weights and the plan to memory as well.
+template <int L, int NV, bool WRITE>
+__device__ __forceinline__ int route_few(const RouteCall& c, RoutedLds& s) {
+  const int p = threadIdx.x, tokens = (int)c.tokens;
+  s.pair[p] = s.p.expert[p] = -1;
+  __syncthreads();
+  if constexpr (WRITE) {
+    const int l = threadIdx.x % L, group = threadIdx.x / L;
+    for (int t = group; t - group < tokens; t += 256 / L) {
+      const bool live = t < tokens;
+      if (__ballot(live) == 0) break;
+      int id;
+      float w;
+      choose<L, NV>(c, t, live, l, id, w);
+      if (live && l < c.topk) {
+        s.pair[t * c.topk + l] = id;
         c.ids[t * c.topk + l] = id;
         c.weights[t * c.topk + l] = w;
       }
     }
+  } else {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    auto few = [&](auto Q) __attribute__((always_inline)) {
+      int id[decltype(Q)::value];
+      choose_wave<L * NV / 64>(c, wave, id);
+#pragma unroll
+      for (int q = 0; q < decltype(Q)::value; ++q)
+        if (lane < c.topk && wave + 4 * q < tokens) s.pair[(wave + 4 * q) * c.topk + lane] = id[q];
+    };
+    static_assert(kLayerTokens == 16, "four tokens a wave");
+    if (tokens > 4) few(std::integral_constant<int, 4>{});
+    else few(std::integral_constant<int, 1>{});
   }
   __syncthreads();
+  const int pairs = tokens * c.topk, e = s.pair[p];
+  const int4* four = reinterpret_cast<const int4*>(s.pair);
+  auto before = [](int f, int q, int x, int at) __attribute__((always_inline)) {   // pair q of expert f before pair at of x
+    return f >= 0 && (f < x || (f == x && q < at)) ? 1 : 0;
+  };
+  auto count = [&](int x, int at) __attribute__((always_inline)) {
+    int n = 0;
+#pragma unroll 4
+    for (int q = 0; q < pairs; q += 4) {
+      const int4 f = four[q / 4];   // (behind the last pair: -1)
+      n += before(f.x, q, x, at) + before(f.y, q + 1, x, at) + before(f.z, q + 2, x, at) + before(f.w, q + 3, x, at);
+    }
+    return n;
+  };
+  if (e >= 0) {
+    const int slot = count(e, p), t = p / c.topk;
+    s.p.expert[slot] = e;
+    s.p.token[slot] = t;
+    if constexpr (WRITE) {
+      c.slots[p] = slot;
+      c.rows[slot] = t;
+    }
+  } else if (WRITE && p < pairs) {
+    c.slots[p] = -1;
+  }
+  if constexpr (WRITE) {
+    for (int x = p; x <= c.experts; x += 256) c.offsets[x] = count(x, 0);
+  }
+  __syncthreads();
+  return list_items<kLayerTokens>(s.p);
 }
 
 // The kernel for a layer's number of experts: lanes a token times keys a lane.
 template <typename F>
 hipError_t with_routed(const RouteCall& c, F&& f) {
   if (c.experts <= 64) return f(RoutedRows<16, 4>{c, c.tokens * c.topk, c.tokens});
+  if (c.experts <= 128) return f(RoutedRows<16, 8>{c, c.tokens * c.topk, c.tokens});
+  if (c.experts <= 192) return f(RoutedRows<16, 12>{c, c.tokens * c.topk, c.tokens});
   if (c.experts <= 256) return f(RoutedRows<16, 16>{c, c.tokens * c.topk, c.tokens});
   return f(RoutedRows<64, 16>{c, c.tokens * c.topk, c.tokens});
 }
-// Blocks: the plan's, then `ntiles` for every expert that can have pairs.
-inline int64_t routed_grid(const RouteCall& c, int64_t ntiles) {
-  const int64_t pairs = c.tokens * c.topk;
-  return 1 + ntiles * (pairs < c.experts ? pairs : c.experts);
-}
-
-// The plan of the choice in s.  A pair's slot is the number of pairs before it, by
-// expert, then by pair.
-__device__ __forceinline__ void plan_few(const RouteCall& c, const RoutedLds& s) {
-  const int pairs = (int)c.tokens * c.topk, p = threadIdx.x, e = s.pair[p];
-  if (p < pairs) {
-    int slot = 0;
-    for (int q = 0; q < pairs; ++q) {
-      const int f = s.pair[q];
-      slot += f >= 0 && (f < e || (f == e && q < p)) ? 1 : 0;
-    }
-    c.slots[p] = e >= 0 ? slot : -1;
-    if (e >= 0) c.rows[slot] = p / c.topk;
-  }
-  for (int x = p; x <= c.experts; x += 256) {
-    int n = 0;
-    for (int q = 0; q < pairs; ++q) n += s.pair[q] >= 0 && s.pair[q] < x ? 1 : 0;
-    c.offsets[x] = n;
-  }
-}
-
-// The share of the chunk-th expert that has pairs, by index; count 0: there are not
-// that many.  Its tokens in the order of their slots go to s.tok[wave].
-__device__ __forceinline__ Share share_few(const RouteCall& c, RoutedLds& s, int chunk) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const uint32_t word = lane < kMaxExperts / 32 ? s.has[lane] : 0u;
-  const int mine = __popc(word);
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < kMaxExperts / 32; d <<= 1) {
-    const int up = __shfl_up(upto, d);
-    upto += lane >= d ? up : 0;
-  }
-  Share out{0, 0, 0};
-  const uint64_t hit = __ballot(chunk >= upto - mine && chunk < upto);
-  if (hit == 0) return out;
-  const int src = __ffsll((unsigned long long)hit) - 1;
-  uint32_t bits = (uint32_t)__builtin_amdgcn_readlane((int)word, src);
-  for (int i = chunk - __builtin_amdgcn_readlane(upto - mine, src); i > 0; --i) bits &= bits - 1u;
-  const int e = 32 * src + __ffs((int)bits) - 1;
-  out.expert = e;
-  int first = 0, count = 0;
-#pragma unroll
-  for (int i = 0; i < kLayerPairs / 64; ++i) {
-    const int p = 64 * i + lane, f = s.pair[p];
-    const uint64_t eq = __ballot(f == e);
-    first += __popcll(__ballot(f >= 0 && f < e));
-    if (f == e) s.tok[wave][count + __popcll(eq & ((1ull << lane) - 1ull))] = p / c.topk;
-    count += __popcll(eq);
-  }
-  out.first = first;
-  out.count = count;   // at most one pair a token
-  wave_fence();
-  return out;
+// Blocks: the plan's, then one for each of `ntiles` tiles of every expert that can have
+// pairs, or as many as a CU holds at once (`resident`) on every CU.
+inline int64_t routed_grid(const RouteCall& c, int64_t ntiles, int resident) {
+  const int64_t pairs = c.tokens * c.topk, tiles = ntiles * (pairs < c.experts ? pairs : c.experts);
+  const int64_t most = (int64_t)device_cus() * resident;
+  return 1 + (tiles < most ? tiles : most);
 }
 
 }  // namespace
