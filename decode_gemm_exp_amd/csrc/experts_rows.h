@@ -143,6 +143,7 @@ struct Finder<RaggedRows> {
   static constexpr bool kWalks = false;
   struct Lds {};
   // false: the block has nothing (more) to do
+  template <int NW>
   __device__ __forceinline__ bool begin(const RaggedRows&, Lds&) { return true; }
   __device__ __forceinline__ bool find(const RaggedRows& rr, Lds&, int, unsigned ntiles, unsigned chunks, int experts,
                                        int most, unsigned& tile, Share& sh) const {
@@ -169,12 +170,13 @@ struct Finder<RoutedRows<L, NV>> {
   static constexpr bool kWalks = true;
   using Lds = RoutedLds;
   int items;
+  template <int NW>
   __device__ __forceinline__ bool begin(const RoutedRows<L, NV>& rr, Lds& lds) {
     if (blockIdx.x == 0) {
-      route_few<L, NV, true>(rr.c, lds);
+      write_few<L, NV, NW>(rr.c, lds);
       return false;
     }
-    items = __builtin_amdgcn_readfirstlane(route_few<L, NV, false>(rr.c, lds));
+    items = __builtin_amdgcn_readfirstlane(route_few<L, NV, NW>(rr.c, lds));
     return true;
   }
   // the block's turn-th tile
@@ -183,15 +185,16 @@ struct Finder<RoutedRows<L, NV>> {
     const unsigned at = blockIdx.x - 1 + (unsigned)turn * (gridDim.x - 1), item = at / ntiles;
     if (item >= (unsigned)items) return false;
     tile = at - item * ntiles;
-    sh.expert = __builtin_amdgcn_readfirstlane(lds.p.item_expert[item]);
-    sh.first = __builtin_amdgcn_readfirstlane(lds.p.item_first[item]);
-    sh.count = __builtin_amdgcn_readfirstlane(lds.p.item_first[item + 1]) - (int)sh.first;
+    sh.expert = __builtin_amdgcn_readfirstlane(lds.expert[item]);
+    sh.first = __builtin_amdgcn_readfirstlane(lds.first[item]);
+    sh.count = __builtin_amdgcn_readfirstlane(lds.first[item + 1]) - (int)sh.first;
     return true;
   }
   template <int N, typename F>
   __device__ __forceinline__ void rows(const RoutedRows<L, NV>&, const Lds& lds, const Share& sh, int32_t (&row)[N], F&& slot) const {
+    const uint32_t tokens = lds.tokens[sh.expert];
 #pragma unroll
-    for (int q = 0; q < N; ++q) row[q] = lds.p.token[sh.first + (slot(q) < sh.count ? slot(q) : 0)];
+    for (int q = 0; q < N; ++q) row[q] = nth_bit(tokens, slot(q) < sh.count ? slot(q) : 0);
   }
 };
 

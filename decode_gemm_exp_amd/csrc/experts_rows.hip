@@ -33,7 +33,7 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
   __shared__ f32x4_t red[4 * R * Q * 64];
   __shared__ typename Finder<RR>::Lds found;
   Finder<RR> finder;
-  if (!finder.begin(rr, found)) return;
+  if (!finder.template begin<4>(rr, found)) return;
   for (int turn = 0;; ++turn) {
     unsigned tile;
     Share sh;
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, Experts
   __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
   __shared__ typename Finder<RR>::Lds found;
   Finder<RR> finder;
-  if (!finder.begin(rr, found)) return;
+  if (!finder.template begin<NW>(rr, found)) return;
   for (int turn = 0;; ++turn) {
     unsigned tile;
     Share sh;

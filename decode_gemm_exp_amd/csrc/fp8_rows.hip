@@ -31,7 +31,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
   __shared__ __attribute__((aligned(128))) char x0[NW * kX], x1[NW * kX];
   __shared__ typename Finder<RR>::Lds found;
   Finder<RR> finder;
-  if (!finder.begin(rr, found)) return;
+  if (!finder.template begin<NW>(rr, found)) return;
   for (int turn = 0;; ++turn) {
     unsigned tile;
     Share sh;
@@ -241,12 +241,14 @@ hipError_t launch_grouped(const ExpertsCall& c, hipStream_t s) {
 
 }  // namespace
 
+// Sixteen outputs a block and eight waves, so that a token's few tiles are many blocks with all of a
+// wave's windows on their way at once.
 hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
-  const int64_t ntiles = (c.w.n + 31) / 32, grid = routed_grid(r, ntiles, 2);
-  if (!grid_fits(grid, 256)) return hipErrorNotSupported;
+  const int64_t ntiles = (c.w.n + 15) / 16, grid = routed_grid(r, ntiles, 2);
+  if (!grid_fits(grid, 512)) return hipErrorNotSupported;
   return with_routed(r, [&](auto rr) {
-    hipLaunchKernelGGL((k_experts_fp8<4, 1, true, false, false, 4, decltype(rr)>), dim3((unsigned)grid), dim3(256), 0, s, c.w,
-                       c.u, rr, c.x, c.y, (int)ntiles, 0);
+    hipLaunchKernelGGL((k_experts_fp8<2, 1, true, false, false, 8, decltype(rr)>), dim3((unsigned)grid), dim3(512), 0, s,
+                       c.w, c.u, rr, c.x, c.y, (int)ntiles, 0);
     return hipGetLastError();
   });
 }

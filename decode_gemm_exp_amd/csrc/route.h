@@ -145,18 +145,18 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The same choice on a whole wave, without weights, of Q tokens t, t + 4, .. at once: the
+// The same choice on a whole wave, without weights, of Q tokens t, t + NW, .. at once: the
 // largest key goes through scalar registers, and ballots find the lowest index that
 // has it, so a round is one chain of row maxima instead of two butterflies, and
 // the tokens' chains run beside each other.
-template <int NV, int Q>
+template <int NV, int NW, int Q>
 __device__ __forceinline__ void choose_wave(const RouteCall& c, int t, int (&id)[Q]) {
   const int lane = threadIdx.x & 63;
   float v[Q][NV];
   uint32_t key[Q][NV];
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    load_keys<64, NV>(c, t + 4 * q, t + 4 * q < c.tokens, lane, v[q], key[q]);
+    load_keys<64, NV>(c, t + NW * q, t + NW * q < c.tokens, lane, v[q], key[q]);
     id[q] = -1;
   }
   for (int j = 0; j < c.topk; ++j) {
@@ -186,8 +186,8 @@ __device__ __forceinline__ void choose_wave(const RouteCall& c, int t, int (&id)
 }
 
 // ---- a few tokens, routed by every block for itself ----------------------------
-// kLayerTokens tokens at most.  Each block makes the choice anew (a microsecond, while a launch
-// of its own and the wait for it cost several) and finds its expert's rows in it;
+// kLayerTokens tokens at most.  Each block makes the choice anew (a microsecond or two, while a
+// launch of its own and the wait for it cost several) and finds its experts' rows in it;
 // block 0 writes the plan, the same that uw_route_experts writes, and nothing else.
 template <int L, int NV>
 struct RoutedRows {
@@ -240,77 +240,126 @@ __device__ __forceinline__ int list_items(PairsLds& s) {
   return items;
 }
 
+// What a block of the gated product knows of the choice: the experts that have pairs, by
+// index, each with its tokens as bits and its first slot.
 struct RoutedLds {
-  __attribute__((aligned(16))) int32_t pair[kLayerPairs];   // a pair's expert, -1: none
-  PairsLds p;
+  uint32_t tokens[kMaxExperts];
+  int32_t expert[kLayerPairs + 1];
+  int32_t first[kLayerPairs + 1];
 };
 
-// The choice of every token, sorted by expert, into s; returns the number of experts
-// with pairs.  A pair's slot is the number of pairs before it, by expert, then by pair.
-// WRITE: ids, weights and the plan to memory as well.
-template <int L, int NV, bool WRITE>
+// The choice of every token by a block of NW waves; returns the number of experts with
+// pairs.  A pair's slot is the number of pairs before it, by expert, then by token.
+template <int L, int NV, int NW>
 __device__ __forceinline__ int route_few(const RouteCall& c, RoutedLds& s) {
-  const int p = threadIdx.x, tokens = (int)c.tokens;
-  s.pair[p] = s.p.expert[p] = -1;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int tokens = (int)c.tokens;
+  for (int i = threadIdx.x; i < c.experts; i += 64 * NW) s.tokens[i] = 0u;
+  auto few = [&](auto Q) __attribute__((always_inline)) {
+    int id[decltype(Q)::value];
+    choose_wave<L * NV / 64, NW>(c, wave, id);
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < decltype(Q)::value; ++q)
+      if (id[q] >= 0) atomicOr(&s.tokens[id[q]], 1u << (wave + NW * q));   // (bits: their order does not matter)
+  };
+  if (tokens > NW) few(std::integral_constant<int, kLayerTokens / NW>{});
+  else few(std::integral_constant<int, 1>{});
   __syncthreads();
-  if constexpr (WRITE) {
-    const int l = threadIdx.x % L, group = threadIdx.x / L;
-    for (int t = group; t - group < tokens; t += 256 / L) {
-      const bool live = t < tokens;
-      if (__ballot(live) == 0) break;
-      int id;
-      float w;
-      choose<L, NV>(c, t, live, l, id, w);
-      if (live && l < c.topk) {
-        s.pair[t * c.topk + l] = id;
-        c.ids[t * c.topk + l] = id;
-        c.weights[t * c.topk + l] = w;
+  // every wave by itself: four experts a lane, 256 at a time
+  int items = 0, slots = 0;
+  for (int e0 = 0; e0 < c.experts; e0 += 256) {
+    uint32_t t[4];
+    int n = 0;   // pairs, and experts that have some in the upper half
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = e0 + 4 * lane + i;
+      t[i] = e < c.experts ? s.tokens[e] : 0u;
+      n += __popc(t[i]) + (t[i] ? 1 << 16 : 0);
+    }
+    int upto = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int up = __shfl_up(upto, d);
+      upto += lane >= d ? up : 0;
+    }
+    if (wave == 0) {
+      int slot = slots + ((upto - n) & 0xFFFF), item = items + ((upto - n) >> 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (t[i]) {
+          s.expert[item] = e0 + 4 * lane + i;
+          s.first[item++] = slot;
+        }
+        slot += __popc(t[i]);
       }
     }
-  } else {
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    auto few = [&](auto Q) __attribute__((always_inline)) {
-      int id[decltype(Q)::value];
-      choose_wave<L * NV / 64>(c, wave, id);
-#pragma unroll
-      for (int q = 0; q < decltype(Q)::value; ++q)
-        if (lane < c.topk && wave + 4 * q < tokens) s.pair[(wave + 4 * q) * c.topk + lane] = id[q];
-    };
-    static_assert(kLayerTokens == 16, "four tokens a wave");
-    if (tokens > 4) few(std::integral_constant<int, 4>{});
-    else few(std::integral_constant<int, 1>{});
+    const int all = __builtin_amdgcn_readlane(upto, 63);
+    slots += all & 0xFFFF;
+    items += all >> 16;
   }
+  if (threadIdx.x == 0) s.first[items] = slots;
   __syncthreads();
-  const int pairs = tokens * c.topk, e = s.pair[p];
-  const int4* four = reinterpret_cast<const int4*>(s.pair);
-  auto before = [](int f, int q, int x, int at) __attribute__((always_inline)) {   // pair q of expert f before pair at of x
-    return f >= 0 && (f < x || (f == x && q < at)) ? 1 : 0;
-  };
-  auto count = [&](int x, int at) __attribute__((always_inline)) {
-    int n = 0;
-#pragma unroll 4
-    for (int q = 0; q < pairs; q += 4) {
-      const int4 f = four[q / 4];   // (behind the last pair: -1)
-      n += before(f.x, q, x, at) + before(f.y, q + 1, x, at) + before(f.z, q + 2, x, at) + before(f.w, q + 3, x, at);
+  return items;
+}
+
+// The same choice with its weights and the plan, to memory, by one block.
+template <int L, int NV, int NW>
+__device__ __forceinline__ void write_few(const RouteCall& c, RoutedLds& s) {
+  const int l = threadIdx.x % L, group = threadIdx.x / L, tokens = (int)c.tokens;
+  for (int t = group; t - group < tokens; t += 64 * NW / L) {
+    const bool live = t < tokens;
+    if (__ballot(live) == 0) break;
+    int id;
+    float w;
+    choose<L, NV>(c, t, live, l, id, w);
+    if (live && l < c.topk) {
+      c.ids[t * c.topk + l] = id;
+      c.weights[t * c.topk + l] = w;
     }
-    return n;
-  };
-  if (e >= 0) {
-    const int slot = count(e, p), t = p / c.topk;
-    s.p.expert[slot] = e;
-    s.p.token[slot] = t;
-    if constexpr (WRITE) {
-      c.slots[p] = slot;
+  }
+  const int items = route_few<L, NV, NW>(c, s);
+  // which of a token's choices an expert is, the ids say, which this block has just written
+  __threadfence_block();
+  __syncthreads();
+  for (int p = threadIdx.x; p < tokens * c.topk; p += 64 * NW) {
+    const int id = c.ids[p], t = p / c.topk;
+    int slot = -1;
+    if (id >= 0) {
+      int lo = 0, hi = items - 1;   // the expert's item
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (s.expert[mid] < id) lo = mid + 1;
+        else hi = mid;
+      }
+      slot = s.first[lo] + __popc(s.tokens[id] & ((1u << t) - 1u));
       c.rows[slot] = t;
     }
-  } else if (WRITE && p < pairs) {
-    c.slots[p] = -1;
+    c.slots[p] = slot;
   }
-  if constexpr (WRITE) {
-    for (int x = p; x <= c.experts; x += 256) c.offsets[x] = count(x, 0);
+  for (int x = threadIdx.x; x <= c.experts; x += 64 * NW) {
+    int lo = 0, hi = items;   // the first item from expert x on
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (s.expert[mid] < x) lo = mid + 1;
+      else hi = mid;
+    }
+    c.offsets[x] = s.first[lo];
   }
-  __syncthreads();
-  return list_items<kLayerTokens>(s.p);
+}
+
+// the place of the n-th set bit (n below their number) of sixteen
+__device__ __forceinline__ int nth_bit(uint32_t bits, int n) {
+  int at = 0;
+#pragma unroll
+  for (int w = 8; w >= 1; w >>= 1) {
+    const int low = __popc(bits & ((1u << w) - 1u));
+    const bool up = n >= low;
+    n -= up ? low : 0;
+    bits = up ? bits >> w : bits;
+    at += up ? w : 0;
+  }
+  return at;
 }
 
 // The kernel for a layer's number of experts: lanes a token times keys a lane.
