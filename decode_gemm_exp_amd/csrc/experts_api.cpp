@@ -120,6 +120,17 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
 // rows and moves with the blocks that the tiles make.
 constexpr int64_t kMx4RowsMax = 8;
 
+// A product with an FP8 matrix: its arguments but for pointers, and how it will run.
+uw_status check_fp8(int64_t n, int64_t k, int64_t batch, uw_activation act, Fp8Plan& p) {
+  if (batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_FP8)) return UW_ERR_INVALID;
+  const uw_status st = check_shape(n, k);
+  if (st != UW_OK) return st;
+  // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
+  if (batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512)) return UW_ERR_UNSUPPORTED;
+  p = plan_fp8(n, k, batch, act == UW_ACT_FP8);
+  return UW_OK;
+}
+
 uw_status check_route(int64_t tokens, int32_t experts, int32_t topk) {
   if (tokens < 0 || experts <= 0 || topk <= 0 || topk > experts) return UW_ERR_INVALID;
   if (experts > kMaxExperts || topk > kMaxTopk || tokens > INT32_MAX / topk) return UW_ERR_UNSUPPORTED;
@@ -276,27 +287,24 @@ uw_status uw_dequantize_fp8(const uint8_t* elem_dev, const float* scale_dev, int
 }
 
 uw_status uw_workspace_size_fp8(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes) {
-  if (!bytes || batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_FP8)) return UW_ERR_INVALID;
-  const uw_status st = check_shape(n, k);
-  if (st != UW_OK) return st;
-  // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
-  if (batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512)) return UW_ERR_UNSUPPORTED;
-  const Fp8Plan p = plan_fp8(n, k, batch, act == UW_ACT_FP8);
-  *bytes = p.x_bytes + p.scale_bytes + p.part_bytes;
-  return UW_OK;
+  if (!bytes) return UW_ERR_INVALID;
+  Fp8Plan p;
+  const uw_status st = check_fp8(n, k, batch, act, p);
+  if (st == UW_OK) *bytes = p.bytes();
+  return st;
 }
 
 uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t n, int64_t k, const uint16_t* x_dev,
                         int64_t batch, float* y_dev, uw_activation act, void* ws_dev, size_t ws_bytes, void* stream) {
   if (batch == 0) return UW_OK;
   if (!elem_dev || !scale_dev || !x_dev || !y_dev) return UW_ERR_INVALID;
-  size_t need = 0;
-  const uw_status st = uw_workspace_size_fp8(n, k, batch, act, &need);
+  Fp8Plan p;
+  const uw_status st = check_fp8(n, k, batch, act, p);
   if (st != UW_OK) return st;
   if (!aligned(elem_dev, 16) || !aligned(scale_dev, 4) || !aligned(x_dev, 16) || !aligned(y_dev, 16) ||
       !aligned(ws_dev, 16))
     return UW_ERR_INVALID;
-  if (need && (!ws_dev || ws_bytes < need)) return UW_ERR_WORKSPACE;
+  if (p.bytes() && (!ws_dev || ws_bytes < p.bytes())) return UW_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   ExpertsCall c{};
   c.w.form = kFormFp8;
@@ -309,7 +317,7 @@ uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t
   c.r = RaggedRows{nullptr, nullptr, batch, batch};
   c.x = x_dev;
   c.y = y_dev;
-  return status_of(launch_fp8_product(c, act == UW_ACT_FP8, ws_dev, s));
+  return status_of(launch_fp8_product(c, p, act == UW_ACT_FP8, ws_dev, s));
 }
 
 uw_status uw_experts_fp8(const uint8_t* elem_dev, const float* scale_dev, int32_t count, int64_t n, int64_t k,

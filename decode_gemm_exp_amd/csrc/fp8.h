@@ -94,9 +94,10 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s);
 struct Fp8Plan {
   bool few;           // launch_fp8_rows
   Fp8Tile tile;       // (pointers not set)
-  uint64_t x_bytes, scale_bytes, part_bytes;
+  uint64_t x_bytes, scale_bytes, part_bytes;   // of the workspace, in this order
+  uint64_t bytes() const { return x_bytes + scale_bytes + part_bytes; }
 };
 Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8);
-hipError_t launch_fp8_product(const ExpertsCall& c, bool act8, void* ws, hipStream_t s);
+hipError_t launch_fp8_product(const ExpertsCall& c, const Fp8Plan& p, bool act8, void* ws, hipStream_t s);
 
 }  // namespace uw

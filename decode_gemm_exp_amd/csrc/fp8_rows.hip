@@ -239,18 +239,25 @@ hipError_t launch_grouped(const ExpertsCall& c, hipStream_t s) {
   return launch_one<4, 2, GATED, false, false, 4>(c, s);
 }
 
-}  // namespace
-
-// Sixteen outputs a block and eight waves, so that a token's few tiles are many blocks with all of a
-// wave's windows on their way at once.
-hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
-  const int64_t ntiles = (c.w.n + 15) / 16, grid = routed_grid(r, ntiles, 2);
-  if (!grid_fits(grid, 512)) return hipErrorNotSupported;
+template <int R, int NW>
+hipError_t launch_routed(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
+  const int64_t ntiles = (c.w.n + 8 * R - 1) / (8 * R), grid = routed_grid(r, ntiles, 2);
+  if (!grid_fits(grid, 64 * NW)) return hipErrorNotSupported;
   return with_routed(r, [&](auto rr) {
-    hipLaunchKernelGGL((k_experts_fp8<2, 1, true, false, false, 8, decltype(rr)>), dim3((unsigned)grid), dim3(512), 0, s,
-                       c.w, c.u, rr, c.x, c.y, (int)ntiles, 0);
+    hipLaunchKernelGGL((k_experts_fp8<R, 1, true, false, false, NW, decltype(rr)>), dim3((unsigned)grid), dim3(64 * NW),
+                       0, s, c.w, c.u, rr, c.x, c.y, (int)ntiles, 0);
     return hipGetLastError();
   });
+}
+
+}  // namespace
+
+// 32 outputs a tile, or where that makes fewer tiles than blocks fit the chip 16 and eight waves, so
+// that all of a wave's windows are on their way at once (64 experts 1408x2048, us: 16 tokens 63 / 67).
+hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
+  const int64_t pairs = r.tokens * r.topk;
+  if ((c.w.n + 31) / 32 * (pairs < r.experts ? pairs : r.experts) < 2 * device_cus()) return launch_routed<2, 8>(c, r, s);
+  return launch_routed<4, 4>(c, r, s);
 }
 
 hipError_t launch_fp8_rows(const ExpertsCall& c, bool act8, hipStream_t s) {
@@ -265,8 +272,7 @@ namespace {
 //   tiles  rounds of one block a CU, each its steps of 128 k and three more, at 1.15 (64 rows) or
 //          1.55 (128 rows);
 //   rows   3 and the weights once per group of rows.
-double tile_us(int64_t blocks, int64_t steps, int rows) {
-  const int64_t cus = device_cus();
+double tile_us(int64_t blocks, int64_t steps, int rows, int64_t cus) {
   return (double)((blocks + cus - 1) / cus * (steps + 3)) * (rows == 64 ? 1.15 : 1.55);
 }
 
@@ -289,7 +295,8 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
   if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_fp8_tile(c, Fp8Tile{128, spread, 1, nullptr, nullptr}, s);
   const double weights = (c.gated ? 2.0 : 1.0) * (double)c.w.n * (double)c.w.k * 1e-6;
   const int64_t steps = fp8_blocks(c.w.k);
-  const double t64 = tile_us(ntiles * chunks(64), steps, 64), t128 = tile_us(ntiles * chunks(128), steps, 128);
+  const int64_t cus = device_cus();
+  const double t64 = tile_us(ntiles * chunks(64), steps, 64, cus), t128 = tile_us(ntiles * chunks(128), steps, 128, cus);
   const double least = (double)with_rows * weights / 4.7, best = t64 < t128 ? t64 : t128;
   if (3 + (double)chunks(avg > 12 ? 32 : 16) * weights / 5 < (best > least ? best : least))
     return launch_fp8_rows(c, false, s);
@@ -309,7 +316,7 @@ Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   for (int rows = big ? 128 : 64; rows <= 128; rows *= 2)
     for (int splits = 1; splits <= 16 && (splits == 1 || steps >= 2 * splits); ++splits) {
       const int64_t blocks = (batch + rows - 1) / rows * ((n + 255) / 256) * splits;
-      double us = tile_us(blocks, (steps + splits - 1) / splits, rows);
+      double us = tile_us(blocks, (steps + splits - 1) / splits, rows, cus);
       if (us < weights / 2.5) us = weights / 2.5;
       if (splits > 1) us += 6.5 + (double)splits * (double)batch * (double)n * 8e-6 / 5.3;
       if (best == 0 || us < best) {
@@ -331,8 +338,7 @@ Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   return p;
 }
 
-hipError_t launch_fp8_product(const ExpertsCall& c, bool act8, void* ws, hipStream_t s) {
-  const Fp8Plan p = plan_fp8(c.w.n, c.w.k, c.r.slots, act8);
+hipError_t launch_fp8_product(const ExpertsCall& c, const Fp8Plan& p, bool act8, void* ws, hipStream_t s) {
   if (p.few) return launch_fp8_rows(c, act8, s);
   char* const at = static_cast<char*>(ws);
   ExpertsCall call = c;

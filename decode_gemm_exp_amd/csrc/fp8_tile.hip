@@ -51,12 +51,14 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   constexpr int TM = BM / 64;                 // 32-slot tiles of a wave; two column tiles
   constexpr int OUT = GATED ? 128 : 256;      // output columns of a block
   constexpr int XP = BM / 32, WP = 4, P = XP + WP;   // pieces a thread moves per step
-  constexpr int S = BM == 64 ? 3 : 2;         // buffers: as many as fit
+  // buffers of x and of weights: as many as fit, the weights', which come from memory,
+  // first (1024 rows of 28672x8192, 128-row tiles, two of each / three of weights: 500 / XXX us)
+  constexpr int SX = BM == 64 ? 3 : 2, SW = 3;
   constexpr int kX = BM * 256, kW = kBN * 128;
   // objects of their own rather than parts of one, so that the compiler sees that
   // what is read from one does not wait for what travels into another
-  __shared__ __attribute__((aligned(256))) char x0[kX], x1[kX], w0[kW], w1[kW];
-  __shared__ __attribute__((aligned(256))) char x2[S > 2 ? kX : 16], w2[S > 2 ? kW : 16];
+  __shared__ __attribute__((aligned(256))) char x0[kX], x1[kX], w0[kW], w1[kW], w2[kW];
+  __shared__ __attribute__((aligned(16))) char x2[SX > 2 ? kX : 16];   // (16 bytes are never touched and take no space)
   char* const xbufs[3] = {x0, x1, x2};
   char* const wbufs[3] = {w0, w1, w2};
 
@@ -179,13 +181,13 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
     for (int r = 0; r < 16; ++r) acc[i][j][r] = __builtin_fmaf(part[i][j][r], s, acc[i][j][r]);
   };
 
-  // Step s finds its data in buffers J % S; the sums of the step before, scaled by
+  // Step s finds its data in buffers J % SX and J % SW; the sums of the step before, scaled by
   // sc[(J + 1) % 2], are added on the way.  TA: the wave's slot tiles that hold slots
   // (0: it moves data for the others).
   auto step = [&](int s, auto J, auto TA) __attribute__((always_inline)) {
     constexpr int j = decltype(J)::value, ta = decltype(TA)::value;
-    char* const xcur = xbufs[j % S];
-    char* const wcur = wbufs[j % S];
+    char* const xcur = xbufs[j % SX];
+    char* const wcur = wbufs[j % SW];
     if constexpr (ta > 0) {
 #pragma unroll
       for (int t = 0; t < 7; ++t) {
@@ -208,7 +210,6 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
               part[i][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[c], fx[t & 1][i], part[i][c], 0, 0, 0);
             }
           }
-        if (t == 0) load_scales(s + 1, sc[(j + 1) % 2]);
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -219,29 +220,33 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
     }
     // This thread's part of step s + 1 has landed, and this wave has read all
     // of step s: after the barrier both hold for the block.  What may still
-    // travel, all issued after s + 1's pieces: those of the S - 2 later steps
-    // (the scale loads among them only make the wait stricter).
-    __builtin_amdgcn_s_waitcnt(0x70 | (P * (S - 2)));   // vmcnt, lgkmcnt 0
+    // travel, all issued after s + 1's x: with as many buffers of both the pieces of
+    // s + 2, with one more of weights the weights of s + 2.  (Scales are loaded before
+    // a step's pieces, so that wherever they end up they only make the wait stricter.)
+    constexpr int kLater = SX == SW ? P : WP;
+    static_assert(SX == SW ? SX == 3 : SX == 2 && SW == 3, "what is issued when");
+    __builtin_amdgcn_s_waitcnt(0x70 | kLater);   // vmcnt kLater, lgkmcnt 0
     bare_barrier();
     bf16x8_t fl[TM];
     if constexpr (ta > 0) {
 #pragma unroll
       for (int i = 0; i < ta; ++i) fl[i] = fx[1][i];
-      read_x(xbufs[(j + 1) % S], 0, 0, TA);
-      read_w(wbufs[(j + 1) % S], 0, 0);
+      read_x(xbufs[(j + 1) % SX], 0, 0, TA);
+      read_w(wbufs[(j + 1) % SW], 0, 0);
+      load_scales(s + 1, sc[(j + 1) % 2]);
       __builtin_amdgcn_sched_barrier(0);
     }
     // the pieces that refill this step's buffers, some behind each MFMA
     constexpr int kMma = 2 * ta, kPer = kMma ? (P + kMma - 1) / kMma : P;
-    const int k0 = kStep * block_of(s + S);
+    const int kx = kStep * block_of(s + SX), kw = kStep * block_of(s + SW);
 #pragma unroll
     for (int m = 0; m < (kMma ? kMma : 1); ++m) {
       if constexpr (ta > 0)
         part[m / 2][m % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m % 2], fl[m / 2], part[m / 2][m % 2], 0, 0, 0);
 #pragma unroll
       for (int i = m * kPer; i < (m + 1) * kPer; ++i) {
-        if (i < XP) direct_x(k0, xcur, i);
-        else if (i < P) direct_w(k0, wcur, i - XP);
+        if (i < XP) direct_x(kx, xcur, i);
+        else if (i < P) direct_w(kw, wcur, i - XP);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
@@ -303,7 +308,7 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
     }
     // whole rounds of buffers and register sets, then what is left; what the last
     // steps fetch lies past K: zeros
-    constexpr int kRound = S == 2 ? 2 : 6;
+    constexpr int kRound = 6;   // a multiple of both numbers of buffers and of two
     auto steps_from = [&](int s, auto J, auto self) __attribute__((always_inline)) {
       step(s, J, TA);
       constexpr int j = decltype(J)::value + 1;
@@ -334,21 +339,30 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
     }
   };
 
-#pragma unroll
-  for (int b = 0; b < S; ++b) {
-    const int k0 = kStep * block_of(b);
-#pragma unroll
-    for (int i = 0; i < XP; ++i) direct_x(k0, xbufs[b], i);
-#pragma unroll
-    for (int i = 0; i < WP; ++i) direct_w(k0, wbufs[b], i);
-  }
   // before the first step there are no sums to add
   sc[1].w[0] = sc[1].w[1] = 0.0f;
 #pragma unroll
   for (int i = 0; i < TM; ++i) sc[0].x[i] = sc[1].x[i] = 0.0f;
   load_scales(0, sc[0]);
+  // the buffers' first filling, in the order in which the steps go on
+  auto fill_x = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < XP; ++i) direct_x(kStep * block_of(b), xbufs[b], i);
+  };
+  auto fill_w = [&](int b) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < WP; ++i) direct_w(kStep * block_of(b), wbufs[b], i);
+  };
+  if constexpr (SX != SW) fill_w(0);
+#pragma unroll
+  for (int b = 0; b < SX; ++b) {
+    fill_x(b);
+    fill_w(b + SW - SX);
+  }
   asm volatile("" : : "s"(y));   // its scalar load ends here: pending, it would make the loop's first LDS wait a full one
-  __builtin_amdgcn_s_waitcnt(0x70 | (P * (S - 1) < 16 ? P * (S - 1) : 15));   // step 0 has landed
+  constexpr int kAhead = SX == SW ? P * (SX - 1) : WP + P;   // what was sent after step 0's x
+  static_assert(kAhead < 16, "the counter's low field");
+  __builtin_amdgcn_s_waitcnt(0x70 | kAhead);   // step 0 has landed
   bare_barrier();
   // (a wave takes one of the loops as a whole; all pass the same barriers)
   if (sh.count > (TM > 1 ? 64 + 32 * wm : 32 * wm)) {
