@@ -81,8 +81,8 @@ hipError_t launch_round_fp8(const uint16_t* x, int64_t rows, int64_t cols, uint1
 struct Fp8Tile {
   int rows;           // of a tile: 64 or 128
   bool spread;
-  int splits;         // slices of K, summed by a second kernel (one matrix, plain)
-  float* part;        // [splits][slots][n], when there are several
+  int tail, splits;   // one matrix, plain: the last `tail` tiles' K goes in slices, summed by a second kernel
+  float* part;        // tail * splits tiles of rows * 256
   const float* act;   // x's scales when c.x holds E4M3 values as BF16
 };
 hipError_t launch_fp8_tile(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s);

@@ -292,7 +292,7 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
   };
   const bool spread = avg <= 96;
   // x past 2 GiB goes by pointers, in 128-row tiles
-  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_fp8_tile(c, Fp8Tile{128, spread, 1, nullptr, nullptr}, s);
+  if (c.r.x_rows * 2 * c.w.k > kOutside) return launch_fp8_tile(c, Fp8Tile{128, spread, 0, 1, nullptr, nullptr}, s);
   const double weights = (c.gated ? 2.0 : 1.0) * (double)c.w.n * (double)c.w.k * 1e-6;
   const int64_t steps = fp8_blocks(c.w.k);
   const int64_t cus = device_cus();
@@ -300,11 +300,11 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
   const double least = (double)with_rows * weights / 4.7, best = t64 < t128 ? t64 : t128;
   if (3 + (double)chunks(avg > 12 ? 32 : 16) * weights / 5 < (best > least ? best : least))
     return launch_fp8_rows(c, false, s);
-  return launch_fp8_tile(c, Fp8Tile{t64 < t128 ? 64 : 128, spread, 1, nullptr, nullptr}, s);
+  return launch_fp8_tile(c, Fp8Tile{t64 < t128 ? 64 : 128, spread, 0, 1, nullptr, nullptr}, s);
 }
 
-// One matrix.  The weights pass the tiles at 2.5 TB/s at most; K in slices costs 6.5 and the slices'
-// sums at 5.3 TB/s; the rows kernel takes the weights once per 16 rows at 7 TB/s, or per 32 at 6.2
+// One matrix.  The tiles of the last, partly filled round go in slices of K where that is faster: it
+// costs 6.5 and the slices' sums at 5.3 TB/s.  The weights pass the tiles at 2.5 TB/s at most; the rows kernel takes the weights once per 16 rows at 7 TB/s, or per 32 at 6.2
 // where that fills the chip.
 Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   auto pad = [](uint64_t b) { return (b + 255) / 256 * 256; };
@@ -313,17 +313,20 @@ Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   const int64_t cus = device_cus(), steps = fp8_blocks(k);
   const double weights = (double)n * (double)k * 1e-6;
   double best = 0;
-  for (int rows = big ? 128 : 64; rows <= 128; rows *= 2)
-    for (int splits = 1; splits <= 16 && (splits == 1 || steps >= 2 * splits); ++splits) {
-      const int64_t blocks = (batch + rows - 1) / rows * ((n + 255) / 256) * splits;
-      double us = tile_us(blocks, (steps + splits - 1) / splits, rows, cus);
+  for (int rows = big ? 128 : 64; rows <= 128; rows *= 2) {
+    const int64_t tiles = (batch + rows - 1) / rows * ((n + 255) / 256), tail = tiles % cus;
+    for (int splits = 1; splits <= 16 && (splits == 1 || (tail && steps >= 2 * splits)); ++splits) {
+      double us = tile_us(splits > 1 ? tiles - tail : tiles, steps, rows, cus);
+      if (splits > 1)
+        us += tile_us(tail * splits, (steps + splits - 1) / splits, rows, cus) + 6.5 +
+              (double)(tail * splits * rows) * 2048e-6 / 5.3;
       if (us < weights / 2.5) us = weights / 2.5;
-      if (splits > 1) us += 6.5 + (double)splits * (double)batch * (double)n * 8e-6 / 5.3;
       if (best == 0 || us < best) {
         best = us;
-        p.tile = Fp8Tile{rows, batch <= 96, splits, nullptr, nullptr};
+        p.tile = Fp8Tile{rows, batch <= 96, splits > 1 ? (int)tail : 0, splits, nullptr, nullptr};
       }
     }
+  }
   if (batch <= 256 && !big) {   // (beyond, x's share of the traffic would count)
     const double sixteens = (double)((batch + 15) / 16) * weights / 7, twos = (double)((batch + 31) / 32) * weights / 6.2;
     const bool fills = (n + 63) / 64 * ((batch + 31) / 32) >= cus;
@@ -334,7 +337,7 @@ Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
     p.x_bytes = pad(2 * (uint64_t)batch * (uint64_t)k);
     p.scale_bytes = pad(4 * (uint64_t)batch * (uint64_t)steps);
   }
-  if (p.tile.splits > 1) p.part_bytes = pad(4 * (uint64_t)p.tile.splits * (uint64_t)batch * (uint64_t)n);
+  p.part_bytes = pad((uint64_t)p.tile.tail * (uint64_t)p.tile.splits * (uint64_t)p.tile.rows * 1024);
   return p;
 }
 

@@ -40,10 +40,24 @@ __device__ __attribute__((aligned(16))) const uint32_t g_zero16[4] = {0, 0, 0, 0
 
 struct TileArgs {
   const float* act;   // x's scales, [rows][blocks of k] (ACT8)
-  int ntiles;
+  int ntiles;         // of columns
   int spread;         // blocks start along K at different places (see experts_tile.hip)
-  int splits;         // slices of K; slice i's sums go to y + i * slots * n (one matrix, plain)
+  // One matrix: the first `whole` tiles, then `tail` ones whose K goes in `splits` slices, a block
+  // each, to part + (tile * splits + slice) * BM * 256.
+  int whole, tail, splits;
+  float* part;
 };
+
+// Tile `at` of one matrix.
+template <int BM>
+__device__ __forceinline__ int one_tile(const RaggedRows& rr, int64_t at, int ntiles, Share& sh) {
+  int m, nt;
+  tile_of((uint32_t)at, (uint32_t)((rr.slots + BM - 1) / BM), (uint32_t)ntiles, m, nt);
+  sh.expert = 0;
+  sh.first = (int64_t)m * BM;
+  sh.count = (int)(rr.slots - sh.first < BM ? rr.slots - sh.first : BM);
+  return nt;
+}
 
 template <int BM, bool GATED, bool ACT8, bool BIG>
 __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu, RaggedRows rr,
@@ -62,15 +76,32 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   char* const xbufs[3] = {x0, x1, x2};
   char* const wbufs[3] = {w0, w1, w2};
 
+  // the block's tile, and its slice of K
   Share sh;
-  const int nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, args.ntiles, BM, sh);
-  if (nt < 0) return;
+  int nt, slice = 0, splits = 1, tail = 0;
+  if (rr.offsets) {
+    nt = find_tile(rr, vw.count, blockIdx.x & 7, blockIdx.x >> 3, args.ntiles, BM, sh);
+    if (nt < 0) return;
+  } else {   // the whole tiles dealt so that each XCD works on one contiguous run of them
+    const int share = (args.whole + 7) / 8, b = (int)blockIdx.x - 8 * share;
+    if (b < 0) {
+      const int at = ((int)blockIdx.x & 7) * share + ((int)blockIdx.x >> 3);
+      if (at >= args.whole) return;
+      nt = one_tile<BM>(rr, at, args.ntiles, sh);
+    } else {
+      tail = b / args.splits;
+      if (tail >= args.tail) return;
+      splits = args.splits;
+      slice = b - tail * splits;
+      nt = one_tile<BM>(rr, args.whole + tail, args.ntiles, sh);
+    }
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 2, wn = wave & 3, col = lane & 31, half = lane >> 5;
   // the slice's blocks of k: `steps` from `first` on
-  const int K = (int)vw.k, nk = (int)fp8_blocks(K), slice = (int)blockIdx.y;
-  const int first = (int)((int64_t)nk * slice / args.splits);
-  const int steps = (int)((int64_t)nk * (slice + 1) / args.splits) - first;
+  const int K = (int)vw.k, nk = (int)fp8_blocks(K);
+  const int first = (int)((int64_t)nk * slice / splits);
+  const int steps = (int)((int64_t)nk * (slice + 1) / splits) - first;
   const int64_t n0 = (int64_t)nt * OUT;
 
   // x: thread t's pieces are those at its place, piece t % 16 ^ t / 16 % 16 of rows t / 16 + 32 i
@@ -253,12 +284,15 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   };
   // D of the MFMA: lane l, register r: weight row 8 (r / 4) + 4 (l / 32) + r % 4, slot l % 32.
   // The tile's rows of y are one buffer resource: rows behind the last slot are
-  // dropped by its bound, as are columns past N, by an offset outside.
+  // dropped by its bound, as are columns past N, by an offset outside.  A slice's sums
+  // are a tile of their own, all 256 columns of it.
   auto write = [&](auto TA) __attribute__((always_inline)) {
     constexpr int kSize = GATED ? 2 : 4, kCols = GATED ? 1 : 2;
-    const __amdgpu_buffer_rsrc_t ry =
-        rsrc_of(static_cast<char*>(y) + (slice * rr.slots + sh.first) * vw.n * kSize, (uint64_t)sh.count * (uint64_t)vw.n * kSize);
-    const int N = (int)vw.n;
+    const bool sliced = !GATED && splits > 1;
+    const int N = sliced ? kBN : (int)vw.n, from = sliced ? 0 : (int)n0;
+    char* const base = sliced ? reinterpret_cast<char*>(args.part + (int64_t)(tail * splits + slice) * (BM * kBN))
+                              : static_cast<char*>(y) + sh.first * vw.n * kSize;
+    const __amdgpu_buffer_rsrc_t ry = rsrc_of(base, (uint64_t)sh.count * (uint64_t)N * kSize);
     const bool whole = N % 4 == 0;
 #pragma unroll
     for (int i = 0; i < decltype(TA)::value; ++i)
@@ -266,7 +300,7 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
       for (int j = 0; j < kCols; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int n = (int)n0 + (GATED ? wn * 32 : wn * 64 + 32 * j) + 8 * q + 4 * half;
+          const int n = from + (GATED ? wn * 32 : wn * 64 + 32 * j) + 8 * q + 4 * half;
           const uint32_t at = (uint32_t)((slot_of(i) + col) * N + n) * kSize;
           float v[4];
 #pragma unroll
@@ -375,38 +409,46 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
   __builtin_amdgcn_s_waitcnt(0);   // nothing travels to LDS any more when the block gives it back
 }
 
-// y[i] = the slices' sums in their order
-__global__ __launch_bounds__(256) void k_sum_slices(const float* __restrict__ part, int splits, int64_t count,
-                                                    float* __restrict__ y) {
-  const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-  if (i >= count) return;
-  if (i + 4 <= count && count % 4 == 0) {
-    f32x4_t s = *reinterpret_cast<const f32x4_t*>(part + i);
-    for (int v = 1; v < splits; ++v) s += *reinterpret_cast<const f32x4_t*>(part + v * count + i);
-    *reinterpret_cast<f32x4_t*>(y + i) = s;
-    return;
-  }
-  for (int64_t c = i; c < count && c < i + 4; ++c) {
-    float s = part[c];
-    for (int v = 1; v < splits; ++v) s += part[v * count + c];
-    y[c] = s;
+// The tail tiles' slices, summed in their order: a block sixteen rows of a tile, a thread four
+// columns of each fourth of them.
+template <int BM>
+__global__ __launch_bounds__(256) void k_sum_slices(RaggedRows rr, TileArgs args, int64_t N, float* __restrict__ y) {
+  const int tail = blockIdx.x / (BM / 16), r0 = 16 * (blockIdx.x % (BM / 16)) + (threadIdx.x >> 6);
+  Share sh;
+  const int nt = one_tile<BM>(rr, args.whole + tail, args.ntiles, sh);
+  const int c = 4 * (threadIdx.x & 63);
+  const int64_t n = (int64_t)nt * kBN + c;
+  const float* part = args.part + (int64_t)tail * args.splits * (BM * kBN) + c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * i;
+    if (r >= sh.count || n >= N) continue;
+    f32x4_t s = *reinterpret_cast<const f32x4_t*>(part + r * kBN);
+#pragma unroll 4
+    for (int v = 1; v < args.splits; ++v) s += *reinterpret_cast<const f32x4_t*>(part + (int64_t)v * (BM * kBN) + r * kBN);
+    float* o = y + (sh.first + r) * N + n;
+    if (N % 4 == 0) {
+      *reinterpret_cast<f32x4_t*>(o) = s;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (n + j < N) o[j] = s[j];
+    }
   }
 }
 
 template <int BM, bool GATED, bool ACT8, bool BIG = false>
 hipError_t launch_one(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s) {
   const int64_t out = GATED ? 128 : 256, ntiles = (c.w.n + out - 1) / out;
-  // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
   const int64_t tiles = max_chunks(c.r.slots, c.w.count, BM, c.r.offsets != nullptr) * ntiles;
-  const int64_t grid = (tiles + 7) / 8 * 8;
-  if (!grid_fits(grid * t.splits, kNT)) return hipErrorNotSupported;
-  const TileArgs a{t.act, (int)ntiles, (int)t.spread, t.splits};
-  hipLaunchKernelGGL((k_fp8_tile<BM, GATED, ACT8, BIG>), dim3((unsigned)grid, (unsigned)t.splits), dim3(kNT), 0, s, c.w,
-                     c.u, c.r, c.x, a, t.splits > 1 ? t.part : c.y);
+  // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
+  const int64_t grid = (tiles - t.tail + 7) / 8 * 8 + (int64_t)t.tail * t.splits;
+  if (!grid_fits(grid, kNT)) return hipErrorNotSupported;
+  const TileArgs a{t.act, (int)ntiles, (int)t.spread, (int)(tiles - t.tail), t.tail, t.splits, t.part};
+  hipLaunchKernelGGL((k_fp8_tile<BM, GATED, ACT8, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x, a, c.y);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || t.splits == 1) return e;
-  const int64_t count = c.r.slots * c.w.n;
-  hipLaunchKernelGGL(k_sum_slices, dim3((unsigned)((count + 1023) / 1024)), dim3(256), 0, s, t.part, t.splits, count,
+  if (e != hipSuccess || t.tail == 0) return e;
+  hipLaunchKernelGGL(k_sum_slices<BM>, dim3((unsigned)(t.tail * (BM / 16))), dim3(256), 0, s, c.r, a, c.w.n,
                      static_cast<float*>(c.y));
   return hipGetLastError();
 }
