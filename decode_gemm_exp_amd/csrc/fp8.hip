@@ -18,10 +18,12 @@ struct Eight {
 
 template <bool F32>
 __device__ __forceinline__ Eight<F32> load8(const void* src, int64_t at) {
-  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(src) + at * (F32 ? 4 : 2));
+  // (read once: kept out of the caches, 14336x4096 34.5 -> 30.5 us)
+  const u32x4_t* p = reinterpret_cast<const u32x4_t*>(static_cast<const char*>(src) + at * (F32 ? 4 : 2));
+  auto piece = [](const u32x4_t& v) __attribute__((always_inline)) { return make_uint4(v.x, v.y, v.z, v.w); };
   Eight<F32> e;
-  e.a = p[0];
-  if constexpr (F32) e.b = p[1];
+  e.a = piece(__builtin_nontemporal_load(p));
+  if constexpr (F32) e.b = piece(__builtin_nontemporal_load(p + 1));
   return e;
 }
 
@@ -110,40 +112,37 @@ __global__ __launch_bounds__(256) void k_quantize_fp8(const void* __restrict__ s
   }
 }
 
-// A block of threads takes 64 rows of 256 columns, a thread sixteen elements of every
-// sixteenth row.
+// A block of threads takes 64 rows of 256 columns, a thread eight elements of every
+// eighth row, so that a wave's stores are whole lines.
 __global__ __launch_bounds__(256) void k_dequantize_fp8(const uint8_t* __restrict__ elem,
                                                         const float* __restrict__ scale, int64_t rows, int64_t cols,
                                                         int block_rows, uint16_t* __restrict__ out, int64_t ld,
                                                         uint32_t nt) {
+  constexpr int U = 8;
   const uint32_t rt = blockIdx.x / nt, ct = blockIdx.x - rt * nt;
-  const int64_t col = (int64_t)ct * 256 + 16 * (threadIdx.x & 15), row0 = (int64_t)rt * 64 + (threadIdx.x >> 4);
+  const int64_t col = (int64_t)ct * 256 + 8 * (threadIdx.x & 31), row0 = (int64_t)rt * 64 + (threadIdx.x >> 5);
   if (col >= cols) return;
   const int64_t nb = fp8_blocks(cols);
-  uint4 q[4];
-  float f[4];
+  uint2 q[U];
+  float f[U];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int64_t row = row0 + 16 * u < rows ? row0 + 16 * u : rows - 1;
-    q[u] = *reinterpret_cast<const uint4*>(elem + row * cols + col);
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + 8 * u < rows ? row0 + 8 * u : rows - 1;
+    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(elem + row * cols + col);
+    q[u] = make_uint2(v.x, v.y);
     f[u] = scale[(block_rows == 1 ? row : row >> 7) * nb + (col >> 7)];
   }
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int64_t row = row0 + 16 * u;
+  for (int u = 0; u < U; ++u) {
+    const int64_t row = row0 + 8 * u;
     if (row >= rows) break;
-    const uint32_t w[4] = {q[u].x, q[u].y, q[u].z, q[u].w};
-    uint32_t o[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    auto two = [&](uint32_t w, bool hi) __attribute__((always_inline)) {
       typedef __attribute__((ext_vector_type(2))) float f2;
-      const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
-      o[2 * i] = bf16_pair(lo.x * f[u], lo.y * f[u]);
-      o[2 * i + 1] = bf16_pair(hi.x * f[u], hi.y * f[u]);
-    }
-    uint4* p = reinterpret_cast<uint4*>(out + row * ld + col);
-    p[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    p[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      const f2 v = hi ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+      return bf16_pair(v.x * f[u], v.y * f[u]);
+    };
+    *reinterpret_cast<uint4*>(out + row * ld + col) =
+        make_uint4(two(q[u].x, false), two(q[u].x, true), two(q[u].y, false), two(q[u].y, true));
   }
 }
 

@@ -212,7 +212,8 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   return hipGetLastError();
 }
 // One matrix: 64 rows of it a wave, or 32 and eight waves a block where that makes too
-// few blocks; x through LDS, like the weights, once its loads are many, or two groups of
+// few blocks, or 16 where those fit the chip at once (32 / 16 rows, us: 13 rows of 1000x16384 12.6 / 9.8, of
+// 4096x4096 6.5 / 5.7, of 5001x8224, 313 blocks of 16, 17.3 / 21.7); x through LDS, like the weights, once its loads are many, or two groups of
 // sixteen rows where the blocks still fill the chip.  Measured (us; 64 rows, 64 with x in LDS, 32
 // with eight waves, the same with x in LDS, two groups; x in BF16):
 //   14336x4096   1 row 14.4 / 15.6 / 14.2 / 15.8, 16 rows 15.3 / 16.0 / 17.5 / 17.5, 32 rows 21.5 / 22.2 / 26.8 / 26.7 / 19.2
@@ -227,6 +228,7 @@ hipError_t launch_matrix(const ExpertsCall& c, hipStream_t s) {
   if (blocks >= cus * 3 / 4)
     return rows > (ACT8 ? 8 : 15) ? launch_one<4, 1, false, ACT8, true, 4>(c, s)
                                   : launch_one<4, 1, false, ACT8, false, 4>(c, s);
+  if ((c.w.n + 15) / 16 * ((rows + 15) / 16) <= cus) return launch_one<1, 1, false, ACT8, true, 8>(c, s);
   return rows > 8 ? launch_one<2, 1, false, ACT8, true, 8>(c, s) : launch_one<2, 1, false, ACT8, false, 8>(c, s);
 }
 
