@@ -372,11 +372,13 @@ hipError_t with_routed(const RouteCall& c, F&& f) {
   return f(RoutedRows<64, 16>{c, c.tokens * c.topk, c.tokens});
 }
 // Blocks: the plan's, then one for each of `ntiles` tiles of every expert that can have
-// pairs, or as many as a CU holds at once (`resident`) on every CU.
+// pairs, or, where those are more than the CUs hold at once (`resident` each), as many as
+// take the same number of them in turn.  (us with 4 / 2 / 8 a CU / one a tile, BF16, 16 tokens, 64 experts
+// 1408x2048: 112 / 124 / 118 / 141; MXFP4, 160 experts, with 2 / one a tile: 56 / 97.)
 inline int64_t routed_grid(const RouteCall& c, int64_t ntiles, int resident) {
   const int64_t pairs = c.tokens * c.topk, tiles = ntiles * (pairs < c.experts ? pairs : c.experts);
-  const int64_t most = (int64_t)device_cus() * resident;
-  return 1 + (tiles < most ? tiles : most);
+  const int64_t most = (int64_t)device_cus() * resident, turns = (tiles + most - 1) / most;
+  return 1 + (tiles + turns - 1) / turns;
 }
 
 }  // namespace
