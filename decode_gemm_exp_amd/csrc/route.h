@@ -372,13 +372,14 @@ hipError_t with_routed(const RouteCall& c, F&& f) {
   return f(RoutedRows<64, 16>{c, c.tokens * c.topk, c.tokens});
 }
 // Blocks: the plan's, then one for each of `ntiles` tiles of every expert that can have
-// pairs, or, where those are more than the CUs hold at once (`resident` each), as many as
-// take the same number of them in turn.  (us with 4 / 2 / 8 a CU / one a tile, BF16, 16 tokens, 64 experts
-// 1408x2048: 112 / 124 / 118 / 141; MXFP4, 160 experts, with 2 / one a tile: 56 / 97.)
+// pairs, or `resident` on every CU where that is fewer.  (us with 4 / 2 / 8 a CU / one a tile, BF16, 16
+// tokens, 64 experts 1408x2048: 112 / 124 / 118 / 141; MXFP4, 160 experts, with 2 / one a tile: 56 / 97.  Fewer
+// blocks that all take the same number of tiles leave less on its way: one token, two of eight BF16
+// experts 14336x4096 133 -> 140, eight of 64 FP8 experts 20.1 -> 21.5 for the layer.)
 inline int64_t routed_grid(const RouteCall& c, int64_t ntiles, int resident) {
   const int64_t pairs = c.tokens * c.topk, tiles = ntiles * (pairs < c.experts ? pairs : c.experts);
-  const int64_t most = (int64_t)device_cus() * resident, turns = (tiles + most - 1) / most;
-  return 1 + (tiles + turns - 1) / turns;
+  const int64_t most = (int64_t)device_cus() * resident;
+  return 1 + (tiles < most ? tiles : most);
 }
 
 }  // namespace
