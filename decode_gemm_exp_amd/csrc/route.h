@@ -56,23 +56,31 @@ __device__ __forceinline__ float logit_at(const RouteCall& c, int64_t at) {
                 : static_cast<const float*>(c.logits)[at];
 }
 
-// A token's logits v and keys on L lanes (l: this lane's place), expert i L + l in
-// place i; live: the token exists.
-template <int L, int NV>
-__device__ __forceinline__ void load_keys(const RouteCall& c, int64_t t, bool live, int l, float (&v)[NV],
-                                          uint32_t (&key)[NV]) {
+// Q tokens t, t + step, .. on L lanes each (l: this lane's place): logits v and keys, expert
+// i L + l in place i; a token from `end` on has no keys.
+template <int L, int NV, int Q>
+__device__ __forceinline__ void load_keys(const RouteCall& c, int64_t t, int64_t step, int64_t end, int l,
+                                          float (&v)[Q][NV], uint32_t (&key)[Q][NV]) {
   // all loads first, absent keys' from the row's first place (a load under a
   // condition waits for itself: twelve in a row took most of the kernel's time)
-  const int64_t row = (live ? t : 0) * c.ld;
+  auto at = [&](int q, int i) __attribute__((always_inline)) {
+    return (t + q * step < end ? t + q * step : 0) * c.ld + (i * L + l < c.experts ? i * L + l : 0);
+  };
   if (c.bf16) {
-    uint16_t u[NV];
+    uint16_t u[Q][NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) u[i] = static_cast<const uint16_t*>(c.logits)[row + (i * L + l < c.experts ? i * L + l : 0)];
+    for (int q = 0; q < Q; ++q)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = __builtin_bit_cast(float, (uint32_t)u[i] << 16);
+      for (int i = 0; i < NV; ++i) u[q][i] = static_cast<const uint16_t*>(c.logits)[at(q, i)];
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[q][i] = __builtin_bit_cast(float, (uint32_t)u[q][i] << 16);
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] = static_cast<const float*>(c.logits)[row + (i * L + l < c.experts ? i * L + l : 0)];
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) v[q][i] = static_cast<const float*>(c.logits)[at(q, i)];
   }
   float bias[NV] = {};
   if (c.bias) {
@@ -80,25 +88,31 @@ __device__ __forceinline__ void load_keys(const RouteCall& c, int64_t t, bool li
     for (int i = 0; i < NV; ++i) bias[i] = c.bias[i * L + l < c.experts ? i * L + l : 0];
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const bool in = live && i * L + l < c.experts;
-    key[i] = in ? order_key(v[i] + bias[i]) : 0u;
-  }
-  if (c.on_score) {
+  for (int q = 0; q < Q; ++q)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const bool in = live && i * L + l < c.experts && order_key(v[i]);
-      key[i] = in ? order_key(1.0f / (1.0f + expf(-v[i])) + bias[i]) : 0u;
+      const bool in = t + q * step < end && i * L + l < c.experts;
+      key[q][i] = in ? order_key(v[q][i] + bias[i]) : 0u;
     }
+  if (c.on_score) {
+#pragma unroll
+    for (int q = 0; q < Q; ++q)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const bool in = t + q * step < end && i * L + l < c.experts && order_key(v[q][i]);
+        key[q][i] = in ? order_key(1.0f / (1.0f + expf(-v[q][i])) + bias[i]) : 0u;
+      }
   }
 }
 
 // One token on L lanes: lane j < topk returns choice j (-1: none) and its weight.
 template <int L, int NV>
 __device__ __forceinline__ void choose(const RouteCall& c, int64_t t, bool live, int l, int& id, float& weight) {
-  float v[NV];
-  uint32_t key[NV];
-  load_keys<L, NV>(c, t, live, l, v, key);
+  float v1[1][NV];
+  uint32_t key1[1][NV];
+  load_keys<L, NV>(c, t, 1, live ? t + 1 : t, l, v1, key1);
+  float(&v)[NV] = v1[0];
+  uint32_t(&key)[NV] = key1[0];
   float top = -__builtin_inff(), sum = 0.0f;
   if (c.scoring == 0) {
 #pragma unroll
@@ -145,42 +159,58 @@ __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
-// The same choice on a whole wave, without weights, of Q tokens t, t + NW, .. at once: the
-// largest key goes through scalar registers, and ballots find the lowest index that
-// has it, so a round is one chain of row maxima instead of two butterflies, and
-// the tokens' chains run beside each other.
+// The same choice on a whole wave as a set, without order and weights, of Q tokens t, t +
+// NW, .. at once: sel[q] has bit i where this lane's expert 64 i + lane is chosen.  The
+// smallest key that is chosen is found from its top bit down: of the keys with the
+// bits so far at least as many as are wanted must remain.  A step is a few compares and scalar bit
+// counts, it ends where exactly as many remain, and the tokens' chains run
+// beside each other.  A block's time up to its first tile, us: one token, 8 of 64
+// experts 2.6, with a round a choice as in choose 3.3; sixteen tokens 4.9, 6 of 160 experts 7.9.
 template <int NV, int NW, int Q>
-__device__ __forceinline__ void choose_wave(const RouteCall& c, int t, int (&id)[Q]) {
+__device__ __forceinline__ void choose_set(const RouteCall& c, int t, uint32_t (&sel)[Q]) {
   const int lane = threadIdx.x & 63;
   float v[Q][NV];
-  uint32_t key[Q][NV];
+  uint32_t key[Q][NV], least[Q];   // at least `want` keys are not below least
+  int want[Q];
+  bool exact[Q], open = false;     // exact: `want` are not, no more
+  auto remain = [&](int q, uint32_t from) __attribute__((always_inline)) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) n += __popcll(__ballot(key[q][i] >= from));
+    return n;
+  };
+  load_keys<64, NV>(c, t, NW, c.tokens, lane, v, key);
 #pragma unroll
   for (int q = 0; q < Q; ++q) {
-    load_keys<64, NV>(c, t + NW * q, t + NW * q < c.tokens, lane, v[q], key[q]);
-    id[q] = -1;
+    const int live = remain(q, 1u);   // (key 0: never chosen)
+    const bool all = live <= c.topk;
+    want[q] = all ? live : c.topk;
+    least[q] = all ? 1u : 0u;
+    exact[q] = all;
+    open = open || !all;
   }
-  for (int j = 0; j < c.topk; ++j) {
-    uint32_t best[Q];
+  for (int b = 31; b >= 0 && open; --b) {
+    open = false;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      best[q] = key[q][0];
-#pragma unroll
-      for (int i = 1; i < NV; ++i) best[q] = max(best[q], key[q][i]);
-      butterfly<16>([&](auto from) { best[q] = max(best[q], from(best[q])); });
+    for (int q = 0; q < Q; ++q) {   // (for a token that has ended more bits change nothing; skipping it costs more)
+      const uint32_t from = least[q] | 1u << b;
+      const int n = remain(q, from);
+      least[q] = n >= want[q] ? from : least[q];
+      exact[q] = exact[q] || n == want[q];
+      open = open || !exact[q];
     }
+  }
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      auto row = [&](int r) __attribute__((always_inline)) { return (uint32_t)__builtin_amdgcn_readlane((int)best[q], 16 * r); };
-      const uint32_t most = max(max(row(0), row(1)), max(row(2), row(3)));
-      int e = -1;   // stays so when nothing is left
+  for (int q = 0; q < Q; ++q) {
+    // above the least key all are chosen, of the equal ones the first
+    int left = want[q] - remain(q, least[q] + 1u);
+    sel[q] = 0u;
 #pragma unroll
-      for (int i = NV - 1; i >= 0; --i) {
-        const uint64_t has = __ballot(key[q][i] == most);
-        e = has && most ? 64 * i + __ffsll((unsigned long long)has) - 1 : e;
-      }
-      id[q] = lane == j ? e : id[q];
-#pragma unroll
-      for (int i = 0; i < NV; ++i) key[q][i] = e == 64 * i + lane ? 0u : key[q][i];
+    for (int i = 0; i < NV; ++i) {
+      const uint64_t same = __ballot(key[q][i] == least[q]);
+      const bool first = __popcll(same & ((1ull << lane) - 1ull)) < left;
+      sel[q] |= key[q][i] > least[q] || (key[q][i] == least[q] && first) ? 1u << i : 0u;
+      left -= __popcll(same);
     }
   }
 }
@@ -256,12 +286,13 @@ __device__ __forceinline__ int route_few(const RouteCall& c, RoutedLds& s) {
   const int tokens = (int)c.tokens;
   for (int i = threadIdx.x; i < c.experts; i += 64 * NW) s.tokens[i] = 0u;
   auto few = [&](auto Q) __attribute__((always_inline)) {
-    int id[decltype(Q)::value];
-    choose_wave<L * NV / 64, NW>(c, wave, id);
+    uint32_t sel[decltype(Q)::value];
+    choose_set<L * NV / 64, NW>(c, wave, sel);
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < decltype(Q)::value; ++q)
-      if (id[q] >= 0) atomicOr(&s.tokens[id[q]], 1u << (wave + NW * q));   // (bits: their order does not matter)
+      for (uint32_t left = sel[q]; left; left &= left - 1u)   // (bits: their order does not matter)
+        atomicOr(&s.tokens[64 * (__ffs((int)left) - 1) + lane], 1u << (wave + NW * q));
   };
   if (tokens > NW) few(std::integral_constant<int, kLayerTokens / NW>{});
   else few(std::integral_constant<int, 1>{});
