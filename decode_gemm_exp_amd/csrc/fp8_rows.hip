@@ -212,10 +212,11 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   return hipGetLastError();
 }
 // One matrix: 64 rows of it a wave, or 32 and eight waves a block where that makes too
-// few blocks, or 16 where those fit the chip at once (32 / 16 rows, us: 13 rows of 1000x16384 12.6 / 9.8, of
-// 4096x4096 6.5 / 5.7, of 5001x8224, 313 blocks of 16, 17.3 / 21.7); x through LDS, like the weights, once its loads are many, or two groups of
-// sixteen rows where the blocks still fill the chip.  Measured (us; 64 rows, 64 with x in LDS, 32
-// with eight waves, the same with x in LDS, two groups; x in BF16):
+// few blocks, or 16 where those fit the chip at once (32 / 16 a wave, us, 13 rows of x:
+// 1000x16384 12.6 / 9.8, 4096x4096 6.5 / 5.7, 5001x8224, 313 blocks of 16, 17.3 / 21.7); x
+// through LDS, like the weights, once its loads are many, or two groups of sixteen rows
+// where the blocks still fill the chip.  Measured (us; 64 rows, 64 with x in LDS, 32 with
+// eight waves, the same with x in LDS, two groups; x in BF16):
 //   14336x4096   1 row 14.4 / 15.6 / 14.2 / 15.8, 16 rows 15.3 / 16.0 / 17.5 / 17.5, 32 rows 21.5 / 22.2 / 26.8 / 26.7 / 19.2
 //   5001x8224    1 row 21.7 / 24.1 / 15.0 / 15.6, 16 rows 28.2 / 25.4 / 18.9 / 17.9, 32 rows 26.6 / 24.1 / 29.5 / 27.3 / 39.8
 //   4096x4096    1 row  7.9 /  8.6 /  5.8 /  6.1, 16 rows  9.2 /  8.9 /  8.2 /  6.7, 32 rows  9.3 /  8.7 /  8.4 /  7.0 / 13.0
@@ -254,8 +255,10 @@ hipError_t launch_routed(const ExpertsCall& c, const RouteCall& r, hipStream_t s
 
 }  // namespace
 
-// 32 outputs a tile, or where that makes fewer tiles than blocks fit the chip 16 and eight waves, so
-// that all of a wave's windows are on their way at once (64 experts 1408x2048, us: 16 tokens 63 / 67).
+// 32 outputs a tile, or where that makes fewer tiles than blocks fit the chip 16 and eight
+// waves, so that all of a wave's windows are on their way at once (layer of one token, 8 of 64
+// experts, us with 32 / 16: 512x7168 32.6 / 28.4, 1408x2048 23.0 / 22.2; two of eight 2048x4096
+// 22.8 / 19.2; beyond the rule, 16 tokens over 64 of 1408x2048, the product alone 63 / 67).
 hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s) {
   const int64_t pairs = r.tokens * r.topk;
   if ((c.w.n + 31) / 32 * (pairs < r.experts ? pairs : r.experts) < 2 * device_cus()) return launch_routed<2, 8>(c, r, s);
@@ -281,10 +284,11 @@ double tile_us(int64_t blocks, int64_t steps, int rows, int64_t cus) {
 }  // namespace
 
 // Grouped by expert.  The chunks of rows that the plan will make are not known here: one an
-// expert at least, and half a chunk an expert more than whole ones.  Weights pass the rows kernel
-// at 5 TB/s, in groups of 16 rows or, with more than 12 an expert, 32, and the tiles at 4.7 TB/s at
-// most.  (us, measured rows / 64 / 128: 32 experts 2048x2048 of 4 rows 31 / 29 / 31, of 32 rows 43 / 31 / 32, of
-// 64 rows 65 / 50 / 37; 8 of 2048x4096, 64 rows 32 / 38 / 46, 256 rows - / 81 / 59.)
+// expert at least, and half a chunk an expert more than whole ones.  Weights pass the rows
+// kernel at 5 TB/s, in groups of 16 rows or, with more than 12 an expert, 32, and the tiles
+// at 4.7 TB/s at most.  (us, measured rows / 64 / 128: 32 experts 2048x2048 of 4 rows 31 /
+// 29 / 31, of 32 rows 43 / 31 / 32, of 64 rows 65 / 50 / 37; 8 of 2048x4096, 64 rows 32 / 38 /
+// 46, 256 rows - / 81 / 59.)
 hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
   const int64_t e = c.w.count, slots = c.r.slots, avg = (slots + e - 1) / e, with_rows = slots < e ? slots : e;
   const int64_t ntiles = (c.w.n + (c.gated ? 127 : 255)) / (c.gated ? 128 : 256);
@@ -305,9 +309,11 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
   return launch_fp8_tile(c, Fp8Tile{t64 < t128 ? 64 : 128, spread, 0, 1, nullptr, nullptr}, s);
 }
 
-// One matrix.  The tiles of the last, partly filled round go in slices of K where that is faster: it
-// costs 6.5 and the slices' sums at 5.3 TB/s.  The weights pass the tiles at 2.5 TB/s at most; the rows kernel takes the weights once per 16 rows at 7 TB/s, or per 32 at 6.2
-// where that fills the chip.
+// One matrix.  The tiles of the last, partly filled round go in slices of K where that is
+// faster: it costs 6.5 and the slices' sums at 5.3 TB/s.  The weights pass the tiles at
+// 2.5 TB/s at most; the rows kernel takes them once per 16 rows of x at 7 TB/s, or per 32 at
+// 6.2 where that fills the chip.  (us without / with slices: 5001x8224, 200 rows 55 / 40;
+// 4096x14336, 333 rows 173 / 56.)
 Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   auto pad = [](uint64_t b) { return (b + 255) / 256 * 256; };
   Fp8Plan p{};

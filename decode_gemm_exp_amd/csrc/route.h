@@ -161,11 +161,12 @@ __device__ __forceinline__ void wave_fence() {
 
 // The same choice on a whole wave as a set, without order and weights, of Q tokens t, t +
 // NW, .. at once: sel[q] has bit i where this lane's expert 64 i + lane is chosen.  The
-// smallest key that is chosen is found from its top bit down: of the keys with the
-// bits so far at least as many as are wanted must remain.  A step is a few compares and scalar bit
-// counts, it ends where exactly as many remain, and the tokens' chains run
-// beside each other.  A block's time up to its first tile, us: one token, 8 of 64
-// experts 2.6, with a round a choice as in choose 3.3; sixteen tokens 4.9, 6 of 160 experts 7.9.
+// smallest key that is chosen is found from its top bit down: of the keys not below the
+// bits so far at least as many as are wanted must remain.  A step is a few compares and
+// scalar bit counts, the search ends where exactly as many remain, and the tokens' chains
+// run beside each other.  A block's time up to its first tile, us: one token, 8 of 64
+// experts 2.6, with a round a choice as in choose 3.3; sixteen tokens 4.9, 6 of 160
+// experts 7.9.
 template <int NV, int NW, int Q>
 __device__ __forceinline__ void choose_set(const RouteCall& c, int t, uint32_t (&sel)[Q]) {
   const int lane = threadIdx.x & 63;
@@ -216,21 +217,21 @@ __device__ __forceinline__ void choose_set(const RouteCall& c, int t, uint32_t (
 }
 
 // ---- a few tokens, routed by every block for itself ----------------------------
-// kLayerTokens tokens at most.  Each block makes the choice anew (a microsecond or two, while a
-// launch of its own and the wait for it cost several) and finds its experts' rows in it;
-// block 0 writes the plan, the same that uw_route_experts writes, and nothing else.
+// kLayerTokens tokens at most.  Each block makes the choice anew (2.6 to 8 us with all that
+// precedes its first tile; a launch of its own takes 5.7 and the wait for it) and finds its
+// experts' rows in it; block 0 writes the plan, the same that uw_route_experts writes, and
+// nothing else.
 template <int L, int NV>
 struct RoutedRows {
-  static constexpr int kLanes = L, kKeys = NV;
   RouteCall c;
-  int64_t slots, x_rows;
+  int64_t x_rows;
 };
 
 // The pairs by expert, and the items they make: an expert and up to C of its tokens.
 struct PairsLds {
   int32_t expert[kLayerPairs];                       // by slot, -1 behind the last
   int32_t token[kLayerPairs];
-  float weight[kLayerPairs];                         // (where they are needed)
+  float weight[kLayerPairs];
   int32_t item_expert[kLayerPairs + 1];              // (one more, and of the first slots, for reading ahead)
   int32_t item_first[kLayerPairs + 2];               // its first slot; behind the last item the number of slots
 };
@@ -396,17 +397,18 @@ __device__ __forceinline__ int nth_bit(uint32_t bits, int n) {
 // The kernel for a layer's number of experts: lanes a token times keys a lane.
 template <typename F>
 hipError_t with_routed(const RouteCall& c, F&& f) {
-  if (c.experts <= 64) return f(RoutedRows<16, 4>{c, c.tokens * c.topk, c.tokens});
-  if (c.experts <= 128) return f(RoutedRows<16, 8>{c, c.tokens * c.topk, c.tokens});
-  if (c.experts <= 192) return f(RoutedRows<16, 12>{c, c.tokens * c.topk, c.tokens});
-  if (c.experts <= 256) return f(RoutedRows<16, 16>{c, c.tokens * c.topk, c.tokens});
-  return f(RoutedRows<64, 16>{c, c.tokens * c.topk, c.tokens});
+  if (c.experts <= 64) return f(RoutedRows<16, 4>{c, c.tokens});
+  if (c.experts <= 128) return f(RoutedRows<16, 8>{c, c.tokens});
+  if (c.experts <= 192) return f(RoutedRows<16, 12>{c, c.tokens});
+  if (c.experts <= 256) return f(RoutedRows<16, 16>{c, c.tokens});
+  return f(RoutedRows<64, 16>{c, c.tokens});
 }
 // Blocks: the plan's, then one for each of `ntiles` tiles of every expert that can have
-// pairs, or `resident` on every CU where that is fewer.  (us with 4 / 2 / 8 a CU / one a tile, BF16, 16
-// tokens, 64 experts 1408x2048: 112 / 124 / 118 / 141; MXFP4, 160 experts, with 2 / one a tile: 56 / 97.  Fewer
-// blocks that all take the same number of tiles leave less on its way: one token, two of eight BF16
-// experts 14336x4096 133 -> 140, eight of 64 FP8 experts 20.1 -> 21.5 for the layer.)
+// pairs, or `resident` on every CU where that is fewer.  (us with 4 / 2 / 8 a CU / one a
+// tile, BF16, 16 tokens, 64 experts 1408x2048: 112 / 124 / 118 / 141; MXFP4, 160 experts,
+// with 2 / one a tile: 56 / 97.  Fewer blocks that all take the same number of tiles leave
+// less on its way: layer of one token, two of eight BF16 experts 14336x4096 133 -> 140,
+// eight of 64 FP8 experts 20.1 -> 21.5.)
 inline int64_t routed_grid(const RouteCall& c, int64_t ntiles, int resident) {
   const int64_t pairs = c.tokens * c.topk, tiles = ntiles * (pairs < c.experts ? pairs : c.experts);
   const int64_t most = (int64_t)device_cus() * resident;
