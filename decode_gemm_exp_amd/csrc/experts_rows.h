@@ -127,7 +127,8 @@ struct Place {
 };
 __device__ __forceinline__ Place place_of(const RaggedRows& rr, unsigned ntiles, unsigned chunks) {
   if (rr.offsets) return {blockIdx.x % ntiles, blockIdx.x / ntiles};
-  const unsigned turn = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);   // (the grid is a multiple of 8)
+  const unsigned eighth = (ntiles * chunks + 7) / 8;   // (of the grid, a multiple of 8: one argument less to load)
+  const unsigned turn = (blockIdx.x & 7) * eighth + (blockIdx.x >> 3);
   return {turn / chunks, turn % chunks};
 }
 
@@ -200,8 +201,10 @@ struct Finder<RoutedRows<L, NV>> {
 
 // The waves' sums, added in wave order and stored.  red: per wave and tile
 // the MFMA's D: lane l holds output features 4 (l / 16) .. +3 of slot l % 16.
+// rows: the block's, up to N - n0 of them or a multiple of four.
 template <int R, int Q, bool GATED, int NW>
-__device__ __forceinline__ void finish(const f32x4_t* red, const Share& sh, int64_t n0, int64_t N, void* __restrict__ y) {
+__device__ __forceinline__ void finish(const f32x4_t* red, const Share& sh, int64_t n0, int64_t rows, int64_t N,
+                                       void* __restrict__ y) {
   constexpr int RT = GATED ? R / 2 : R;
   for (int i = threadIdx.x; i < RT * Q * 64; i += 64 * NW) {
     const int ln = i & 63, q = (i >> 6) % Q, t = (i >> 6) / Q;
@@ -213,8 +216,9 @@ __device__ __forceinline__ void finish(const f32x4_t* red, const Share& sh, int6
     };
     f32x4_t s = sum(t);
     const int b = 16 * q + (ln & 15);
-    const int64_t n = n0 + 16 * t + 4 * (ln >> 4);
-    if (b >= sh.count || n >= N) continue;
+    const int f = 16 * t + 4 * (ln >> 4);
+    const int64_t n = n0 + f;
+    if (b >= sh.count || f >= rows) continue;
     const int64_t at = (sh.first + b) * N + n;
     if constexpr (GATED) {
       const f32x4_t u = sum(t + RT);

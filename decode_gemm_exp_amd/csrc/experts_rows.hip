@@ -120,7 +120,7 @@ __global__ __launch_bounds__(256) void k_experts_rows(ExpertsView vw, ExpertsVie
 #pragma unroll
       for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
     __syncthreads();
-    finish<R, Q, GATED, 4>(red, sh, n0, N, y);
+    finish<R, Q, GATED, 4>(red, sh, n0, N - n0, N, y);
     if constexpr (!Finder<RR>::kWalks) return;
     __syncthreads();   // the sums have been read
   }
@@ -299,7 +299,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_mx4(ExpertsView vw, Experts
 #pragma unroll
       for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
     __syncthreads();
-    finish<R, Q, GATED, NW>(red, sh, n0, N, y);
+    finish<R, Q, GATED, NW>(red, sh, n0, N - n0, N, y);
     if constexpr (!Finder<RR>::kWalks) return;
     __syncthreads();   // the sums have been read
   }

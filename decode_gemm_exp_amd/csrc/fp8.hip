@@ -1,7 +1,8 @@
 // fp8.hip -- conversion between BF16 / FP32 and E4M3 with an FP32 scale per block
 // of 1 x 128 (a row's) or 128 x 128 (a matrix's); see fp8.h for the arithmetic.
 //
-// Bound: HBM, 2 (or 4) + 1 bytes an element.  One pass: what a block's maximum is
+// Bound: HBM, 2 (or 4) + 1 bytes an element; 14336x4096 BF16 in 128 x 128 takes 30 to 32 us,
+// back 30 (176 MB: 5.5 to 5.9 TB/s).  One pass: what a block's maximum is
 // taken over stays in registers until it is converted.  A thread holds pieces of
 // eight elements, sixteen lanes a row of a block, so that loads and stores run
 // over whole rows of blocks.

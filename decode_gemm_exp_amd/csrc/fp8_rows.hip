@@ -23,8 +23,10 @@ namespace {
 template <int R, int Q, bool GATED, bool ACT8, bool XL, int NW, typename RR>
 __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, ExpertsView vu, RR rr,
                                                          const uint16_t* __restrict__ x, void* __restrict__ y,
-                                                         int ntiles, int chunks) {
-  constexpr int RT = GATED ? R / 2 : R, kRows = 16 * RT;
+                                                         int ntiles, int chunks, int most) {
+  constexpr int RT = GATED ? R / 2 : R;
+  constexpr bool kBelow = !GATED && !ACT8 && R > 1;   // tiles of `most` rows, which may end in the next row of blocks
+  const int span = kBelow ? most : 16 * RT;
   constexpr int kW = 16 * R * 128;   // a wave's weights of a window
   constexpr int kX = XL ? 16 * 256 : 4;
   __shared__ __attribute__((aligned(128))) char w0[NW * kW], w1[NW * kW];
@@ -40,16 +42,21 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
     const int i16 = lane & 15, g = lane >> 4;
     const int64_t N = vw.n;
     const int K = (int)vw.k, nwin = (int)fp8_blocks(K);
-    const int64_t n0 = (int64_t)tile * kRows;
-    const int64_t rows = N - n0 < kRows ? N - n0 : kRows;
+    const int64_t n0 = (int64_t)tile * span;
+    const int64_t rows = N - n0 < span ? N - n0 : span;
     auto weights = [&](const ExpertsView& v) __attribute__((always_inline)) {
       return rsrc_of(v.w + (int64_t)sh.expert * v.w_stride + n0 * K, (uint64_t)(rows * K));
     };
-    auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {   // the row of blocks that holds n0
-      return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + (n0 >> 7) * nwin * 4, (uint64_t)nwin * 4);
+    // The row of blocks that holds n0 and, kBelow, the next; the upper half of the wave
+    // loads that one's.
+    const int row_blocks = (int)(fp8_blocks(N) - (n0 >> 7));
+    auto scales = [&](const ExpertsView& v) __attribute__((always_inline)) {
+      return rsrc_of(v.scale + (int64_t)sh.expert * v.scale_stride + (n0 >> 7) * nwin * 4,
+                     (uint64_t)nwin * (kBelow && row_blocks > 1 ? 8 : 4));
     };
     const __amdgpu_buffer_rsrc_t ww = weights(vw), ws = scales(vw);
     const __amdgpu_buffer_rsrc_t uw = GATED ? weights(vu) : ww, us = GATED ? scales(vu) : ws;
+    const int upper = 128 - (int)(n0 & 127);   // rows of the tile in the first of them
 
     // x rows of this lane's slots
     const __amdgpu_buffer_rsrc_t rx = rsrc_of(x, (uint64_t)rr.x_rows * 2 * (uint64_t)K);
@@ -82,7 +89,7 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
     };
     struct Win {
       uint4 xv[Q][4];
-      float s[2];   // the blocks' scales, 0 past the last window
+      float s[2];   // the blocks' scales (gated: W's and U's), 0 past the last window
     };
     auto load_x = [&](int j, char* xbuf, Win& w) __attribute__((always_inline)) {
       const int k0 = 128 * j;
@@ -102,9 +109,9 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
             w.xv[q][i] = bload16(rx, k < K ? xrow[q] + 2u * (uint32_t)k : kOutside);
           }
       }
-      const int at = j < nwin ? 4 * j : (int)kOutside;
+      const int at = j < nwin ? 4 * (kBelow ? j + (lane >> 5) * nwin : j) : (int)kOutside;
       w.s[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(ws, at, 0, 0));
-      w.s[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(us, at, 0, 0)) : w.s[0];
+      if constexpr (GATED) w.s[1] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(us, at, 0, 0));
     };
     auto compute = [&](const char* wbuf, const char* xbuf, Win& w) __attribute__((always_inline)) {
       if constexpr (XL) {
@@ -158,11 +165,23 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
             part[t][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, xv[q][i]), part[t][q],
                                                                  0, 0, 0);
         }
+      float sw[R];
+      if constexpr (kBelow) {
+        auto half = [&](int l) __attribute__((always_inline)) {
+          return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w.s[0]), l));
+        };
+        const float first = half(0), below = half(32);
+#pragma unroll
+        for (int t = 0; t < R; ++t) sw[t] = 16 * t + 4 * g < upper ? first : below;
+      } else {
+#pragma unroll
+        for (int t = 0; t < R; ++t) sw[t] = w.s[t >= RT ? 1 : 0];
+      }
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
         for (int t = 0; t < R; ++t) {
-          const float sw = w.s[t >= RT ? 1 : 0], s = ACT8 ? sx[q] * sw : sw;
+          const float s = ACT8 ? sx[q] * sw[t] : sw[t];
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[t][q][c] = __builtin_fmaf(part[t][q][c], s, acc[t][q][c]);
         }
@@ -195,20 +214,33 @@ __global__ __launch_bounds__(64 * NW) void k_experts_fp8(ExpertsView vw, Experts
 #pragma unroll
       for (int q = 0; q < Q; ++q) red[((wave * R + t) * Q + q) * 64 + lane] = acc[t][q];
     __syncthreads();
-    finish<R, Q, GATED, NW>(red, sh, n0, N, y);
+    finish<R, Q, GATED, NW>(red, sh, n0, rows, N, y);
     if constexpr (!Finder<RR>::kWalks) return;
     __syncthreads();   // the sums have been read
   }
 }
 
+// One matrix and BF16 x: where whole tiles fill the rounds of blocks on the CUs to less than
+// three quarters, each block gets as few rows as make no more rounds, in fours, half its tile
+// at least.  (us, whole tiles / so, weights out of every cache: 5001x8224, 157 / 251 blocks, 1
+// row 15.9 / 14.8, 13 rows 17.7 / 16.4; 9000x4096 13.6 / 12.9, 16.2 / 15.1; 18432x5120 26.1 / 21.8,
+// 33.3 / 29.3.  With less to even out a block's own work counts: 7168x2048, 224 / 256 blocks,
+// 1 row 6.0 / 6.2; so does x's conversion, which every block makes: 5001x8224, 13 rows, weights
+// in the last-level cache 15.5 / 16.1.)
 template <int R, int Q, bool GATED, bool ACT8, bool XL, int NW>
 hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
-  const int64_t rows = GATED ? 8 * R : 16 * R, ntiles = (c.w.n + rows - 1) / rows;
   const int64_t chunks = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr);
+  int64_t rows = GATED ? 8 * R : 16 * R, ntiles = (c.w.n + rows - 1) / rows;
+  if (!c.r.offsets && !ACT8 && R > 1) {
+    const int64_t cus = device_cus(), most = (ntiles * chunks + cus - 1) / cus * cus / chunks;
+    const int64_t even = ((c.w.n + most - 1) / most + 3) / 4 * 4;
+    if (4 * even < 3 * rows) rows = even > rows / 2 ? even : rows / 2;
+    ntiles = (c.w.n + rows - 1) / rows;
+  }
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (!grid_fits(grid, 64 * NW)) return hipErrorNotSupported;
   hipLaunchKernelGGL((k_experts_fp8<R, Q, GATED, ACT8, XL, NW, RaggedRows>), dim3((unsigned)grid), dim3(64 * NW), 0, s,
-                     c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks);
+                     c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks, (int)rows);
   return hipGetLastError();
 }
 // One matrix: 64 rows of it a wave, or 32 and eight waves a block where that makes too
@@ -248,7 +280,7 @@ hipError_t launch_routed(const ExpertsCall& c, const RouteCall& r, hipStream_t s
   if (!grid_fits(grid, 64 * NW)) return hipErrorNotSupported;
   return with_routed(r, [&](auto rr) {
     hipLaunchKernelGGL((k_experts_fp8<R, 1, true, false, false, NW, decltype(rr)>), dim3((unsigned)grid), dim3(64 * NW),
-                       0, s, c.w, c.u, rr, c.x, c.y, (int)ntiles, 0);
+                       0, s, c.w, c.u, rr, c.x, c.y, (int)ntiles, 0, 0);
     return hipGetLastError();
   });
 }

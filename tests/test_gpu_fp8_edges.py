@@ -52,6 +52,31 @@ def test_slices_of_k_exactly(uw, batch, n, k, act):
         assert bool((y[batch] == 7.0).all()) and bool((ws[nb:] == fill).all())
 
 
+# Blocks of 20, 24, 32, 36 and 44 rows of the matrix, some of which end in the next row of scale blocks, with the last
+# block cut off; a number of columns that is no multiple of four; one to three groups of rows of x.
+@pytest.mark.parametrize("n,k", [(4500, 160), (5001, 2080), (5900, 1056), (8300, 96), (9000, 544), (17001, 224),
+                                 (22400, 128)])
+@pytest.mark.parametrize("batch", [1, 7, 13, 16, 20, 33])
+@pytest.mark.parametrize("act", ["bf16", "fp8"])
+def test_rows_that_straddle_scale_blocks_exactly(uw, n, k, batch, act):
+    """Scales are powers of two from 1/4 to 4, every one of a block's neighbours another."""
+    g = torch.Generator().manual_seed(n + k + batch)
+    w, x = whole_numbers(g, n, k), whole_numbers(g, batch, k)
+    a = uw.ACT_BF16
+    if act == "fp8":
+        a = uw.ACT_FP8
+        x[:, ::128] = 448.0           # x's own scales are one
+        w[:, ::128] = 0.0
+    i, j = (torch.arange(m, device=DEV) for m in uw.fp8_scale_shape(n, k, 128))
+    scale = torch.exp2((2.0 * i[:, None] + j) % 5 - 2)
+    wide = w * scale.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    y = torch.full((batch + 1, n), 7.0, device=DEV)
+    ws = torch.empty(uw.uw_workspace_size_fp8(n, k, batch, a), dtype=torch.uint8, device=DEV)
+    uw.uw_matmul_fp8(w.to(torch.float8_e4m3fn), scale, x.bfloat16(), y[:batch], ws, a)
+    assert torch.equal(y[:batch].double(), x.double() @ wide.double().T)
+    assert bool((y[batch] == 7.0).all())
+
+
 def test_workspace_too_small_is_refused(uw):
     n, k, batch = 4096, 14336, 333
     elem = torch.zeros(n, k, dtype=torch.uint8, device=DEV)
