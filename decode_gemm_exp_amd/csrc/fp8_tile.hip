@@ -172,14 +172,15 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
     return s >= steps ? nk : first + (ss >= steps ? ss - steps : ss);
   };
   auto load_scales = [&](int s, Scales& c) __attribute__((always_inline)) {
-    const int b = block_of(s), at = b < nk ? 4 * b : (int)kOutside;
-    c.w[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs0, at, 0, 0));
-    c.w[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs1, at, 0, 0)) : c.w[0];
+    const int b = block_of(s);
+    const uint32_t at = b < nk ? 4u * (uint32_t)b : kOutside;   // (unsigned: a slot's own offset is added to kOutside as well)
+    c.w[0] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs0, (int)at, 0, 0));
+    c.w[1] = GATED ? __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs1, (int)at, 0, 0)) : c.w[0];
     if constexpr (ACT8) {
 #pragma unroll
       for (int i = 0; i < TM; ++i)
         c.x[i] = __builtin_bit_cast(
-            float, __builtin_amdgcn_raw_buffer_load_b32(ra, at + 4 * nk * (slot_of(i) + col), 0, 0));
+            float, __builtin_amdgcn_raw_buffer_load_b32(ra, (int)(at + 4u * (uint32_t)(nk * (slot_of(i) + col))), 0, 0));
     }
   };
 

@@ -211,7 +211,7 @@ __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
     const bool tail = wl.j == nwin - 1;
     const int k0 = P * W * wl.j;
     auto pick = [&](uint32_t most, uint32_t end) __attribute__((always_inline)) {
-      return (int)(in ? tail ? end : most : kOutside);
+      return in ? tail ? end : most : kOutside;
     };
     if constexpr (form_is_pal(FORM)) {
       load_raw(mat, row, K, in ? k0 + W * place : K, g, f, w.r);
@@ -220,20 +220,20 @@ __global__ __launch_bounds__(kNT) void k_layer_down(LayerDown c) {
 #pragma unroll
       for (int i = 0; i < NW_; ++i) {
         const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(
-            rw, pick(wo[0][i], wo[1][i]), FORM == kFormBf16 ? 2 * k0 : FORM == kFormFp8 ? k0 : k0 / 2, 0);
+            rw, (int)pick(wo[0][i], wo[1][i]), FORM == kFormBf16 ? 2 * k0 : FORM == kFormFp8 ? k0 : k0 / 2, 0);
         w.r.d[i] = make_uint4(v.x, v.y, v.z, v.w);
       }
       if constexpr (FORM == kFormFp8)
-        w.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, pick(so[0][0], so[1][0]), k0 / 32, 0);
+        w.sc[0] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)pick(so[0][0], so[1][0]), k0 / 32, 0);
       if constexpr (FORM == kFormMx4) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
-          w.sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, pick(so[0][i], so[1][i]), k0 / 32, 0);
+          w.sc[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, (int)pick(so[0][i], so[1][i]), k0 / 32, 0);
       }
     }
 #pragma unroll
     for (int l = 0; l < NX; ++l) {
-      const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)hrow + pick(xo[0][l], xo[1][l]), 2 * k0, 0);
+      const u32x4_t v = __builtin_amdgcn_raw_buffer_load_b128(rh, (int)(hrow + pick(xo[0][l], xo[1][l])), 2 * k0, 0);
       w.xv[l] = make_uint4(v.x, v.y, v.z, v.w);
     }
     next(wl);

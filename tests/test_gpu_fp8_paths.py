@@ -1,0 +1,61 @@
+"""FP8 products through kernels and splits that a call's sizes choose, exactly.
+
+Whole numbers: elements and x in -2 .. 2 at scales that are powers of two give sums far below 2^24
+steps, exact in FP32 whatever their order, so results are equal, not near.  With x in 8 bits a 448 at
+the head of each of its blocks, beside a zero weight, makes its scales one.
+"""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+@pytest.fixture(scope="module")
+def uw():
+    from decode_gemm_exp_amd import uw as _uw
+    return _uw
+
+
+def whole_numbers(g, *shape):
+    return torch.randint(-2, 3, shape, generator=g).float().to(DEV)
+
+
+def problem(uw, batch, n, k, act, seed=0):
+    """elem, scale, x, activation type and the product."""
+    g = torch.Generator().manual_seed(batch + n + k + seed)
+    w, x = whole_numbers(g, n, k), whole_numbers(g, batch, k)
+    if act == "fp8":
+        x[:, ::128] = 448.0
+        w[:, ::128] = 0.0
+    i, j = (torch.arange(m, device=DEV) for m in uw.fp8_scale_shape(n, k, 128))
+    scale = torch.exp2((2.0 * i[:, None] + j) % 5 - 2)   # 1/4 .. 4, every one of a block's neighbours another
+    wide = w * scale.repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)[:, :k]
+    return (w.to(torch.float8_e4m3fn), scale, x.bfloat16(), uw.ACT_FP8 if act == "fp8" else uw.ACT_BF16,
+            (x.double() @ wide.double().T).float())
+
+
+def workspace(uw, batch, n, k, a, fill=0xA5):
+    return torch.full((uw.uw_workspace_size_fp8(n, k, batch, a) + 256,), fill, dtype=torch.uint8, device=DEV)
+
+
+def check(uw, batch, n, k, act):
+    """The product is exact, twice, whatever the workspace held, and nothing beside y and the workspace is written;
+    returns the workspace's bytes afterwards, filled with 0xA5 before."""
+    elem, scale, x, a, want = problem(uw, batch, n, k, act)
+    y = torch.full((batch + 1, n), 7.0, device=DEV)
+    for fill in (0xFF, 0xA5):
+        ws = workspace(uw, batch, n, k, a, fill)
+        y[:batch] = float("nan")
+        uw.uw_matmul_fp8(elem, scale, x, y[:batch], ws[:-256], a)
+        assert torch.equal(y[:batch], want)
+        assert bool((y[batch] == 7.0).all()) and bool((ws[-256:] == fill).all())
+    return ws[:-256]
+
+
+@pytest.mark.parametrize("batch,n,k", [(300, 300, 20000), (700, 130, 32768), (1100, 520, 16544)])
+def test_scales_of_long_rows_of_x(uw, batch, n, k):
+    """Tiles whose rows' scales of x lie far apart: with more than 129 blocks a row, offsets of rows behind the last
+    block of k pass 2^31."""
+    ws = check(uw, batch, n, k, "fp8")
+    assert bool((ws != 0xA5).any())   # the tiles' x was laid out there
