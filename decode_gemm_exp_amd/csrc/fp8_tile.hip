@@ -280,6 +280,7 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
         part[m / 2][m % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[m % 2], fl[m / 2], part[m / 2][m % 2], 0, 0, 0);
 #pragma unroll
       for (int i = m * kPer; i < (m + 1) * kPer; ++i) {
+        if (i == XP) __builtin_amdgcn_sched_barrier(0);   // (x before weights: what the wait above counts on)
         if (i < XP) direct_x(kx, xcur, i);
         else if (i < P) direct_w(kw, wcur, i - XP);
       }
@@ -382,14 +383,17 @@ __global__ __launch_bounds__(kNT) void k_fp8_tile(ExpertsView vw, ExpertsView vu
 #pragma unroll
   for (int i = 0; i < TM; ++i) sc[0].x[i] = sc[1].x[i] = 0.0f;
   load_scales(0, sc[0]);
-  // the buffers' first filling, in the order in which the steps go on
+  // the buffers' first filling, in the order in which the steps go on; the waits count the loads, so the
+  // scheduler may not change it
   auto fill_x = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < XP; ++i) direct_x(kStep * block_of(b), xbufs[b], i);
+    __builtin_amdgcn_sched_barrier(0);
   };
   auto fill_w = [&](int b) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < WP; ++i) direct_w(kStep * block_of(b), wbufs[b], i);
+    __builtin_amdgcn_sched_barrier(0);
   };
   if constexpr (SX != SW) fill_w(0);
 #pragma unroll
