@@ -290,8 +290,11 @@ uw_status uw_workspace_size_fp8(int64_t n, int64_t k, int64_t batch, uw_activati
   if (!bytes) return UW_ERR_INVALID;
   Fp8Plan p;
   const uw_status st = check_fp8(n, k, batch, act, p);
-  if (st == UW_OK) *bytes = p.bytes();
-  return st;
+  if (st != UW_OK) return st;
+  // The rows kernel needs none, but fewer rows may go by tiles (the choice is alike for every sixteen).
+  for (int64_t b = (batch - 1) / 16 * 16; p.few && b > 0; b -= 16) p = plan_fp8(n, k, b, act == UW_ACT_FP8);
+  *bytes = p.bytes;
+  return UW_OK;
 }
 
 uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t n, int64_t k, const uint16_t* x_dev,
@@ -304,7 +307,7 @@ uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t
   if (!aligned(elem_dev, 16) || !aligned(scale_dev, 4) || !aligned(x_dev, 16) || !aligned(y_dev, 16) ||
       !aligned(ws_dev, 16))
     return UW_ERR_INVALID;
-  if (p.bytes() && (!ws_dev || ws_bytes < p.bytes())) return UW_ERR_WORKSPACE;
+  if (p.uses_workspace() && (!ws_dev || ws_bytes < p.bytes)) return UW_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   ExpertsCall c{};
   c.w.form = kFormFp8;

@@ -95,7 +95,10 @@ struct Fp8Plan {
   bool few;           // launch_fp8_rows
   Fp8Tile tile;       // (pointers not set)
   uint64_t x_bytes, scale_bytes, part_bytes;   // of the workspace, in this order
-  uint64_t bytes() const { return x_bytes + scale_bytes + part_bytes; }
+  // What a caller provides: never less for more rows, 0 with `few`.  Slices go up and down
+  // with the rows, so their share is a bound that all plans of as many rows or fewer keep.
+  uint64_t bytes;
+  bool uses_workspace() const { return x_bytes + scale_bytes + part_bytes != 0; }
 };
 Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8);
 hipError_t launch_fp8_product(const ExpertsCall& c, const Fp8Plan& p, bool act8, void* ws, hipStream_t s);

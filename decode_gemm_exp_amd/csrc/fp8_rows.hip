@@ -14,6 +14,8 @@
 // (p ^ (r / 2 % 8)); the waves' sums meet in LDS and are added in a fixed order.
 // ACT8: a lane's 32 values of x become elements by the maximum over the four lanes
 // that hold a block, which the wait for the weights hides.
+#include <algorithm>
+
 #include "experts_rows.h"
 #include "fp8.h"
 
@@ -345,7 +347,8 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
 // faster: it costs 6.5 and the slices' sums at 5.3 TB/s.  The weights pass the tiles at
 // 2.5 TB/s at most; the rows kernel takes them once per 16 rows of x at 7 TB/s, or per 32 at
 // 6.2 where that fills the chip.  (us without / with slices: 5001x8224, 200 rows 55 / 40;
-// 4096x14336, 333 rows 173 / 56.)
+// 4096x14336, 333 rows 173 / 56.)  Slices hold 512 rows of 256 sums a CU at most, which no
+// plan of a million shapes tried wanted to pass (1 to 60000 x 32 to 32768, 17 to 20000 rows).
 Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   auto pad = [](uint64_t b) { return (b + 255) / 256 * 256; };
   Fp8Plan p{};
@@ -353,9 +356,13 @@ Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   const int64_t cus = device_cus(), steps = fp8_blocks(k);
   const double weights = (double)n * (double)k * 1e-6;
   double best = 0;
+  constexpr int kSplits = 16;
+  const int64_t slice_rows = 4 * 128 * cus;
+  auto tiles_of = [&](int rows) { return (batch + rows - 1) / rows * ((n + 255) / 256); };
   for (int rows = big ? 128 : 64; rows <= 128; rows *= 2) {
-    const int64_t tiles = (batch + rows - 1) / rows * ((n + 255) / 256), tail = tiles % cus;
-    for (int splits = 1; splits <= 16 && (splits == 1 || (tail && steps >= 2 * splits)); ++splits) {
+    const int64_t tiles = tiles_of(rows), tail = tiles % cus;
+    for (int splits = 1; splits <= kSplits && (splits == 1 || (tail && steps >= 2 * splits && tail * splits * rows <= slice_rows));
+         ++splits) {
       double us = tile_us(splits > 1 ? tiles - tail : tiles, steps, rows, cus);
       if (splits > 1)
         us += tile_us(tail * splits, (steps + splits - 1) / splits, rows, cus) + 6.5 +
@@ -378,6 +385,13 @@ Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
     p.scale_bytes = pad(4 * (uint64_t)batch * (uint64_t)steps);
   }
   p.part_bytes = pad((uint64_t)p.tile.tail * (uint64_t)p.tile.splits * (uint64_t)p.tile.rows * 1024);
+  const int64_t splits = steps / 2 < kSplits ? steps / 2 : kSplits;
+  int64_t slices = 0;   // rows of the largest tail in most slices, as far as the tiles reach
+  for (int rows = 64; rows <= 128 && splits > 1; rows *= 2) {
+    const int64_t tiles = tiles_of(rows), tail = tiles < cus ? tiles : cus - 1;
+    slices = std::max(slices, tail * splits * rows);
+  }
+  p.bytes = p.x_bytes + p.scale_bytes + 1024 * (uint64_t)std::min(slices, slice_rows);
   return p;
 }
 

@@ -572,7 +572,8 @@ uw_status uw_dequantize_fp8(const uint8_t* elem_dev, const float* scale_dev, int
  * added to y's, in FP32, rounded once where it is a fused multiply-add.  Results
  * repeat bit for bit.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
  * 16-byte aligned.  The workspace (uw_workspace_size_fp8 bytes, 16-byte aligned, may
- * be 0) serves one call at a time. */
+ * be 0) serves one call at a time; the size never falls with more rows, so that one
+ * for the largest batch serves every smaller batch of that matrix and activation. */
 uw_status uw_workspace_size_fp8(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes);
 uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t n, int64_t k, const uint16_t* x_dev,
                         int64_t batch, float* y_dev, uw_activation act, void* ws_dev, size_t ws_bytes, void* stream);

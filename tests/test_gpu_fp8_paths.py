@@ -59,3 +59,18 @@ def test_scales_of_long_rows_of_x(uw, batch, n, k):
     block of k pass 2^31."""
     ws = check(uw, batch, n, k, "fp8")
     assert bool((ws != 0xA5).any())   # the tiles' x was laid out there
+
+
+@pytest.mark.parametrize("n,k,batches", [(4096, 14336, (2048, 1024, 333, 200, 48, 13, 1)),
+                                         (14336, 4096, (2048, 640, 129, 100, 96, 5)),
+                                         (5960, 8736, (96, 80, 64, 30)), (2532, 5152, (256, 208, 192, 100, 16))])
+@pytest.mark.parametrize("act", ["bf16", "fp8"])
+def test_workspace_of_the_largest_batch_serves_the_smaller(uw, n, k, batches, act):
+    a = uw.ACT_FP8 if act == "fp8" else uw.ACT_BF16
+    ws = workspace(uw, batches[0], n, k, a)
+    for batch in batches:
+        elem, scale, x, _, want = problem(uw, batch, n, k, act)
+        y = torch.full((batch, n), float("nan"), device=DEV)
+        uw.uw_matmul_fp8(elem, scale, x, y, ws[:-256], a)
+        assert torch.equal(y, want), batch
+    assert bool((ws[-256:] == 0xA5).all())
