@@ -1,6 +1,7 @@
 // experts_api.cpp -- the extern "C" entry points of the mixture-of-experts,
 // MXFP4 and FP8 operators (include/unweight.h): argument checks, the experts' weight
 // sets, workspaces.
+#include <algorithm>
 #include <cstring>
 #include <new>
 #include <vector>
@@ -120,6 +121,22 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
 // rows and moves with the blocks that the tiles make.
 constexpr int64_t kMx4RowsMax = 8;
 
+// A product with an MXFP4 matrix: its arguments but for pointers.
+uw_status check_mx4(int64_t n, int64_t k, int64_t batch, uw_activation act) {
+  if (batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_MX4)) return UW_ERR_INVALID;
+  const uw_status st = check_shape(n, k);
+  if (st != UW_OK) return st;
+  // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
+  return batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512) ? UW_ERR_UNSUPPORTED : UW_OK;
+}
+// The workspace it takes.
+uint64_t mx4_bytes(int64_t k, int64_t batch, uw_activation act) {
+  const uint64_t b = (uint64_t)batch;
+  return act != UW_ACT_MX4     ? 0
+         : batch <= kMx4RowsMax ? pad256(2 * b * (uint64_t)k)
+                                : pad256(b * (uint64_t)(k / 2)) + pad256(b * (uint64_t)mx4_scale_stride(k));
+}
+
 // A product with an FP8 matrix: its arguments but for pointers, and how it will run.
 uw_status check_fp8(int64_t n, int64_t k, int64_t batch, uw_activation act, Fp8Plan& p) {
   if (batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_FP8)) return UW_ERR_INVALID;
@@ -207,16 +224,11 @@ uw_status uw_dequantize_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, i
 }
 
 uw_status uw_workspace_size_mx4(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes) {
-  if (!bytes || batch < 0 || (act != UW_ACT_BF16 && act != UW_ACT_MX4)) return UW_ERR_INVALID;
-  const uw_status st = check_shape(n, k);
-  if (st != UW_OK) return st;
-  // (refused here rather than at a launch, so that nothing has run yet; tiles are 64 rows of 256 at least)
-  if (batch > INT32_MAX || !grid_fits((batch + 63) / 64 * ((n + 255) / 256), 512)) return UW_ERR_UNSUPPORTED;
-  const uint64_t b = (uint64_t)batch;
-  *bytes = act != UW_ACT_MX4     ? 0
-           : batch <= kMx4RowsMax ? pad256(2 * b * (uint64_t)k)
-                                  : pad256(b * (uint64_t)(k / 2)) + pad256(b * (uint64_t)mx4_scale_stride(k));
-  return UW_OK;
+  if (!bytes) return UW_ERR_INVALID;
+  const uw_status st = check_mx4(n, k, batch, act);
+  // (x takes 16 bits an element up to kMx4RowsMax rows, so that many rows need more than a few rows beyond)
+  if (st == UW_OK) *bytes = std::max(mx4_bytes(k, batch, act), mx4_bytes(k, std::min(batch, kMx4RowsMax), act));
+  return st;
 }
 
 uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64_t n, int64_t k,
@@ -224,9 +236,9 @@ uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64
                         size_t ws_bytes, void* stream) {
   if (batch == 0) return UW_OK;
   if (!elem_dev || !scale_dev || !x_dev || !y_dev) return UW_ERR_INVALID;
-  size_t need = 0;
-  uw_status st = uw_workspace_size_mx4(n, k, batch, act, &need);
+  uw_status st = check_mx4(n, k, batch, act);
   if (st != UW_OK) return st;
+  const uint64_t need = mx4_bytes(k, batch, act);
   if (!aligned(elem_dev, 16) || !aligned(scale_dev, 4) || !aligned(x_dev, 16) || !aligned(y_dev, 16) ||
       !aligned(ws_dev, 16))
     return UW_ERR_INVALID;

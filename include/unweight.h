@@ -531,7 +531,7 @@ uw_status uw_dequantize_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, i
  * uw_quantize_mx4 never writes) counts as infinite with UW_ACT_BF16, and with
  * UW_ACT_MX4 up to 8 rows; beyond, UW_ACT_MX4 multiplies it as it is.  x_dev is [batch][k] BF16, y_dev [batch][n] (overwritten), both
  * 16-byte aligned.  The workspace (uw_workspace_size_mx4 bytes, 16-byte
- * aligned) serves one call at a time. */
+ * aligned) serves one call at a time; the size never falls with more rows. */
 typedef enum { UW_ACT_BF16 = 0, UW_ACT_MX4 = 1, UW_ACT_FP8 = 2 /* uw_matmul_fp8 */ } uw_activation;
 uw_status uw_workspace_size_mx4(int64_t n, int64_t k, int64_t batch, uw_activation act, size_t* bytes);
 uw_status uw_matmul_mx4(const uint8_t* elem_dev, const uint8_t* scale_dev, int64_t n, int64_t k,

@@ -37,3 +37,11 @@ def test_fp8_size_is_bounded(uw, act):
         for b in (200, 1024, 20000):
             x = (2 * k + 4 * (-(-k // 128))) * b + 512 if act == "fp8" else 0
             assert uw.uw_workspace_size_fp8(n, k, b, a) <= x + (128 << 20)
+
+
+def test_mx4_size_never_falls_with_more_rows(uw):
+    rng = random.Random(8)
+    for n, k in SHAPES:
+        for a in (uw.ACT_BF16, uw.ACT_MX4):
+            sizes = [uw.uw_workspace_size_mx4(n, k, b, a) for b in batches(rng)]
+            assert sizes == sorted(sizes), (n, k)
