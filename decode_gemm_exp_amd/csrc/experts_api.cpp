@@ -154,6 +154,11 @@ uw_status check_route(int64_t tokens, int32_t experts, int32_t topk) {
   return UW_OK;
 }
 
+// The workspace that routing by this many blocks takes.
+uint64_t route_bytes(int64_t blocks, int32_t experts) {
+  return blocks > 1 ? pad256(4 * (uint64_t)blocks * (uint64_t)experts) : 0;
+}
+
 // A router's arguments, checked and as the kernels take them.
 uw_status set_route(RouteCall& c, const void* logits_dev, uw_type type, int64_t tokens, int32_t experts, int64_t ld,
                     const float* bias_dev, int32_t topk, uw_scoring scoring, int32_t* ids_dev, float* weights_dev,
@@ -183,9 +188,9 @@ uw_status set_route(RouteCall& c, const void* logits_dev, uw_type type, int64_t 
 uw_status run_route(RouteCall& c, void* ws, size_t ws_bytes, hipStream_t s) {
   // without tokens only the offsets are written
   if (!c.offsets || (c.tokens != 0 && (!c.rows || !c.slots))) return UW_ERR_INVALID;
-  size_t need = 0;
-  const uw_status st = uw_workspace_size_route(c.tokens, c.experts, c.topk, &need);
+  const uw_status st = check_route(c.tokens, c.experts, c.topk);
   if (st != UW_OK) return st;
+  const uint64_t need = route_bytes(route_blocks(c.tokens, c.topk), c.experts);
   if (need && (!ws || ws_bytes < need)) return UW_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return UW_ERR_INVALID;
   c.hist = static_cast<int32_t*>(ws);
@@ -476,8 +481,9 @@ uw_status uw_workspace_size_route(int64_t tokens, int32_t experts, int32_t topk,
   if (!bytes) return UW_ERR_INVALID;
   const uw_status st = check_route(tokens, experts, topk);
   if (st != UW_OK) return st;
+  // (the blocks of fewer tokens may be a few more, up to 256 of 64 tokens)
   const int b = route_blocks(tokens, topk);
-  *bytes = b > 1 ? pad256(4 * (uint64_t)b * (uint64_t)experts) : 0;
+  *bytes = route_bytes(b > 1 ? std::max<int64_t>(b, std::min<int64_t>((tokens + 63) / 64, 256)) : b, experts);
   return UW_OK;
 }
 

@@ -607,7 +607,7 @@ uw_status uw_matmul_fp8(const uint8_t* elem_dev, const float* scale_dev, int64_t
  * ids_dev and weights_dev are [tokens][topk].  experts <= 1024 and topk <= 16
  * (UW_ERR_UNSUPPORTED), topk <= experts.  Results repeat bit for bit.  The
  * workspace (uw_workspace_size_route bytes, may be 0) serves one call at a
- * time. */
+ * time; the size never falls with more tokens. */
 typedef enum {
   UW_SCORE_SOFTMAX = 0,
   UW_SCORE_SOFTMAX_TOPK = 1,

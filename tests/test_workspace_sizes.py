@@ -1,4 +1,5 @@
-"""Workspace sizes of products with inner conversions or slices, on the host alone."""
+"""Workspace sizes as batches grow, on the host alone."""
+import ctypes
 import random
 
 import pytest
@@ -45,3 +46,33 @@ def test_mx4_size_never_falls_with_more_rows(uw):
         for a in (uw.ACT_BF16, uw.ACT_MX4):
             sizes = [uw.uw_workspace_size_mx4(n, k, b, a) for b in batches(rng)]
             assert sizes == sorted(sizes), (n, k)
+
+
+def test_router_and_layer_sizes_never_fall_with_more_tokens(uw):
+    """16385 tokens make fewer, larger blocks than 16384."""
+    tokens = list(range(0, 1200, 7)) + list(range(16300, 17000)) + [32768, 32769, 33000, 65536, 65537]
+    n = ctypes.c_size_t()
+    sets = []
+    for n_, k in ((32, 32), (1408, 2048)):
+        for shape in ((n_, k), (k, n_)):
+            h = ctypes.c_void_p()
+            assert uw._lib.uw_experts_bf16(4096, 1024, *shape, 0, ctypes.byref(h)) == 0
+            sets.append(h)
+
+    def sizes(f, *args):
+        out = []
+        for t in tokens:
+            assert f(*args[0], t, *args[1], ctypes.byref(n)) == 0
+            out.append(n.value)
+        return out
+
+    for topk in (1, 3, 16):
+        for experts in [e for e in (1, 60, 1024) if e >= topk]:
+            got = sizes(uw._lib.uw_workspace_size_route, (), (experts, topk))
+            assert got == sorted(got)
+        for i in (0, 2):
+            for f in (uw._lib.uw_workspace_size_expert_mlp, uw._lib.uw_workspace_size_expert_layer):
+                got = sizes(f, (sets[i], sets[i + 1]), (topk,))
+                assert got == sorted(got)
+    for h in sets:
+        uw._lib.uw_free_experts(h)
