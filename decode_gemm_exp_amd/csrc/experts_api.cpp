@@ -600,6 +600,10 @@ uw_status uw_expert_layer(const uw_experts* gate, const uw_experts* up, const uw
   if (!offsets_dev || !rows_dev || !slots_dev || !x_dev || !out_dev) return UW_ERR_INVALID;
   if (need && (!ws_dev || ws_bytes < need)) return UW_ERR_WORKSPACE;
   if (!aligned(ws_dev, 16) || !aligned(x_dev, 16) || !aligned(out_dev, 16)) return UW_ERR_INVALID;
+  if (!aligned(logits_dev, type == UW_TYPE_BF16 ? 2 : 4)) return UW_ERR_INVALID;
+  for (const void* p : {(const void*)bias_dev, (const void*)ids_dev, (const void*)weights_dev, (const void*)offsets_dev,
+                        (const void*)rows_dev, (const void*)slots_dev})
+    if (!aligned(p, 4)) return UW_ERR_INVALID;
   for (const uw_experts* e : {gate, up, down})
     if (st == UW_OK) st = check_set(e);
   ExpertsCall c{};
