@@ -345,6 +345,7 @@ struct ExpertsCall {
   RaggedRows r;
   const uint16_t* x;
   void* y;
+  bool check;   // refuse what a launch would, launch nothing
 };
 hipError_t launch_experts(const ExpertsCall& c, hipStream_t s);
 hipError_t launch_experts_rows(const ExpertsCall& c, hipStream_t s);

@@ -96,8 +96,10 @@ uw_status set_weights(const uw_experts* w, const uw_experts* u, ExpertsCall& c) 
   return UW_OK;
 }
 
-uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r, void* y, hipStream_t s) {
+uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r, void* y, hipStream_t s,
+                      bool check = false) {
   ExpertsCall c{};
+  c.check = check;
   const uw_status st = set_weights(w, u, c);
   if (st != UW_OK) return st;
   if (r.slots == 0) return UW_OK;
@@ -105,6 +107,19 @@ uw_status run_experts(const uw_experts* w, const uw_experts* u, const Ragged& r,
   c.x = r.x;
   c.y = y;
   return status_of(launch_experts(c, s));
+}
+
+// Both products of a layer, before anything of it is enqueued: the sets fit each other and the grids a
+// launch.  (The kernels' own choice is asked only where tiles of 16 by 16, which all are at least, could
+// be too many.)
+uw_status check_products(const uw_experts* gate, const uw_experts* up, const uw_experts* down, const Ragged& in,
+                         const Ragged& mid) {
+  ExpertsCall c{};
+  const uw_status st = set_weights(gate, up, c);
+  const int64_t wide = std::max(down->v.n, gate->v.n), tiles = max_chunks(in.slots, gate->v.count, 16, true) * (wide / 16 + 1);
+  if (st != UW_OK || grid_fits(tiles + 8, 512)) return st;
+  const uw_status first = run_experts(gate, up, in, nullptr, nullptr, true);
+  return first != UW_OK ? first : run_experts(down, nullptr, mid, nullptr, nullptr, true);
 }
 
 // Up to this many rows x's 4-bit values go through the register-fed kernel as
@@ -562,6 +577,7 @@ uw_status uw_expert_mlp(const uw_experts* gate, const uw_experts* up, const uw_e
   float* d = reinterpret_cast<float*>(static_cast<uint8_t*>(ws_dev) + pad256(2 * (uint64_t)pairs * (uint64_t)gate->v.n));
   const Ragged in{offsets_dev, rows_dev, pairs, x_dev, tokens}, mid{offsets_dev, nullptr, pairs, h, pairs};
   st = check_rows(in, out_dev);
+  if (st == UW_OK) st = check_products(gate, up, down, in, mid);
   if (st == UW_OK) st = check_set(gate);
   if (st == UW_OK) st = check_set(up);
   if (st == UW_OK) st = check_set(down);
@@ -604,10 +620,13 @@ uw_status uw_expert_layer(const uw_experts* gate, const uw_experts* up, const uw
   for (const void* p : {(const void*)bias_dev, (const void*)ids_dev, (const void*)weights_dev, (const void*)offsets_dev,
                         (const void*)rows_dev, (const void*)slots_dev})
     if (!aligned(p, 4)) return UW_ERR_INVALID;
+  const int64_t pairs = tokens * topk;
+  ExpertsCall c{};
+  st = tokens > kLayerTokens ? check_products(gate, up, down, {offsets_dev, rows_dev, pairs, x_dev, tokens},
+                                              {offsets_dev, nullptr, pairs, nullptr, pairs})
+                             : set_weights(gate, up, c);   // (its grids always fit)
   for (const uw_experts* e : {gate, up, down})
     if (st == UW_OK) st = check_set(e);
-  ExpertsCall c{};
-  if (st == UW_OK) st = set_weights(gate, up, c);
   if (st != UW_OK) return st;
   if (tokens > kLayerTokens) {
     size_t mlp = 0;
@@ -616,7 +635,7 @@ uw_status uw_expert_layer(const uw_experts* gate, const uw_experts* up, const uw
     return st != UW_OK ? st : uw_expert_mlp(gate, up, down, tokens, topk, offsets_dev, rows_dev, slots_dev, weights_dev,
                                             x_dev, out_dev, ws_dev, mlp, stream);
   }
-  c.r = RaggedRows{nullptr, nullptr, tokens * topk, tokens};
+  c.r = RaggedRows{nullptr, nullptr, pairs, tokens};
   c.x = x_dev;
   c.y = ws_dev;
   st = status_of(launch_layer_gated(c, r, s));

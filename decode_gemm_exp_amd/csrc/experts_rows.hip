@@ -311,6 +311,7 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   const int64_t chunks = max_chunks(c.r.slots, c.w.count, 16 * Q, c.r.offsets != nullptr);
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (!grid_fits(grid, 256)) return hipErrorNotSupported;
+  if (c.check) return hipSuccess;
   if constexpr (FORM == kFormMx4) {
     auto k = k_experts_mx4<Q, GATED, false, 4, RaggedRows>;
     int waves = 4;

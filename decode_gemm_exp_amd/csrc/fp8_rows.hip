@@ -241,6 +241,7 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
   }
   const int64_t grid = (chunks * ntiles + 7) / 8 * 8;
   if (!grid_fits(grid, 64 * NW)) return hipErrorNotSupported;
+  if (c.check) return hipSuccess;
   hipLaunchKernelGGL((k_experts_fp8<R, Q, GATED, ACT8, XL, NW, RaggedRows>), dim3((unsigned)grid), dim3(64 * NW), 0, s,
                      c.w, c.u, c.r, c.x, c.y, (int)ntiles, (int)chunks, (int)rows);
   return hipGetLastError();

@@ -453,6 +453,7 @@ hipError_t launch_one(const ExpertsCall& c, const Fp8Tile& t, hipStream_t s) {
   // a multiple of 8 blocks: every XCD's eighth of the list, rounded up, has its blocks
   const int64_t grid = (tiles - t.tail + 7) / 8 * 8 + (int64_t)t.tail * t.splits;
   if (!grid_fits(grid, kNT)) return hipErrorNotSupported;
+  if (c.check) return hipSuccess;
   const TileArgs a{t.act, (int)ntiles, (int)t.spread, (int)(tiles - t.tail), t.tail, t.splits, t.part};
   hipLaunchKernelGGL((k_fp8_tile<BM, GATED, ACT8, BIG>), dim3((unsigned)grid), dim3(kNT), 0, s, c.w, c.u, c.r, c.x, a, c.y);
   const hipError_t e = hipGetLastError();
