@@ -250,16 +250,21 @@ hipError_t launch_one(const ExpertsCall& c, hipStream_t s) {
 // few blocks, or 16 where those fit the chip at once (32 / 16 a wave, us, 13 rows of x:
 // 1000x16384 12.6 / 9.8, 4096x4096 6.5 / 5.7, 5001x8224, 313 blocks of 16, 17.3 / 21.7); x
 // through LDS, like the weights, once its loads are many, or two groups of sixteen rows
-// where the blocks still fill the chip.  Measured (us; 64 rows, 64 with x in LDS, 32 with
+// where the blocks still make three quarters of the chip.  Measured (us; 64 rows, 64 with x in LDS, 32 with
 // eight waves, the same with x in LDS, two groups; x in BF16):
 //   14336x4096   1 row 14.4 / 15.6 / 14.2 / 15.8, 16 rows 15.3 / 16.0 / 17.5 / 17.5, 32 rows 21.5 / 22.2 / 26.8 / 26.7 / 19.2
 //   5001x8224    1 row 21.7 / 24.1 / 15.0 / 15.6, 16 rows 28.2 / 25.4 / 18.9 / 17.9, 32 rows 26.6 / 24.1 / 29.5 / 27.3 / 39.8
 //   4096x4096    1 row  7.9 /  8.6 /  5.8 /  6.1, 16 rows  9.2 /  8.9 /  8.2 /  6.7, 32 rows  9.3 /  8.7 /  8.4 /  7.0 / 13.0
 //   28672x8192  16 rows 47.8 / 47.2 / 55.5 / 52.9, in 8 bits 51.3 / 45.9 / 67.1 / 57.3
+// Two groups with 192 to 255 blocks, us, one group with x in LDS / two, weights out of every cache:
+//   12288x4096  17 rows 20.8 / 15.1, 32 rows 21.4 / 18.5, in 8 bits 21.9 / 18.7, 22.0 / 19.2
+//   14336x4096  17 rows 21.5 / 15.9, 32 rows 22.0 / 19.2, in 8 bits 22.4 / 19.2, 22.3 / 19.9
+//   6144x4096   64 rows 18.4 / 15.5, in 8 bits 21.4 / 17.1;  16049x12224, 24 rows in 8 bits 57.9 / 50.0
+// Sixteen rows, x past LDS / through it: 28672x2048 15.5 / 16.7, 28672x4096 29.1 / 29.0, 28672x8192 52.2 / 48.7.
 template <bool ACT8>
 hipError_t launch_matrix(const ExpertsCall& c, hipStream_t s) {
   const int64_t cus = device_cus(), rows = c.r.slots, tiles = (c.w.n + 63) / 64;
-  if (rows > 16 && tiles * ((rows + 31) / 32) >= cus) return launch_one<4, 2, false, ACT8, false, 4>(c, s);
+  if (rows > 16 && tiles * ((rows + 31) / 32) >= cus * 3 / 4) return launch_one<4, 2, false, ACT8, false, 4>(c, s);
   const int64_t blocks = tiles * ((rows + 15) / 16);
   if (blocks >= cus * 3 / 4)
     return rows > (ACT8 ? 8 : 15) ? launch_one<4, 1, false, ACT8, true, 4>(c, s)
@@ -348,7 +353,10 @@ hipError_t launch_fp8_experts(const ExpertsCall& c, hipStream_t s) {
 // faster: it costs 6.5 and the slices' sums at 5.3 TB/s.  The weights pass the tiles at
 // 2.5 TB/s at most; the rows kernel takes them once per 16 rows of x at 7 TB/s, or per 32 at
 // 6.2 where that fills the chip.  (us without / with slices: 5001x8224, 200 rows 55 / 40;
-// 4096x14336, 333 rows 173 / 56.)  Slices hold 512 rows of 256 sums a CU at most, which no
+// 4096x14336, 333 rows 173 / 56.)  Two groups on three quarters of the chip, which launch_matrix
+// takes, are not counted at 6.2 here: that would send long rows of few tiles there (us as it is /
+// so: 6328x8160, 64 rows 29.1 / 34.4; 3037x10176, 119 rows 26.4 / 33.4; 2018x5600, 200 rows
+// 22.6 / 16.1).  Slices hold 512 rows of 256 sums a CU at most, which no
 // plan of a million shapes tried wanted to pass (1 to 60000 x 32 to 32768, 17 to 20000 rows).
 Fp8Plan plan_fp8(int64_t n, int64_t k, int64_t batch, bool act8) {
   auto pad = [](uint64_t b) { return (b + 255) / 256 * 256; };

@@ -74,3 +74,12 @@ def test_workspace_of_the_largest_batch_serves_the_smaller(uw, n, k, batches, ac
         uw.uw_matmul_fp8(elem, scale, x, y, ws[:-256], a)
         assert torch.equal(y, want), batch
     assert bool((ws[-256:] == 0xA5).all())
+
+
+# 192 to 255 blocks of 64 rows of the matrix and two groups of sixteen rows of x: the last block and the last group cut off.
+@pytest.mark.parametrize("batch,n,k", [(17, 12288, 160), (32, 12229, 1056), (25, 16331, 96), (31, 14337, 2080),
+                                       (33, 6145, 288), (64, 7001, 416), (50, 8129, 544), (96, 4100, 224)])
+@pytest.mark.parametrize("act", ["bf16", "fp8"])
+def test_two_groups_of_rows(uw, batch, n, k, act):
+    ws = check(uw, batch, n, k, act)
+    assert bool((ws == 0xA5).all())   # the rows kernel uses none
