@@ -83,3 +83,32 @@ def test_workspace_of_the_largest_batch_serves_the_smaller(uw, n, k, batches, ac
 def test_two_groups_of_rows(uw, batch, n, k, act):
     ws = check(uw, batch, n, k, act)
     assert bool((ws == 0xA5).all())   # the rows kernel uses none
+
+
+def check_slices(uw, ws, batch, n, k, act, rows, count):
+    """`count` slices of tiles of `rows` rows by 256 sums, from the workspace's bytes after x's share, and nothing
+    else, were written (each tile's rows up to the batch's last)."""
+    at = 0
+    if act == "fp8":
+        at = sum(-(-b // 256) * 256 for b in (2 * batch * k, 4 * batch * (-(-k // 128))))
+        assert bool((ws[:at].view(-1, 256) != 0xA5).any(1).all())
+    part = ws[at:]
+    wrote = (part[:len(part) // 1024 * 1024].view(-1, 1024) != 0xA5).any(1)
+    assert bool(wrote[0:count * rows:rows].all()) and not bool(wrote[count * rows:].any()), "other slices than expected"
+
+
+# Up to 96 rows blocks start along K at different places, each inside its own slice: 64-row and 128-row tiles, all of
+# them in slices or the last round's alone, or none; then more rows, as in tests/test_gpu_fp8_edges.py.  The last two
+# numbers: rows of a tile, tiles in slices times slices, on 256 CUs.
+TILES = [(57, 4096, 8192, 64, 16 * 13), (33, 4096, 16384, 64, 16 * 13), (65, 4096, 8224, 64, 32 * 8),
+         (96, 5001, 8224, 64, 40 * 6), (72, 33838, 5056, 64, 10 * 7), (79, 5931, 18400, 128, 24 * 10),
+         (76, 8101, 14144, 128, 32 * 8), (45, 49228, 416, 64, 0), (68, 22654, 2560, 64, 0), (66, 33000, 1024, 128, 0),
+         (80, 43410, 1184, 128, 0), (333, 4096, 14336, 128, 48 * 5), (200, 5001, 8224, 128, 40 * 6),
+         (2100, 4100, 4096, 128, 33 * 4), (1500, 6400, 2080, 128, 44 * 3), (1100, 300, 9600, 64, 36 * 7),
+         (300, 300, 20000, 64, 10 * 16), (640, 14337, 1056, 128, 0)]
+
+
+@pytest.mark.parametrize("batch,n,k,rows,slices", TILES)
+@pytest.mark.parametrize("act", ["bf16", "fp8"])
+def test_tiles_and_slices(uw, batch, n, k, rows, slices, act):
+    check_slices(uw, check(uw, batch, n, k, act), batch, n, k, act, rows, slices)
