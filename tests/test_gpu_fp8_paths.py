@@ -112,3 +112,48 @@ TILES = [(57, 4096, 8192, 64, 16 * 13), (33, 4096, 16384, 64, 16 * 13), (65, 409
 @pytest.mark.parametrize("act", ["bf16", "fp8"])
 def test_tiles_and_slices(uw, batch, n, k, rows, slices, act):
     check_slices(uw, check(uw, batch, n, k, act), batch, n, k, act, rows, slices)
+
+
+@pytest.mark.parametrize("per,n", [(3, 33), (3, 5000), (20, 4160), (140, 33), (400, 33), (400, 2600)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_plans_that_descend_or_leave_the_rows(uw, per, n, gated):
+    """Offsets count as clamped to the slots and to those before them, row indices outside x as rows of zeros;
+    slots that no expert has, and what lies behind the last, keep what they held."""
+    g = torch.Generator().manual_seed(per + n)
+    e, k = 4, 160
+    slots = e * per
+    w = whole_numbers(g, 2, e, n, k)
+    scale = torch.ones(e, *uw.fp8_scale_shape(n, k, 128), device=DEV)
+    gate, up = (uw.uw_experts_fp8(v.to(torch.float8_e4m3fn), scale, e, n, k) for v in w)
+    x = whole_numbers(g, 6, k)
+    rows = torch.randint(0, 6, (slots,), generator=g, dtype=torch.int32)
+    rows[1], rows[per + 1], rows[-1] = -1, 6, -(1 << 31)
+    xs = x[rows.clamp(0, 5).long()] * ((rows >= 0) & (rows < 6)).to(DEV)[:, None]
+    for off in ([per * i for i in range(e + 1)], [0, 3 * per, 2, 1, 3], [-9, per, 1 << 30, 2, slots],
+                [-(1 << 31), (1 << 31) - 1, 0, 0, 0], [2, 1, per, per, slots - 1], [slots + 5] * 5, [0] * 5):
+        at, bounds = 0, []
+        for o in off:
+            at = max(at, min(max(o, 0), slots))
+            bounds.append(at)
+        want = torch.full((slots + 3, n), 7.0, device=DEV)
+        for i in range(e):
+            s = slice(bounds[i], bounds[i + 1])
+            a = xs[s] @ w[0][i].T
+            if gated:   # (whole numbers: the sums are exact; silu, the product and BF16's rounding are not)
+                b = xs[s] @ w[1][i].T
+                a = (a.double() * torch.sigmoid(a.double()) * b.double()).float()
+            want[s] = a
+        got = torch.full((slots + 3, n), 7.0, device=DEV, dtype=torch.bfloat16 if gated else torch.float32)
+        dev = torch.tensor(off, dtype=torch.int32, device=DEV), rows.to(DEV), x.bfloat16()
+        if gated:
+            uw.uw_matmul_experts_gated(gate, up, *dev, got[:slots])
+            # the exponential of up to 150 and what follows it 2^-17 (tests/test_gpu_experts_edges.py, gates over the
+            # whole range), BF16 2^-8, and one more FP32 step of `want`; 1e-38 covers subnormals
+            near = (got.float() - want).abs() <= (2.0 ** -8 + 2.0 ** -17 + 2.0 ** -23) * want.abs() + 1e-38
+            assert bool(near.all()), off
+            kept = torch.ones(slots + 3, dtype=torch.bool, device=DEV)
+            kept[bounds[0]:bounds[-1]] = False
+            assert bool((got[kept] == 7.0).all()), off
+        else:
+            uw.uw_matmul_experts(gate, *dev, got[:slots])
+            assert torch.equal(got, want), off
