@@ -9,7 +9,7 @@ namespace uw {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 16;
-// Tokens of a layer that goes in two kernels; a block of 256 threads holds all their pairs.
+// Tokens of a layer that goes in two kernels; a block of 256 threads or more holds all their pairs.
 constexpr int kLayerTokens = UW_LAYER_TOKENS, kLayerPairs = kLayerTokens * kMaxTopk;
 
 // Weight forms of the expert products, a template argument of the kernels.
@@ -379,7 +379,7 @@ int route_blocks(int64_t tokens, int topk);   // 1: no workspace
 hipError_t launch_route(const RouteCall& c, hipStream_t s);
 
 // A layer for at most kLayerTokens tokens (route.h): the choice, the plan and the gated
-// product h [tokens * topk][n] by slot (c.r counts for nothing but x_rows), then the down product with the weighted sum.
+// product h [tokens * topk][n] by slot (c.r is not used), then the down product with the weighted sum.
 hipError_t launch_layer_gated(const ExpertsCall& c, const RouteCall& r, hipStream_t s);
 hipError_t launch_layer_gated_fp8(const ExpertsCall& c, const RouteCall& r, hipStream_t s);
 hipError_t launch_layer_down(const ExpertsView& d, const RouteCall& r, const uint16_t* h, uint16_t* out, hipStream_t s);

@@ -635,7 +635,6 @@ uw_status uw_expert_layer(const uw_experts* gate, const uw_experts* up, const uw
     return st != UW_OK ? st : uw_expert_mlp(gate, up, down, tokens, topk, offsets_dev, rows_dev, slots_dev, weights_dev,
                                             x_dev, out_dev, ws_dev, mlp, stream);
   }
-  c.r = RaggedRows{nullptr, nullptr, pairs, tokens};
   c.x = x_dev;
   c.y = ws_dev;
   st = status_of(launch_layer_gated(c, r, s));
