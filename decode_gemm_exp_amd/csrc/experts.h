@@ -9,7 +9,16 @@ namespace uw {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 16;
-// Tokens of a layer that goes in two kernels; a block of 256 threads or more holds all their pairs.
+// Tokens of a layer that goes in two kernels; a block of 256 threads or more holds all their pairs, and
+// sixteen are the columns of an MFMA.  us, two kernels / router, both products and the weighted sum, 1, 8 and 16 tokens:
+//   FP8, 8 of 64 experts 1408x2048    18.8 / 27.8    65 / 86      99 / 110
+//   MXFP4, 6 of 160 1408x2048         16.4 / 23.2    51 / 61      84 / 96
+//   BF16, 8 of 64 1408x2048           29.1 / 38.2   125 / 147    183 / 193
+//   BF16, 2 of 16 512x1024            11.1 / 17.3    17 / 22      20 / 26
+//   UWF1, 4 of 32 2048x4096           34.7 / 39.4   175 / 175    234 / 235
+//   BF16, 2 of 8 14336x4096            124 / 130    496 / 493    507 / 500
+//   FP8, 2 of 8 14336x4096              67 / 78     228 / 223    265 / 254
+// Few large experts, which all have tokens by eight, lose up to 4 % to what they win elsewhere.
 constexpr int kLayerTokens = UW_LAYER_TOKENS, kLayerPairs = kLayerTokens * kMaxTopk;
 
 // Weight forms of the expert products, a template argument of the kernels.

@@ -9,8 +9,9 @@
 // to the running FP32 sum.
 //
 // A stream over the weights, built as the MXFP4 kernel of experts_rows.hip: a wave
-// owns 64 rows and walks every NWth window of 128 k, one block of scales, which it
-// sends to a ring of its own in LDS, 64 rows of 128 bytes, piece p of row r at 16
+// owns 16 R rows (64 as a rule, 16 or 32 of narrow matrices, 20 to 44 where even shares
+// fill the chip better) and walks every NWth window of 128 k, one block of scales, which it
+// sends to a ring of its own in LDS, 16 R rows of 128 bytes, piece p of row r at 16
 // (p ^ (r / 2 % 8)); the waves' sums meet in LDS and are added in a fixed order.
 // ACT8: a lane's 32 values of x become elements by the maximum over the four lanes
 // that hold a block, which the wait for the weights hides.

@@ -3,6 +3,9 @@
 //   out[t] = BF16( sum over e  w[t][e]  h[slot(t, e)] . D_e^T )
 // over the experts e of token t, D_e [n][k] in any form.
 //
+// h is BF16, as uw_matmul_experts_gated gives it: the matrix unit takes it so, and FP32 sums follow
+// (out is off by 0.0023 to 0.0024 of its norm, 0.0017 of which is its own rounding to BF16).
+//
 // A stream over the rows of D of every expert that has tokens.  A block owns 16 / P
 // output features and walks all those experts, so the weighted sum ends in one
 // block and needs neither partial sums in memory nor a third launch.  An item is an
